@@ -10,6 +10,7 @@ module raises: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -52,6 +53,19 @@ class ScanGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "dy", "dh_final", "dx", "dBraw", "dCraw", "ddt", "dA", "dlam", "dtheta", "dB_bias", "dC_bias",
         "dB_normw", "dC_normw", "dh0", "dx_prev", "dBraw_prev")]
+
+
+class LinattnIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "log_decay", "h0", "lengths", "y", "h_final")] + [
+        ("scale", ctypes.c_float)]
+
+
+class LinattnGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "dh_final", "dq", "dk", "dv", "dlog_decay", "dh0")]
+
+
+class LinattnStepIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "log_decay", "h", "y")] + [("scale", ctypes.c_float)]
 
 
 class Plan(ctypes.Structure):
@@ -104,6 +118,18 @@ def _load():
                                        ctypes.c_void_p]
     lib.m3_probe_device_facts.restype = ctypes.c_int
     lib.m3_probe_device_facts.argtypes = [ctypes.c_int, ctypes.POINTER(DeviceFacts)]
+    lib.m3_linattn_fwd.restype = ctypes.c_int
+    lib.m3_linattn_fwd.argtypes = [ctypes.POINTER(Shape), ctypes.POINTER(LinattnIO), ctypes.c_void_p,
+                                   ctypes.c_size_t, ctypes.c_void_p]
+    lib.m3_linattn_workspace_bytes.restype = ctypes.c_size_t
+    lib.m3_linattn_workspace_bytes.argtypes = [ctypes.POINTER(Shape)]
+    lib.m3_linattn_bwd.restype = ctypes.c_int
+    lib.m3_linattn_bwd.argtypes = [ctypes.POINTER(Shape), ctypes.POINTER(LinattnIO), ctypes.POINTER(LinattnGrads),
+                                   ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.m3_linattn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.m3_linattn_bwd_workspace_bytes.argtypes = [ctypes.POINTER(Shape)]
+    lib.m3_linattn_step.restype = ctypes.c_int
+    lib.m3_linattn_step.argtypes = [ctypes.POINTER(Shape), ctypes.POINTER(LinattnStepIO), ctypes.c_void_p]
     return lib
 
 
@@ -526,6 +552,151 @@ def gate_contract(y, z_in, W_Z, W_O, o=None, stream=None):
     _check(lib.m3_gate_contract(ctypes.byref(shape), _ptr(y), _ptr(z_in), _ptr(W_Z), _ptr(W_O), _ptr(o),
                                 _stream(stream)))
     return o
+
+
+# ------------------------- linear attention with a decay for each head ---
+def _owned_by(stream):
+    """Context for allocating a call's outputs and workspace: memory of the stream that the
+    call runs on, so that what is freed after the call is not handed out before it ran."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) on the tensors' device, whichever device is current."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device_index != device.index:
+        raise ValueError("stream: on device %d, expected %d (the device of the inputs)" % (s.device_index, device.index))
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, ctypes.c_void_p(s.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, ctypes.c_void_p(s.cuda_stream))
+    _check(rc)
+
+
+def _linattn_dims(q, k, v, ndim):
+    """(lead, H, G, N, P) of q [*lead, H, N], k [*lead, G, N], v [*lead, G, P]."""
+    qs, _, vs = _dims5("q", q, ndim), _dims5("k", k, ndim), _dims5("v", v, ndim)
+    lead, H, N, G, P = qs[:-2], qs[-2], qs[-1], vs[-2], vs[-1]
+    _io_dtype(q)
+    return lead, H, G, N, P
+
+
+def _linattn_specs(q, k, v, log_decay, h0, lengths, lead, H, G, N, P):
+    io, f32 = q.dtype, torch.float32
+    return [("q", q, lead + (H, N), io), ("k", k, lead + (G, N), io), ("v", v, lead + (G, P), io),
+            ("log_decay", log_decay, (H,), f32), ("h0", h0, (lead[0], H, P, N), f32),
+            ("lengths", lengths, (lead[0],), torch.int32)]
+
+
+def linattn_shape(q, v, nsegments=0) -> Shape:
+    b, L, H, N = q.shape
+    return make_shape(b, L, H, v.shape[2], v.shape[3], N, 1, 1, _io_dtype(q), 0.0, 0, nsegments)
+
+
+def linattn_workspace_bytes(shape: Shape) -> int:
+    return int(lib.m3_linattn_workspace_bytes(ctypes.byref(shape)))
+
+
+def linattn_bwd_workspace_bytes(shape: Shape) -> int:
+    return int(lib.m3_linattn_bwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def linattn_fwd(q, k, v, log_decay, *, scale=None, h0=None, lengths=None, y=None, h_final=None, want_state=True,
+                workspace=None, nsegments=0, stream=None):
+    """Linear attention with a decay for each head over a prompt (m3_linattn_fwd):
+    y_t = scale * sum_{j<=t} e^{(t-j) log_decay} (q_t . k_j) v_j, plus the initial state's
+    term. q [b,L,H,N], k [b,L,G,N], v [b,L,G,P] (fp32 or bf16; head h reads k, v head
+    h // (H // G)), log_decay [H] fp32 <= 0, h0 [b,H,P,N] fp32, lengths [b] int32: row i has
+    lengths[i] tokens, y is 0 behind them and the state is the one after them. scale
+    defaults to N ** -0.5. Returns (y [b,L,H,P], h_final [b,H,P,N] fp32 or None)."""
+    lead, H, G, N, P = _linattn_dims(q, k, v, 4)
+    b, L = lead
+    _need("log_decay", log_decay)
+    _expect_all(_linattn_specs(q, k, v, log_decay, h0, lengths, lead, H, G, N, P)
+                + [("y", y, (b, L, H, P), q.dtype), ("h_final", h_final, (b, H, P, N), torch.float32),
+                   ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
+                q.get_device())
+    shape = linattn_shape(q, v, nsegments)
+    ws = linattn_workspace_bytes(shape)
+    with _owned_by(stream):
+        if y is None:
+            y = torch.empty((b, L, H, P), dtype=q.dtype, device=q.device)
+        if h_final is None and want_state:
+            h_final = torch.empty((b, H, P, N), dtype=torch.float32, device=q.device)
+        if ws and workspace is None:
+            workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
+    io = LinattnIO(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0), _ptr(lengths), _ptr(y), _ptr(h_final),
+                   float(N ** -0.5 if scale is None else scale))
+    wsb = 0 if workspace is None else workspace.numel()
+    _launch(lib.m3_linattn_fwd, q.device, stream, ctypes.byref(shape), ctypes.byref(io), _ptr(workspace), wsb)
+    return y, h_final
+
+
+def linattn_bwd(q, k, v, log_decay, dy, *, scale=None, h0=None, lengths=None, dh_final=None, want_dh0=True,
+                want_dlog_decay=True, workspace=None, grads=None, nsegments=0, stream=None):
+    """Gradients of <dy, y> + <dh_final, h_final> of linattn_fwd (m3_linattn_bwd). Returns a
+    dict: q, k, v in the dtype of the inputs (k and v summed over the heads that share
+    them), log_decay [H] and h0 [b,H,P,N] in fp32 where wanted. grads: such a dict to
+    write into; the entries q, k, v are required, the others are the ones wanted."""
+    lead, H, G, N, P = _linattn_dims(q, k, v, 4)
+    b, L = lead
+    _need("log_decay", log_decay)
+    _need("dy", dy)
+    f32 = torch.float32
+    _expect_all(_linattn_specs(q, k, v, log_decay, h0, lengths, lead, H, G, N, P)
+                + [("dy", dy, (b, L, H, P), q.dtype), ("dh_final", dh_final, (b, H, P, N), f32),
+                   ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
+                q.get_device())
+    shape = linattn_shape(q, v, nsegments)
+    dev = q.device
+    ws = linattn_bwd_workspace_bytes(shape)
+    with _owned_by(stream):
+        if grads is None:
+            grads = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v)}
+            if want_dlog_decay:
+                grads["log_decay"] = torch.empty((H,), dtype=f32, device=dev)
+            if want_dh0:
+                grads["h0"] = torch.empty((b, H, P, N), dtype=f32, device=dev)
+        if workspace is None and ws:
+            workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    want = {"q": (q.shape, q.dtype), "k": (k.shape, q.dtype), "v": (v.shape, q.dtype), "log_decay": ((H,), f32),
+            "h0": ((b, H, P, N), f32)}
+    for name, t in grads.items():
+        if name not in want:
+            raise ValueError("grads: unknown entry %r" % name)
+        _expect("grads[%r]" % name, t, tuple(want[name][0]), want[name][1], q.get_device())
+    for name in "qkv":
+        _need("grads[%r]" % name, grads.get(name))
+    io = LinattnIO(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0), _ptr(lengths), None, None,
+                   float(N ** -0.5 if scale is None else scale))
+    gs = LinattnGrads(_ptr(dy), _ptr(dh_final), _ptr(grads["q"]), _ptr(grads["k"]), _ptr(grads["v"]),
+                      _ptr(grads.get("log_decay")), _ptr(grads.get("h0")))
+    wsb = 0 if workspace is None else workspace.numel()
+    _launch(lib.m3_linattn_bwd, dev, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs), _ptr(workspace),
+            wsb)
+    return grads
+
+
+def linattn_step(q, k, v, log_decay, h, *, scale=None, y=None, stream=None):
+    """One token of linattn_fwd (m3_linattn_step): q [b,H,N], k [b,G,N], v [b,G,P], the state
+    h [b,H,P,N] (fp32 or bf16) updated in place. Returns y [b,H,P]."""
+    lead, H, G, N, P = _linattn_dims(q, k, v, 3)
+    b = lead[0]
+    _need("log_decay", log_decay)
+    _need("h", h)
+    _expect_all(_linattn_specs(q, k, v, log_decay, None, None, lead, H, G, N, P)
+                + [("h", h, (b, H, P, N), (torch.float32, torch.bfloat16)), ("y", y, (b, H, P), q.dtype)],
+                q.get_device())
+    shape = make_shape(b, 1, H, G, P, N, 1, 1, _io_dtype(q), 0.0,
+                       M3_FLAG_BF16_STATE if h.dtype == torch.bfloat16 else 0)
+    if y is None:
+        with _owned_by(stream):
+            y = torch.empty((b, H, P), dtype=q.dtype, device=q.device)
+    io = LinattnStepIO(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h), _ptr(y),
+                       float(N ** -0.5 if scale is None else scale))
+    _launch(lib.m3_linattn_step, q.device, stream, ctypes.byref(shape), ctypes.byref(io))
+    return y
 
 
 # ------------------------------------------------------ calibration probes ---
