@@ -8,8 +8,9 @@
 // is the forward (si = sr = scale, su = 1). Time reversed,
 //   out_j = sum_{i>=j} si a^{i-j} (q_j . k_i) v_i + sr a^{nt-1-j} D^T q_j
 //   D    <- a^{nt} D + sum_i su a^{i+1} k_i v_i^T
-// with D the gradient of the state behind the chunk (si = su = scale, sr = 1). The
-// gradients are three such passes over other tensors:
+// with D the gradient of the state behind the chunk (si = su = scale, sr = 1). With
+// the chunk's tokens taken last first the two differ in two exponents only
+// (i + 1 - rev and nt - 1 - j + rev), and both masks keep j <= i. The gradients are three such passes over other tensors:
 //   dq: forwards,  (q, k, v) = (dy, v, k), the state transposed
 //   dk: backwards, (q, k, v) = (v, dy, q), the state transposed
 //   dv: backwards, (q, k, v) = (k, q, dy)
@@ -35,6 +36,8 @@ namespace m3i {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
@@ -42,11 +45,11 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kVT = 64;  // value columns of a workgroup
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxDim = 256;
 constexpr int64_t kMaxGrid = 0x7fffffff;
 
-enum Mode { kOut = 0, kState = 1, kDecay = 2 };
+// kOut: outputs. kState, kStateU: segment states (and their derivatives) only. kDecay: d log_decay
+enum Mode { kOut = 0, kState = 1, kStateU = 2, kDecay = 3 };
 
 // one of a pass's three tensors: [b, L, heads, dim], read at head h / per
 struct Tensor {
@@ -92,35 +95,37 @@ struct Ops<uint16_t> {
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
-    // x as a sum of NP bf16 parts: each takes 8 of its bits, the remainders are exact
+    // Two values as a sum of NP bf16 pairs: each part takes 8 of a value's bits, the remainders are exact
+    template <int NP, typename F>
+    static __device__ __forceinline__ void split2(float x, float y, const F &put) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const f32x2 v = {x, y};
+            const unsigned w = __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2));
+            put(n, w);
+            if (n + 1 < NP) {
+                x -= __uint_as_float(w << 16);
+                y -= __uint_as_float(w & 0xffff0000u);
+            }
+        }
+    }
     template <int NP>
     static __device__ __forceinline__ void parts(const float *x, frag *p) {
-        float r[8];
+        u32x4 w[NP];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = x[e];
+        for (int e = 0; e < 4; ++e) split2<NP>(x[2 * e], x[2 * e + 1], [&](int n, unsigned u) { w[n][e] = u; });
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[n][e] = (__bf16)r[e];
-                if (n + 1 < NP) r[e] -= (float)p[n][e];
-            }
+        for (int n = 0; n < NP; ++n) p[n] = __builtin_bit_cast(frag, w[n]);
     }
     static __device__ __forceinline__ float value(frag f, int e) { return (float)f[e]; }
     // 4 values to 4 consecutive elements, in parts `plane` elements apart
     template <int NP>
     static __device__ __forceinline__ void store4(uint16_t *to, int plane, f32x4 x) {
+        u32x2 w[NP];
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            bf16x4 b;
+        for (int e = 0; e < 2; ++e) split2<NP>(x[2 * e], x[2 * e + 1], [&](int n, unsigned u) { w[n][e] = u; });
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                b[e] = (__bf16)x[e];
-                if (n + 1 < NP) x[e] -= (float)b[e];
-            }
-            *reinterpret_cast<bf16x4 *>(to + n * plane) = b;
-        }
+        for (int n = 0; n < NP; ++n) *reinterpret_cast<u32x2 *>(to + n * plane) = w[n];
     }
 };
 
@@ -146,39 +151,45 @@ struct Ops<float> {
     }
 };
 
-// 8 elements of a row, zero from column dim on, packed; VEC: dim is a multiple of 8 and rows are 16-byte aligned
-template <bool VEC>
-__device__ __forceinline__ u32x4 load8(const uint16_t *row, int col, int dim, bool live) {
-    u32x4 w = {0, 0, 0, 0};
-    if constexpr (VEC) {
-        if (live && col < dim) w = *reinterpret_cast<const u32x4 *>(row + col);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            unsigned lo = 0, hi = 0;
-            if (live && col + 2 * e < dim) lo = row[col + 2 * e];
-            if (live && col + 2 * e + 1 < dim) hi = row[col + 2 * e + 1];
-            w[e] = lo | (hi << 16);
-        }
-    }
-    return w;
-}
+// A chunk's valid rows of one tensor for one head are read by byte offsets from the first.
+// With dims in multiples of 8 (VEC) the reads are buffer loads, whose bounds check gives zeros for what
+// lies outside (rows before the first wrap around to offsets beyond 2^31; a chunk's rows
+// span less, as H <= 65536) without a branch.
+constexpr unsigned kOutside = 0x80000000u;
 
-template <bool VEC>
-__device__ __forceinline__ f32x8 load8(const float *row, int col, int dim, bool live) {
-    f32x8 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+// 8 elements, packed; `cols` of them exist
+template <typename E, bool VEC>
+__device__ __forceinline__ typename Ops<E>::pack load8(const char *p, unsigned bytes, unsigned at, int cols) {
     if constexpr (VEC) {
-        if (live && col < dim) {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(row + col);
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(row + col + 4);
-            x = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (int)bytes, 0x00020000);
+        if constexpr (sizeof(E) == 2) {
+            return __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+        } else {
+            const f32x4 a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
+            const f32x4 b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + 16, 0, 0));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     } else {
+        const int live = at < bytes ? cols : 0;
+        const E *x = reinterpret_cast<const E *>(p + (live > 0 ? at : 0u));
+        if constexpr (sizeof(E) == 2) {
+            u32x4 w = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (live && col + e < dim) x[e] = row[col + e];
+            for (int e = 0; e < 4; ++e) {
+                unsigned lo = 0, hi = 0;
+                if (2 * e < live) lo = x[2 * e];
+                if (2 * e + 1 < live) hi = x[2 * e + 1];
+                w[e] = lo | (hi << 16);
+            }
+            return w;
+        } else {
+            f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < live) v[e] = x[e];
+            return v;
+        }
     }
-    return x;
 }
 
 // elements 4 half .. + 3 of a packed row
@@ -198,81 +209,96 @@ __device__ __forceinline__ void put_column(float *to, const f32x8 (&x)[4], int e
     *reinterpret_cast<f32x4 *>(to) = f32x4{x[0][e], x[1][e], x[2][e], x[3][e]};
 }
 
+__device__ __forceinline__ u32x2 bf16_pack4(f32x4 x) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const bf16x4 b = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+    return __builtin_bit_cast(u32x2, b);
+}
+
 template <typename E>
 __device__ __forceinline__ typename Ops<E>::frag frag_at(const E *p) {
     return *reinterpret_cast<const typename Ops<E>::frag *>(p);
 }
 
-// LDS tiles, in blocks of 8 elements (one lane's operand slots).
-// Row tile [token][key]: keys permuted so that a block holds what the state's
-// accumulators hold of it: block 4s + g of a row is keys 32s + 4g + 0..3 and
-// 32s + 16 + 4g + 0..3. Blocks are exchanged by the row's low bits, so that the 16 rows
-// which a fragment read touches lie in different banks.
-template <int KD>
-__device__ __forceinline__ int row_at(int row, int block) {
-    return row * KD + ((block ^ (row & 7)) << 3);
+// LDS tiles, in blocks of 8 elements (one lane's operand slots), exchanged within a row so that
+// the 16 rows which a fragment read touches, and the rows that one store fills, lie
+// in different banks.
+// Row tile [token][KD keys]: block b of row i lies at b ^ (i & 7). Keys are permuted so that a block
+// holds what the state's accumulators hold of it: block 4s + g is keys 32s + 4g + 0..3 and
+// 32s + 16 + 4g + 0..3. A lane's fragment (row 16 t + lr, block 4 ks + lg) is at
+// row_base(ks & 1) + 64 (ks >> 1) + 16 KD t.
+template <int LD>
+__device__ __forceinline__ int row_base(int lr, int lg, int odd) {
+    return lr * LD + (((lg + 4 * odd) ^ (lr & (LD >= 64 ? 7 : 3))) << 3);
 }
-// Transposed tile [key or value][token]
+// Transposed tile [key or value][C tokens]: block b of column n lies at b ^ ((n ^ n >> 3) & 7). A lane's
+// fragment (column 16 t + lr, block 4 ks + lg) is at col_base(2 ks ^ (t & 3)) + 16 C t.
 template <int C>
-__device__ __forceinline__ int col_at(int col, int block) {
-    return col * C + ((block ^ ((col ^ (col >> 3)) & (C / 8 - 1))) << 3);
+__device__ __forceinline__ int col_base(int lr, int lg, int x) {
+    return lr * C + (((lg ^ (2 * x) ^ lr ^ (lr >> 3)) & (C / 8 - 1)) << 3);
 }
 
-// 8 consecutive keys from n0 (a multiple of 8) of one token into the row tile
-template <int KD, typename E>
-__device__ __forceinline__ void put_row(E *tile, int row, int n0, typename Ops<E>::pack x) {
-    const int block = 4 * (n0 >> 5) + ((n0 & 15) >> 2), half = (n0 >> 4) & 1;
-    put4(tile + row_at<KD>(row, block) + 4 * half, x, 0);
-    put4(tile + row_at<KD>(row, block + 1) + 4 * half, x, 1);
+// A value the compiler cannot see through: addresses formed from it are formed where they
+// are used, not kept in registers across the loop
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
-__device__ __forceinline__ float power(float g2, int n) {
-    return n == 0 ? 1.f : __builtin_amdgcn_exp2f(g2 * (float)n);  // a decay of 0 is 2^-inf, and 0 * inf no number
+// a^n to half a unit in the last place: a decay's rounding would otherwise add up over
+// the chunks of a long sequence. A decay of 0 is e^-inf, and 0 * inf no number.
+__device__ __forceinline__ double power(float log_decay, int64_t n) {
+    return n == 0 ? 1.0 : exp((double)log_decay * (double)n);
 }
 
 // A workgroup's place in the work: consecutive ones (the value tiles of a chain, the
 // heads of a group, which read the same tensors) go to one XCD and its L2
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
-    const int64_t q = total / 8, r = total % 8, x = id % 8;
+__device__ __forceinline__ unsigned xcd_order(unsigned id, unsigned total) {
+    const unsigned q = total / 8, r = total % 8, x = id % 8;
     return x * q + (x < r ? x : r) + id / 8;
+}
+
+// a value that is the same in all lanes, in a scalar register
+__device__ __forceinline__ float uniform(float x) {
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
 
 template <typename E, int KD, int MODE, bool VEC>
 __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void linattn_kernel(const Args a) {
     typedef Ops<E> O;
     typedef typename O::frag frag;
-    constexpr int C = O::C, KT = KD / 16, KS = KD / 32, JS = C / 32, IT = C / 16;
-    constexpr bool kDec = MODE == kDecay, kSt = MODE == kState;
+    constexpr int C = O::C, KT = KD / 16, KS = KD / 32, JS = C / 32, IT = C / 16, ES = sizeof(E);
+    constexpr bool kDec = MODE == kDecay, kSt = MODE == kState || MODE == kStateU, kU = kDec || MODE == kStateU;
     constexpr int NA = kDec ? O::NU : O::NA, NS = kDec ? O::NU : O::NS;
     __shared__ __align__(16) E Qs[kSt ? 8 : C * KD];
     __shared__ __align__(16) E Ks[kSt ? 8 : C * KD];
     __shared__ __align__(16) E Kc[KD * C];
     __shared__ __align__(16) E Vc[kVT * C];
     __shared__ __align__(16) E As[kSt ? 8 : NA * C * C];
-    __shared__ float wt[C], wu[kDec || kSt ? C : 1];
+    __shared__ __align__(16) float wt[C], wu[kU ? C : 1];
+    __shared__ float pw[C + 1];  // a^n
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, lr = lane & 15, lg = lane >> 4;
-    int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int vt = (int)(id % a.nvt);
-    id /= a.nvt;
-    const int64_t chains = a.b * a.H, chain = id % chains;
-    const int seg = (int)(id / chains);
-    const int64_t bi = chain / a.H;
-    const int h = (int)(chain % a.H);
+    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
+    const int vt = (int)(id % (unsigned)a.nvt);
+    const unsigned rest = id / (unsigned)a.nvt, chains = (unsigned)a.b * (unsigned)a.H;
+    const int64_t chain = rest % chains;
+    const int seg = (int)(rest / chains);
+    const int64_t bi = (unsigned)chain / (unsigned)a.H;
+    const int h = (int)((unsigned)chain % (unsigned)a.H), rv = a.rev ? 1 : 0;
     int64_t len = a.L;
     if (a.lengths) {
         const int64_t l = a.lengths[bi];
         len = l < 0 ? 0 : (l < a.L ? l : a.L);
     }
-    const float g2 = a.log_decay[h] * kLog2e;
+    const float ld = a.log_decay[h];
     const int64_t c_lo = seg * a.seg_chunks;
     const int64_t c_hi = c_lo + a.seg_chunks < a.nchunks ? c_lo + a.seg_chunks : a.nchunks;
     const int v0 = vt * kVT, col = v0 + 16 * wave + lr;  // this lane's value column
     const int64_t nstate = (int64_t)a.kd * a.vd;
-    const bool with_u = kDec || (kSt && a.u_out != nullptr);
 
-    // the state: rows n = 16 nt + 4 lg + r of column col
-    f32x4 S[KT], U[kDec || kSt ? KT : 1];
+    // the state: rows n = 16 t + 4 lg + r of column col
+    f32x4 S[KT], U[kU ? KT : 1];
     const auto load_state = [&](f32x4 *to, const float *from) {
         const float *p = from ? from + (a.seg_in ? chain * a.nseg + seg : chain) * nstate : nullptr;
 #pragma unroll
@@ -280,7 +306,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int n = 16 * t + 4 * lg + r;
-                to[t][r] = p && n < a.kd && col < a.vd ? p[(int64_t)n * a.sk + (int64_t)col * a.sv] : 0.f;
+                to[t][r] = p && n < a.kd && col < a.vd ? p[n * a.sk + col * a.sv] : 0.f;
             }
     };
     const auto store_state = [&](const f32x4 *from, float *to, int64_t at) {
@@ -290,161 +316,228 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int n = 16 * t + 4 * lg + r;
-                if (n < a.kd && col < a.vd) p[(int64_t)n * a.sk + (int64_t)col * a.sv] = from[t][r];
+                if (n < a.kd && col < a.vd) p[n * a.sk + col * a.sv] = from[t][r];
             }
     };
     load_state(S, kSt ? nullptr : a.s_in);
-    if constexpr (kDec || kSt) load_state(U, kSt ? nullptr : a.u_in);
+    if constexpr (kU) load_state(U, kSt ? nullptr : a.u_in);
 
-    // score tile of this wave: output tokens of strip `st`, JW tiles of the others from j0
-    constexpr int JW = IT * IT / 4;
-    const int st = wave % IT, j0 = (wave / IT) * JW;
-    float mask[kSt ? 1 : JW][4];
+    if (tid <= C) pw[tid] = (float)power(ld, tid);
+    __syncthreads();
+    // Score tiles of this wave, (rows, columns) in 16s: of the 4 x 4 the 10 with j <= i are needed, and (0, 1) and
+    // (2, 3) as zeros; three a wave, two of them in one row strip, so that no wave waits for another. fp32 has 2 x 2.
+    constexpr int JW = IT == 4 ? 3 : 1;
+    const int sa = IT == 4 ? (wave < 2 ? 3 : 4 - wave) : wave >> 1, sc_ = IT == 4 ? 2 * ((wave ^ (wave >> 1)) & 1) : sa;
+    const int ta = IT == 4 ? (wave == 1 ? 2 : 0) : wave & 1, tc = IT == 4 ? (wave == 0 ? 0 : 4 - wave) : ta;
+    const auto srow = [&](int t) { return t == 2 ? sc_ : sa; };
+    const auto scol = [&](int t) { return t == 2 ? tc : ta + t; };
+    float mask[kSt ? 1 : JW][4], rs[kSt ? 1 : IT];
     if constexpr (!kSt) {
 #pragma unroll
         for (int t = 0; t < JW; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * st + lr, j = 16 * (j0 + t) + 4 * lg + r, n = a.rev ? j - i : i - j;
-                mask[t][r] = n < 0 ? 0.f : a.si * power(g2, n) * (kDec ? (float)n : 1.f);
-                if (kDec && n == 0) mask[t][r] = 0.f;
+                const int n = 16 * srow(t) + lr - 16 * scol(t) - 4 * lg - r;
+                mask[t][r] = n < 0 ? 0.f : a.si * pw[n < 0 ? 0 : n] * (kDec ? (float)n : 1.f);
             }
+#pragma unroll
+        for (int it = 0; it < IT; ++it) rs[it] = a.sr * pw[16 * it + lr + 1 - rv];
     }
-    const int kh = h / a.k.per, vh = h / a.v.per, qh = kSt ? 0 : h / a.q.per;
-    const E *kb = static_cast<const E *>(a.k.p) + ((int64_t)bi * a.L * a.k.heads + kh) * a.kd;
-    const E *vb = static_cast<const E *>(a.v.p) + ((int64_t)bi * a.L * a.v.heads + vh) * a.vd;
-    const E *qb = kSt ? nullptr : static_cast<const E *>(a.q.p) + ((int64_t)bi * a.L * a.q.heads + qh) * a.kd;
-    const int64_t kst = (int64_t)a.k.heads * a.kd, vst = (int64_t)a.v.heads * a.vd,
-                  qst = kSt ? 0 : (int64_t)a.q.heads * a.kd;
-    double dsum = 0.0;
 
-    // staging units: k and v 4 tokens x 8 columns, q 1 token x 8 columns
+    // Staging units: k and v 4 tokens x 8 columns, q 1 token x 8 columns. Row i of a chunk is its
+    // token i, or nt - 1 - i backwards: at (rv ? nt - 1 - i : i) strides from the first.
     constexpr int KU = (C / 4) * (KD / 8), KN = (KU + kThreads - 1) / kThreads;
     constexpr int VU = (C / 4) * (kVT / 8);
     constexpr int QN = kSt ? 0 : C * (KD / 8) / kThreads;
     static_assert(VU <= kThreads && (kSt || C * (KD / 8) % kThreads == 0), "staging");
+    constexpr int KR = kThreads / (KD / 8);  // units of one pass over the rows
     typename O::pack kx[KN][4], vx[4], qx[QN ? QN : 1];
-
-    const auto fetch_k = [&](int64_t t0, int u) {
-        const int unit = tid + u * kThreads, n0 = 8 * (unit % (KD / 8)), j = 4 * (unit / (KD / 8));
+    const int kn = 8 * (tid % (KD / 8)), kj = 4 * (tid / (KD / 8)), qi = tid / (KD / 8);
+    const int vn = 8 * (tid % (kVT / 8)), vj = 4 * (tid / (kVT / 8));
+    const unsigned kst = (unsigned)(a.k.heads * a.kd * ES), vst = (unsigned)(a.v.heads * a.vd * ES),
+                   qst = kSt ? 0u : (unsigned)(a.q.heads * a.kd * ES);
+    const auto first = [&](const Tensor &x, int head, int dim, unsigned stride) {
+        return static_cast<const char *>(x.p) + bi * a.L * (int64_t)stride + (int64_t)head * dim * ES;
+    };
+    const char *kp = first(a.k, h / a.k.per, a.kd, kst), *vp = first(a.v, h / a.v.per, a.vd, vst),
+               *qp = kSt ? nullptr : first(a.q, h / a.q.per, a.kd, qst);
+    const auto offset = [&](int i, unsigned stride, int n, int dim) {
+        return n < dim ? (unsigned)(rv ? -1 - i : i) * stride + (unsigned)(n * ES) : kOutside;
+    };
+    const unsigned ko = KU % kThreads == 0 || kj < C ? offset(kj, kst, kn, a.kd) : kOutside,
+                   vo = vj < C ? offset(vj, vst, v0 + vn, a.vd) : kOutside,
+                   qo = kSt ? 0u : offset(qi, qst, kn, a.kd);
+    const auto tokens = [&](int64_t c) { return len - c * C >= C ? C : (len > c * C ? (int)(len - c * C) : 0); };
+    const auto span = [&](int nt, unsigned stride, int dim) {
+        return nt > 0 ? (unsigned)(nt - 1) * stride + (unsigned)(dim * ES) : 0u;
+    };
+    const auto fetch_k = [&](int nt, int u) {
+        const unsigned n = span(nt, kst, a.kd);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = 4 * KR * u + r;
+            kx[u][r] = load8<E, VEC>(kp, n, ko + (unsigned)(rv ? nt - d : d) * kst, a.kd - kn);
+        }
+    };
+    const auto fetch_v = [&](int nt) {
+        const unsigned n = span(nt, vst, a.vd);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            kx[u][r] = load8<VEC>(kb + (t0 + j + r) * kst, n0, a.kd, j < C && t0 + j + r < len);
+            vx[r] = load8<E, VEC>(vp, n, vo + (unsigned)(rv ? nt - r : r) * vst, a.vd - v0 - vn);
     };
-    const auto fetch_v = [&](int64_t t0) {
-        const int p0 = 8 * (tid % (kVT / 8)), j = 4 * (tid / (kVT / 8));
+    const auto fetch_q = [&](int nt, int u) {
+        const int d = KR * u;
+        qx[u] = load8<E, VEC>(qp, span(nt, qst, a.kd), qo + (unsigned)(rv ? nt - d : d) * qst,
+                              a.kd - kn);
+    };
+    // block (kn / 32, (kn % 16) / 4) and the next hold keys kn .. + 3 and kn + 4 .. + 7, in half (kn / 16) % 2
+    const int kblock = 4 * (kn >> 5) + ((kn & 15) >> 2), khalf = 4 * ((kn >> 4) & 1);
+    const auto put_row = [&](E *tile, int row, int swap, const typename O::pack &x) {  // swap: row & 7
+        put4(tile + row * KD + ((kblock ^ swap) << 3) + khalf, x, 0);
+        put4(tile + row * KD + ((kblock ^ swap ^ 1) << 3) + khalf, x, 1);
+    };
+    const auto put_columns = [&](E *tile, int n, int j, const typename O::pack(&x)[4]) {
+        const int b = opaque(((j >> 3) ^ (n >> 3)) & (C / 8 - 1));
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            vx[r] = load8<VEC>(vb + (t0 + j + r) * vst, v0 + p0, a.vd, j < C && t0 + j + r < len);
-    };
-    const auto fetch_q = [&](int64_t t0, int u) {
-        const int unit = tid + u * kThreads, n0 = 8 * (unit % (KD / 8)), i = unit / (KD / 8);
-        qx[u] = load8<VEC>(qb + (t0 + i) * qst, n0, a.kd, t0 + i < len);
+        for (int e = 0; e < 8; ++e)
+            put_column(tile + n * C + (j & 4) + e * C + ((b ^ (e & (C / 8 - 1))) << 3), x, e);
     };
     const auto stage_k = [&](int u) {
-        const int unit = tid + u * kThreads, n0 = 8 * (unit % (KD / 8)), j = 4 * (unit / (KD / 8));
-        if (KU % kThreads == 0 || unit < KU) {
+        const int j = kj + 4 * KR * u;
+        if (KU % kThreads == 0 || j < C) {
             if constexpr (!kSt) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) put_row<KD>(Ks, j + r, n0, kx[u][r]);
+                for (int r = 0; r < 4; ++r) put_row(Ks, j + r, (j & 4) + r, kx[u][r]);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) put_column(Kc + col_at<C>(n0 + e, j >> 3) + (j & 4), kx[u], e);
+            put_columns(Kc, kn, j, kx[u]);
         }
     };
     const auto stage_v = [&]() {
-        if (tid < VU) {
-            const int p0 = 8 * (tid % (kVT / 8)), j = 4 * (tid / (kVT / 8));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) put_column(Vc + col_at<C>(p0 + e, j >> 3) + (j & 4), vx, e);
-        }
+        if (VU == kThreads || tid < VU) put_columns(Vc, vn, vj, vx);
     };
-    const auto stage_q = [&](int u) {
-        const int unit = tid + u * kThreads;
-        put_row<KD>(Qs, unit / (KD / 8), 8 * (unit % (KD / 8)), qx[u]);
+    const auto stage_q = [&](int u) { put_row(Qs, qi + KR * u, qi & 7, qx[u]); };
+    static_assert(KR % 8 == 0, "a unit's rows keep their block exchange");
+    // The next chunk's tensors are loaded while this one is computed. Two states of 256 keys, and
+    // loads by single elements of 128, leave no registers for that: there each piece is loaded and staged by itself.
+    constexpr bool kAhead = KD == 256 ? !kDec : VEC || KD != 128 || MODE != kOut || ES == 4;
+    const auto advance = [&](int64_t chunks) {
+        kp += chunks * C * (int64_t)kst;
+        vp += chunks * C * (int64_t)vst;
+        if (!kSt) qp += chunks * C * (int64_t)qst;
     };
-    // The next chunk's tensors are loaded while this one is computed. Two states of 256 keys
-    // leave no registers for that: there each piece is loaded and staged by itself.
-    constexpr bool kAhead = !(kDec && KD == 256);
-    const auto fetch = [&](int64_t c) {
+    const auto fetch_kv = [&](int nt) {
 #pragma unroll
-        for (int u = 0; u < KN; ++u) fetch_k(c * C, u);
-        fetch_v(c * C);
-#pragma unroll
-        for (int u = 0; u < QN; ++u) fetch_q(c * C, u);
+        for (int u = 0; u < KN; ++u) fetch_k(nt, u);
+        fetch_v(nt);
     };
-    const auto stage = [&](int64_t c, int nt) {
+    const auto fetch_qs = [&](int nt) {
+#pragma unroll
+        for (int u = 0; u < QN; ++u) fetch_q(nt, u);
+    };
+    const auto stage = [&](int nt) {
 #pragma unroll
         for (int u = 0; u < KN; ++u) {
             if (!kAhead) {
-                fetch_k(c * C, u);
+                fetch_k(nt, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
             stage_k(u);
         }
         if (!kAhead) {
-            fetch_v(c * C);
+            fetch_v(nt);
             __builtin_amdgcn_sched_barrier(0);
         }
         stage_v();
 #pragma unroll
         for (int u = 0; u < QN; ++u) {
             if (!kAhead) {
-                fetch_q(c * C, u);
+                fetch_q(nt, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
             stage_q(u);
         }
-        if (tid < C) {
-            const int n = a.rev ? tid + 1 : nt - 1 - tid;  // steps from this token to the state behind it
-            const float p = tid < nt ? a.su * power(g2, n) : 0.f;
-            wt[tid] = p;
-            if constexpr (kDec || kSt) wu[tid] = n == 0 || p == 0.f ? 0.f : p * (float)n;
-        }
     };
 
+    // fragment addresses (see row_base and col_base)
+    const int qb[2] = {row_base<KD>(lr, lg, 0), row_base<KD>(lr, lg, 1)};
+    const int ab[2] = {row_base<C>(lr, lg, 0), row_base<C>(lr, lg, 1)};
+    const int cb[4] = {col_base<C>(lr, lg, 0), col_base<C>(lr, lg, 1), col_base<C>(lr, lg, 2), col_base<C>(lr, lg, 3)};
+    const int p0 = v0 + 16 * wave + 4 * lg;  // the 4 values of this lane's outputs
+    const unsigned oes = ES == 4 || a.o32 ? 4 : 2, ost = (unsigned)(a.H * a.vd) * oes;
+    const int64_t ofirst = (bi * a.L * a.H + h) * (int64_t)a.vd;
+    double dsum = 0.0;
+
     const int64_t nc = c_hi > c_lo ? c_hi - c_lo : 0;
-    if (kAhead && nc > 0) fetch(a.rev ? c_hi - 1 : c_lo);
+    const int64_t c0 = rv ? c_hi - 1 : c_lo;
+    const int way = rv ? -1 : 1;
+    if (nc > 0) advance(c0);
+    if (kAhead && nc > 0) {
+        fetch_kv(tokens(c0));
+        fetch_qs(tokens(c0));
+    }
+    int nt_of = -1;                          // the tokens that these are for:
+    float at = 1.f, at_lo = 0.f, atn = 0.f;  // a^nt in two parts, nt a^nt, and the tables wt, wu
+    const auto stage_all = [&](int nt) {
+        stage(nt);
+        if (nt != nt_of) {
+            nt_of = nt;
+            if (tid < C) {
+                const int n = nt - 1 - tid + rv;  // steps from this token to the state behind it
+                wt[tid] = tid < nt ? a.su * pw[n] : 0.f;
+                if constexpr (kU) wu[tid] = tid < nt ? a.su * pw[n] * (float)n : 0.f;
+            }
+            const double p = power(ld, nt);
+            at = uniform((float)p);
+            at_lo = uniform((float)(p - (double)at));
+            atn = uniform((float)(p * (double)nt));
+        }
+    };
+    if (nc > 0) stage_all(tokens(c0));
     for (int64_t s = 0; s < nc; ++s) {
-        const int64_t c = a.rev ? c_hi - 1 - s : c_lo + s, t0 = c * C;
-        const int nt = len - t0 >= C ? C : (len > t0 ? (int)(len - t0) : 0);
-        stage(c, nt);
-        __syncthreads();
-        if (kAhead && s + 1 < nc) fetch(a.rev ? c - 1 : c + 1);
+        const int64_t c = c0 + way * s;
+        const int nt = tokens(c);
+        __syncthreads();  // the chunk's tiles are there, the last one's scores have been read
+        if (s + 1 < nc) {
+            advance(way);
+            if (kAhead) fetch_kv(tokens(c + way));
+        }
         frag vf[JS];
 #pragma unroll
-        for (int ks = 0; ks < JS; ++ks) vf[ks] = frag_at(Vc + col_at<C>(16 * wave + lr, 4 * ks + lg));
+        for (int ks = 0; ks < JS; ++ks)
+            vf[ks] = frag_at(Vc + col_base<C>(lr, lg, 2 * ks ^ (wave & 3)) + 16 * C * wave);
 
+        f32x4 acc[IT];
         if constexpr (!kSt) {
-            // scores, transposed: rows j, column i = this lane's token of the strip
-            f32x4 sc[JW];
+            // Scores, transposed (rows j, column i = this lane's token of the strip), and the carried
+            // state's part of the outputs (rows are values, column i). The fragments of one are read
+            // while the other is computed.
+            f32x4 sc[JW], ac2[kDec ? IT : 1];
 #pragma unroll
             for (int t = 0; t < JW; ++t) sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const frag qf = frag_at(Qs + row_at<KD>(16 * st + lr, 4 * ks + lg));
-#pragma unroll
-                for (int t = 0; t < JW; ++t)
-                    sc[t] = O::mfma(frag_at(Ks + row_at<KD>(16 * (j0 + t) + lr, 4 * ks + lg)), qf, sc[t]);
-            }
-#pragma unroll
-            for (int t = 0; t < JW; ++t) {
-                const int i = 16 * st + lr, jb = 2 * (j0 + t) + (lg >> 1);
-                f32x4 x;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = mask[t][r] == 0.f ? 0.f : sc[t][r] * mask[t][r];
-                O::template store4<NA>(As + i * C + ((jb ^ (i & (C / 8 - 1))) << 3) + 4 * (lg & 1), C * C, x);
-            }
-            // the carried state's part: rows are values, column i
-            f32x4 acc[IT], ac2[kDec ? IT : 1];
 #pragma unroll
             for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
             if constexpr (kDec) {
 #pragma unroll
                 for (int it = 0; it < IT; ++it) ac2[it] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
+            constexpr int QA = IT == 4 ? 2 : 1;
+            frag qs[QA], kf[JW], qf[IT];
+            const auto read_q = [&](int ks) {
+#pragma unroll
+                for (int it = 0; it < IT; ++it) qf[it] = frag_at(Qs + qb[ks & 1] + 64 * (ks >> 1) + 16 * KD * it);
+            };
+            const auto read_s = [&](int ks) {
+                const int f = qb[ks & 1] + 64 * (ks >> 1);
+                qs[0] = frag_at(Qs + f + 16 * KD * sa);
+                if constexpr (QA == 2) qs[1] = frag_at(Qs + f + 16 * KD * sc_);
+#pragma unroll
+                for (int t = 0; t < JW; ++t) kf[t] = frag_at(Ks + f + 16 * KD * scol(t));
+            };
+            read_q(0);
+            read_s(0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
+                __builtin_amdgcn_sched_barrier(0);
                 float x[8];
                 frag sp[NS], up[kDec ? NS : 1];
 #pragma unroll
@@ -456,117 +549,157 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     O::template parts<NS>(x, up);
                 }
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const frag qf = frag_at(Qs + row_at<KD>(16 * it + lr, 4 * ks + lg));
+                for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
-                    for (int n = NS - 1; n >= 0; --n) {
-                        acc[it] = O::mfma(sp[n], qf, acc[it]);
-                        if constexpr (kDec) ac2[it] = O::mfma(up[n], qf, ac2[it]);
+                    for (int it = 0; it < IT; ++it) {
+                        acc[it] = O::mfma(sp[n], qf[it], acc[it]);
+                        if constexpr (kDec) ac2[it] = O::mfma(up[n], qf[it], ac2[it]);
                     }
-                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (ks + 1 < KS) read_q(ks + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int t = 0; t < JW; ++t) sc[t] = O::mfma(kf[t], qs[t == 2 ? 1 : 0], sc[t]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (ks + 1 < KS) read_s(ks + 1);
             }
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int i = 16 * it + lr, n = a.rev ? nt - 1 - i : i + 1;
-                const float p = i < nt ? a.sr * power(g2, n) : 0.f;
+            for (int t = 0; t < JW; ++t) {
+                const int jb = 2 * scol(t) + (lg >> 1);
+                f32x4 x;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (kDec) acc[it][r] = p * (acc[it][r] * (float)n + ac2[it][r]);
-                    else acc[it][r] *= p;
-                }
+                for (int r = 0; r < 4; ++r) x[r] = sc[t][r] * mask[t][r];
+                O::template store4<NA>(As + (16 * srow(t) + lr) * C + ((jb ^ (lr & (C / 8 - 1))) << 3) + 4 * (lg & 1),
+                                       C * C, x);
             }
-            __syncthreads();
 #pragma unroll
             for (int it = 0; it < IT; ++it)
 #pragma unroll
-                for (int ks = 0; ks < JS; ++ks)
-#pragma unroll
-                    for (int n = NA - 1; n >= 0; --n)
-                        acc[it] = O::mfma(
-                            vf[ks], frag_at(As + n * C * C + (16 * it + lr) * C + (((4 * ks + lg) ^ (lr & (C / 8 - 1))) << 3)),
-                            acc[it]);
-            const int p0 = v0 + 16 * wave + 4 * lg;
-            float csum = 0.f;
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int i = 16 * it + lr;
-                const int64_t tok = t0 + i;
-                if (tok >= a.L) continue;
-                const int64_t at = ((bi * a.L + tok) * a.H + h) * a.vd + p0;
-                if constexpr (kDec) {
-                    if (i < nt) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (p0 + r < a.vd) csum += acc[it][r] * ld_io<sizeof(E) == 2>(a.dy, at + r);
-                    }
-                } else {
-                    f32x4 x = acc[it];
-                    if (i >= nt) x = f32x4{0.f, 0.f, 0.f, 0.f};
-                    if (VEC) {
-                        if (p0 < a.vd) {
-                            if (sizeof(E) == 4 || a.o32)
-                                *reinterpret_cast<f32x4 *>(static_cast<float *>(a.o) + at) = x;
-                            else
-                                Ops<uint16_t>::store4<1>(static_cast<uint16_t *>(a.o) + at, 0, x);
-                        }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (p0 + r < a.vd) {
-                                if (sizeof(E) == 4 || a.o32) static_cast<float *>(a.o)[at + r] = x[r];
-                                else static_cast<__bf16 *>(a.o)[at + r] = (__bf16)x[r];
-                            }
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (kDec) acc[it][r] = rs[it] * (acc[it][r] * (float)(16 * it + lr + 1) + ac2[it][r]);
+                    else acc[it][r] *= rs[it];
                 }
-            }
-            if constexpr (kDec) dsum += (double)csum;
         }
+
+        if (kAhead && s + 1 < nc) fetch_qs(tokens(c + way));  // (here, where the registers for it are free)
 
         // the state behind the chunk
         {
-            const float at = power(g2, nt), atn = nt ? at * (float)nt : 0.f;
-            frag wv[JS][O::NW], wv2[kDec || kSt ? JS : 1][O::NW];
+            frag wv[JS][O::NW], wv2[kU ? JS : 1][O::NW], kf[2][2][JS];
+            const auto read = [&](int t) {
+#pragma unroll
+                for (int ks = 0; ks < JS; ++ks)
+#pragma unroll
+                    for (int d = 0; d < 2; ++d)
+                        kf[kAhead ? (t >> 1) & 1 : 0][d][ks] = frag_at(Kc + cb[2 * ks ^ ((t + d) & 3)] + 16 * C * (t + d));
+            };
+            if (kAhead) read(0);
 #pragma unroll
             for (int ks = 0; ks < JS; ++ks) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = wt[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
                 O::template parts<O::NW>(x, wv[ks]);
-                if constexpr (kDec || kSt) {
+                if constexpr (kU) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = wu[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
                     O::template parts<O::NW>(x, wv2[ks]);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                if constexpr (kDec || kSt) {
-                    if (with_u) {
+            for (int t = 0; t < KT; t += 2) {
+                if (!kAhead) read(t);
+                else if (t + 2 < KT) read(t + 2);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) U[t][r] = at * U[t][r] + (atn == 0.f ? 0.f : atn * S[t][r]);
-                    }
-                }
+                for (int d = 0; d < 2; ++d)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[t][r] *= at;
-#pragma unroll
-                for (int ks = 0; ks < JS; ++ks) {
-                    const frag kf = frag_at(Kc + col_at<C>(16 * t + lr, 4 * ks + lg));
-#pragma unroll
-                    for (int n = O::NW - 1; n >= 0; --n) {
-                        S[t] = O::mfma(kf, wv[ks][n], S[t]);
-                        if constexpr (kDec || kSt) {
-                            if (with_u) U[t] = O::mfma(kf, wv2[ks][n], U[t]);
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = S[t + d][r];
+                        if constexpr (kU) {
+                            const float u = U[t + d][r];
+                            U[t + d][r] = __builtin_fmaf(u, at_lo, at * u) + atn * x;
                         }
+                        S[t + d][r] = __builtin_fmaf(x, at_lo, at * x);
+                    }
+#pragma unroll
+                for (int ks = 0; ks < JS; ++ks)
+#pragma unroll
+                    for (int n = O::NW - 1; n >= 0; --n)
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            const frag k = kf[kAhead ? (t >> 1) & 1 : 0][d][ks];
+                            S[t + d] = O::mfma(k, wv[ks][n], S[t + d]);
+                            if constexpr (kU) U[t + d] = O::mfma(k, wv2[ks][n], U[t + d]);
+                        }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        __syncthreads();  // the scores are there, the chunk's tiles have been read
+
+        if constexpr (!kSt) {
+            // (the blocks of 32 tokens that lie behind a strip hold nothing for it)
+#pragma unroll
+            for (int ks = 0; ks < JS; ++ks) {
+                frag af[NA][IT];
+#pragma unroll
+                for (int n = NA - 1; n >= 0; --n)
+#pragma unroll
+                    for (int it = 2 * ks; it < IT; ++it) af[n][it] = frag_at(As + n * C * C + ab[ks] + 16 * C * it);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = NA - 1; n >= 0; --n)
+#pragma unroll
+                    for (int it = 2 * ks; it < IT; ++it) acc[it] = O::mfma(vf[ks], af[n][it], acc[it]);
+            }
+        }
+        if (s + 1 < nc) stage_all(tokens(c + way));
+        if constexpr (!kSt) {
+            const int rows = a.L - c * C < C ? (int)(a.L - c * C) : C;  // written: zeros behind the length
+            const int64_t obase = ofirst + c * C * (int64_t)(a.H * a.vd);
+            float csum = 0.f;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int i = 16 * it + lr, row = rv && i < nt ? nt - 1 - i : i;
+                if constexpr (kDec) {
+                    if (i < nt) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (p0 + r < a.vd)
+                                csum += acc[it][r] * ld_io<ES == 2>(a.dy, obase + (int64_t)row * a.H * a.vd + p0 + r);
+                    }
+                } else {
+                    f32x4 x = acc[it];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[r] = i < nt ? x[r] : 0.f;
+                    if constexpr (VEC) {
+                        const auto rsrc =
+                            __builtin_amdgcn_make_buffer_rsrc(static_cast<char *>(a.o) + obase * oes, 0,
+                                                              (int)((unsigned)(rows - 1) * ost + a.vd * oes), 0x00020000);
+                        const unsigned to = p0 < a.vd ? (unsigned)row * ost + p0 * oes : kOutside;
+                        if (oes == 4) {
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rsrc, to, 0, 0);
+                        } else {
+                            __builtin_amdgcn_raw_buffer_store_b64(bf16_pack4(x), rsrc, to, 0, 0);
+                        }
+                    } else if (row < rows) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (p0 + r < a.vd) {
+                                const int64_t to = obase + (int64_t)row * a.H * a.vd + p0 + r;
+                                if (oes == 4) static_cast<float *>(a.o)[to] = x[r];
+                                else static_cast<__bf16 *>(a.o)[to] = (__bf16)x[r];
+                            }
                     }
                 }
             }
+            if constexpr (kDec) dsum += (double)csum;
         }
-        __syncthreads();
     }
 
     if constexpr (kSt) {
         store_state(S, a.s_out, chain * a.nseg + seg);
-        if (with_u) store_state(U, a.u_out, chain * a.nseg + seg);
+        if constexpr (kU) store_state(U, a.u_out, chain * a.nseg + seg);
     }
     const bool last = a.rev ? seg == 0 : seg == a.nseg - 1;
     if constexpr (MODE == kOut) {
@@ -615,20 +748,21 @@ __global__ __launch_bounds__(kThreads) void linattn_chain_kernel(const ChainArgs
         const int64_t l = a.lengths[bi];
         len = l < 0 ? 0 : (l < a.L ? l : a.L);
     }
-    const float g2 = a.log_decay[chain % a.H] * kLog2e;
-    float s = a.init ? a.init[e] : 0.f, u = 0.f;
+    const float ld = a.log_decay[chain % a.H];
+    const double whole = power(ld, a.seg_tokens);
+    double s = a.init ? a.init[e] : 0.f, u = 0.0;
     for (int k = 0; k < a.nseg; ++k) {
         const int seg = a.rev ? a.nseg - 1 - k : k;
         int64_t n = len - seg * a.seg_tokens;
         n = n < 0 ? 0 : (n < a.seg_tokens ? n : a.seg_tokens);
-        const float p = n == 0 ? 1.f : __builtin_amdgcn_exp2f(g2 * (float)n);
+        const double p = n == a.seg_tokens ? whole : power(ld, n);
         const int64_t at = (chain * a.nseg + seg) * a.nstate + i;
         const float own = a.st[at];
-        a.st[at] = s;
+        a.st[at] = (float)s;
         if (a.ut) {
             const float ou = a.ut[at];
-            a.ut[at] = u;
-            u = p * u + (p == 0.f ? 0.f : p * (float)n * s) + ou;
+            a.ut[at] = (float)u;
+            u = p * u + p * (double)n * s + ou;
         }
         s = p * s + own;
     }
@@ -698,7 +832,7 @@ LinPlan make_lin_plan(const m3_shape &s) {
     int64_t n = s.nsegments;
     if (n == 0) {
         const int64_t have = p.chains * tiles(s.headdim);
-        n = have >= 384 || have == 0 ? 1 : (512 + have - 1) / have;
+        n = have >= 384 || have == 0 ? 1 : 512 / have;
         if (n > p.nchunks / 4) n = p.nchunks / 4;
     }
     if (n > p.nchunks) n = p.nchunks;
@@ -834,7 +968,7 @@ __global__ __launch_bounds__(kThreads) void linattn_step_kernel(const void *q, c
             for (int e = 0; e < V; ++e) x[i][e] = p < P && n0 + e < N ? ld_io<V == 8>(row, e) : 0.f;
         }
     }
-    const float a = expf(log_decay[h]);
+    const float a = (float)power(log_decay[h], 1);
     float kk[V], qq[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -927,7 +1061,7 @@ m3_status status(hipError_t e) { return e == hipSuccess ? M3_OK : M3_ERR_HIP; }
 // Segment states of one direction: each segment's own, then chained from init
 hipError_t segment_states(Args a, const LinPlan &p, bool bf16, float *st, float *ut, const float *init, hipStream_t s) {
     a.s_in = nullptr; a.s_out = st; a.u_out = ut;
-    const hipError_t e = launch_pass<kState>(a, bf16, s);
+    const hipError_t e = ut ? launch_pass<kStateU>(a, bf16, s) : launch_pass<kState>(a, bf16, s);
     return e == hipSuccess ? chain_states(a, p, st, ut, init, a.rev, s) : e;
 }
 
