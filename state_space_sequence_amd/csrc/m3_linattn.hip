@@ -215,27 +215,38 @@ __device__ __forceinline__ u32x2 bf16_pack4(f32x4 x) {
     return __builtin_bit_cast(u32x2, b);
 }
 
-template <typename E>
-__device__ __forceinline__ typename Ops<E>::frag frag_at(const E *p) {
-    return *reinterpret_cast<const typename Ops<E>::frag *>(p);
-}
-
-// LDS tiles, in blocks of 8 elements (one lane's operand slots), exchanged within a row so that
-// the 16 rows which a fragment read touches, and the rows that one store fills, lie
-// in different banks.
-// Row tile [token][KD keys]: block b of row i lies at b ^ (i & 7). Keys are permuted so that a block
+// LDS tiles, in blocks of 8 elements (one lane's operand slots). Blocks, and rows, are exchanged so that
+// the 16 lanes that read together (16 rows, one block) and the rows and columns that one
+// store fills spread over the 64 banks of 4 bytes.
+// Row tile [token][LD keys]: block b of row i lies at b ^ swap(i). Keys are permuted so that a block
 // holds what the state's accumulators hold of it: block 4s + g is keys 32s + 4g + 0..3 and
-// 32s + 16 + 4g + 0..3. A lane's fragment (row 16 t + lr, block 4 ks + lg) is at
-// row_base(ks & 1) + 64 (ks >> 1) + 16 KD t.
-template <int LD>
-__device__ __forceinline__ int row_base(int lr, int lg, int odd) {
-    return lr * LD + (((lg + 4 * odd) ^ (lr & (LD >= 64 ? 7 : 3))) << 3);
+// 32s + 16 + 4g + 0..3.
+template <typename E, int LD>
+__device__ __forceinline__ int row_swap_of(int row) {
+    constexpr int NB = LD / 8, shift = LD * sizeof(E) == 128 ? 1 : 0;  // two rows in the width of the banks
+    return (row >> shift) & (NB < 16 ? NB - 1 : 15);
 }
-// Transposed tile [key or value][C tokens]: block b of column n lies at b ^ ((n ^ n >> 3) & 7). A lane's
-// fragment (column 16 t + lr, block 4 ks + lg) is at col_base(2 ks ^ (t & 3)) + 16 C t.
-template <int C>
-__device__ __forceinline__ int col_base(int lr, int lg, int x) {
-    return lr * C + (((lg ^ (2 * x) ^ lr ^ (lr >> 3)) & (C / 8 - 1)) << 3);
+// byte offset of a lane's fragment (row lr, block lg); (row 16 t + lr, block 4 ks + lg) is row_frag of it
+template <typename E, int LD>
+__device__ __forceinline__ int row_base(int lr, int lg) {
+    return (lr * LD + ((lg ^ row_swap_of<E, LD>(lr)) << 3)) * (int)sizeof(E);
+}
+template <typename E, int LD>
+__device__ __forceinline__ typename Ops<E>::frag row_frag(const E *tile, int base, int t, int ks) {
+    const char *p = reinterpret_cast<const char *>(tile + 128 * (ks >> 2) + 16 * LD * t);
+    return *reinterpret_cast<const typename Ops<E>::frag *>(p + (base ^ (32 * (ks & 3) * (int)sizeof(E))));
+}
+// Transposed tile [key or value][C tokens]: column n = 8m + e lies at row 8m + (e ^ (m & 1)), its block b at
+// b ^ (e / 2) ^ 4 (m & 1) ^ (m / 2).
+template <typename E, int C>
+__device__ __forceinline__ int col_base(int lr, int lg) {
+    const int m = lr >> 3, f = ((lr >> 1) & 3) | (m << 2);
+    return ((lr ^ m) * C + (((lg ^ f) & (C / 8 - 1)) << 3)) * (int)sizeof(E);
+}
+template <typename E, int C>
+__device__ __forceinline__ typename Ops<E>::frag col_frag(const E *tile, int base, int t, int ks) {
+    const char *p = reinterpret_cast<const char *>(tile + 16 * C * t);
+    return *reinterpret_cast<const typename Ops<E>::frag *>(p + (base ^ (8 * ((4 * ks ^ t) & (C / 8 - 1)) * (int)sizeof(E))));
 }
 
 // A value the compiler cannot see through: addresses formed from it are formed where they
@@ -392,22 +403,24 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     };
     // block (kn / 32, (kn % 16) / 4) and the next hold keys kn .. + 3 and kn + 4 .. + 7, in half (kn / 16) % 2
     const int kblock = 4 * (kn >> 5) + ((kn & 15) >> 2), khalf = 4 * ((kn >> 4) & 1);
-    const auto put_row = [&](E *tile, int row, int swap, const typename O::pack &x) {  // swap: row & 7
+    const auto put_row = [&](E *tile, int row, int swap, const typename O::pack &x) {
         put4(tile + row * KD + ((kblock ^ swap) << 3) + khalf, x, 0);
         put4(tile + row * KD + ((kblock ^ swap ^ 1) << 3) + khalf, x, 1);
     };
     const auto put_columns = [&](E *tile, int n, int j, const typename O::pack(&x)[4]) {
-        const int b = opaque(((j >> 3) ^ (n >> 3)) & (C / 8 - 1));
+        const int m = n >> 3, f = ((m & 1) << 2) ^ (m >> 1);
+        const int at = opaque(((n + (m & 1)) * C + ((((j >> 3) ^ f) & (C / 8 - 1)) << 3) + (j & 4)) * ES);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            put_column(tile + n * C + (j & 4) + e * C + ((b ^ (e & (C / 8 - 1))) << 3), x, e);
+            put_column(reinterpret_cast<E *>(reinterpret_cast<char *>(tile) + (at ^ ((e * C + (((e >> 1) & (C / 8 - 1)) << 3)) * ES))),
+                       x, e);
     };
     const auto stage_k = [&](int u) {
         const int j = kj + 4 * KR * u;
         if (KU % kThreads == 0 || j < C) {
             if constexpr (!kSt) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) put_row(Ks, j + r, (j & 4) + r, kx[u][r]);
+                for (int r = 0; r < 4; ++r) put_row(Ks, j + r, row_swap_of<E, KD>(kj + r), kx[u][r]);
             }
             put_columns(Kc, kn, j, kx[u]);
         }
@@ -415,8 +428,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const auto stage_v = [&]() {
         if (VU == kThreads || tid < VU) put_columns(Vc, vn, vj, vx);
     };
-    const auto stage_q = [&](int u) { put_row(Qs, qi + KR * u, qi & 7, qx[u]); };
-    static_assert(KR % 8 == 0, "a unit's rows keep their block exchange");
+    const auto stage_q = [&](int u) { put_row(Qs, qi + KR * u, row_swap_of<E, KD>(qi + KR * u), qx[u]); };
+    static_assert(4 * KR % 16 == 0, "a unit's rows keep their block exchange");
     // The next chunk's tensors are loaded while this one is computed. Two states of 256 keys, and
     // loads by single elements of 128, leave no registers for that: there each piece is loaded and staged by itself.
     constexpr bool kAhead = KD == 256 ? !kDec : VEC || KD != 128 || MODE != kOut || ES == 4;
@@ -458,10 +471,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         }
     };
 
-    // fragment addresses (see row_base and col_base)
-    const int qb[2] = {row_base<KD>(lr, lg, 0), row_base<KD>(lr, lg, 1)};
-    const int ab[2] = {row_base<C>(lr, lg, 0), row_base<C>(lr, lg, 1)};
-    const int cb[4] = {col_base<C>(lr, lg, 0), col_base<C>(lr, lg, 1), col_base<C>(lr, lg, 2), col_base<C>(lr, lg, 3)};
+    const int qb0 = row_base<E, KD>(lr, lg), ab0 = row_base<E, C>(lr, lg), cb0 = col_base<E, C>(lr, lg);
     const int p0 = v0 + 16 * wave + 4 * lg;  // the 4 values of this lane's outputs
     const unsigned oes = ES == 4 || a.o32 ? 4 : 2, ost = (unsigned)(a.H * a.vd) * oes;
     const int64_t ofirst = (bi * a.L * a.H + h) * (int64_t)a.vd;
@@ -501,10 +511,11 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
             advance(way);
             if (kAhead) fetch_kv(tokens(c + way));
         }
+        const int qb = opaque(qb0), ab = opaque(ab0), cb = opaque(cb0);
         frag vf[JS];
 #pragma unroll
         for (int ks = 0; ks < JS; ++ks)
-            vf[ks] = frag_at(Vc + col_base<C>(lr, lg, 2 * ks ^ (wave & 3)) + 16 * C * wave);
+            vf[ks] = col_frag<E, C>(Vc, cb, wave, ks);
 
         f32x4 acc[IT];
         if constexpr (!kSt) {
@@ -524,14 +535,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
             frag qs[QA], kf[JW], qf[IT];
             const auto read_q = [&](int ks) {
 #pragma unroll
-                for (int it = 0; it < IT; ++it) qf[it] = frag_at(Qs + qb[ks & 1] + 64 * (ks >> 1) + 16 * KD * it);
+                for (int it = 0; it < IT; ++it) qf[it] = row_frag<E, KD>(Qs, qb, it, ks);
             };
             const auto read_s = [&](int ks) {
-                const int f = qb[ks & 1] + 64 * (ks >> 1);
-                qs[0] = frag_at(Qs + f + 16 * KD * sa);
-                if constexpr (QA == 2) qs[1] = frag_at(Qs + f + 16 * KD * sc_);
+                qs[0] = row_frag<E, KD>(Qs, qb, sa, ks);
+                if constexpr (QA == 2) qs[1] = row_frag<E, KD>(Qs, qb, sc_, ks);
 #pragma unroll
-                for (int t = 0; t < JW; ++t) kf[t] = frag_at(Ks + f + 16 * KD * scol(t));
+                for (int t = 0; t < JW; ++t) kf[t] = row_frag<E, KD>(Ks, qb, scol(t), ks);
             };
             read_q(0);
             read_s(0);
@@ -569,8 +579,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 f32x4 x;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[r] = sc[t][r] * mask[t][r];
-                O::template store4<NA>(As + (16 * srow(t) + lr) * C + ((jb ^ (lr & (C / 8 - 1))) << 3) + 4 * (lg & 1),
-                                       C * C, x);
+                O::template store4<NA>(
+                    As + (16 * srow(t) + lr) * C + ((jb ^ row_swap_of<E, C>(lr)) << 3) + 4 * (lg & 1), C * C, x);
             }
 #pragma unroll
             for (int it = 0; it < IT; ++it)
@@ -591,7 +601,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 for (int ks = 0; ks < JS; ++ks)
 #pragma unroll
                     for (int d = 0; d < 2; ++d)
-                        kf[kAhead ? (t >> 1) & 1 : 0][d][ks] = frag_at(Kc + cb[2 * ks ^ ((t + d) & 3)] + 16 * C * (t + d));
+                        kf[kAhead ? (t >> 1) & 1 : 0][d][ks] = col_frag<E, C>(Kc, cb, t + d, ks);
             };
             if (kAhead) read(0);
 #pragma unroll
@@ -645,7 +655,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
                 for (int n = NA - 1; n >= 0; --n)
 #pragma unroll
-                    for (int it = 2 * ks; it < IT; ++it) af[n][it] = frag_at(As + n * C * C + ab[ks] + 16 * C * it);
+                    for (int it = 2 * ks; it < IT; ++it) af[n][it] = row_frag<E, C>(As + n * C * C, ab, it, ks);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int n = NA - 1; n >= 0; --n)
