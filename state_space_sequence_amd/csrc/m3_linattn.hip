@@ -23,10 +23,11 @@
 // A workgroup of 4 waves owns one chain (batch, head), 64 of its values (columns of S) and one
 // segment of the tokens. Wave w owns 16 columns: its part of S never leaves its
 // registers. The accumulators of the update (keys down the rows) are, two row
-// tiles at a time, the operand of the product with q, provided that the key
-// index of q is stored in the same order: q and k lie in LDS with their columns
-// permuted so (perm below), and k and v a second time transposed, tokens
-// consecutive, for the products that contract over tokens.
+// tiles at a time, the operand of the product with q: the update's rows are given to
+// the keys so that a lane ends up with 8 consecutive ones. q, k and v lie in LDS as they are
+// in memory, a row a token. The products that contract over tokens need k and v by
+// columns: bf16 through the transposing LDS read (each lane of 16 names 4 consecutive elements of
+// one of 4 rows and gets 4 rows of one column), fp32 element by element.
 #include <math.h>
 
 #include "m3_internal.h"
@@ -192,61 +193,91 @@ __device__ __forceinline__ typename Ops<E>::pack load8(const char *p, unsigned b
     }
 }
 
-// elements 4 half .. + 3 of a packed row
-__device__ __forceinline__ void put4(uint16_t *to, u32x4 w, int half) {
-    *reinterpret_cast<u32x2 *>(to) = half ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]};
-}
-__device__ __forceinline__ void put4(float *to, f32x8 x, int half) {
-    *reinterpret_cast<f32x4 *>(to) = half ? f32x4{x[4], x[5], x[6], x[7]} : f32x4{x[0], x[1], x[2], x[3]};
-}
-// element e of four packed rows
-__device__ __forceinline__ void put_column(uint16_t *to, const u32x4 (&w)[4], int e) {
-    const unsigned sel = e & 1 ? 0x07060302u : 0x05040100u;
-    *reinterpret_cast<u32x2 *>(to) = u32x2{__builtin_amdgcn_perm(w[1][e >> 1], w[0][e >> 1], sel),
-                                           __builtin_amdgcn_perm(w[3][e >> 1], w[2][e >> 1], sel)};
-}
-__device__ __forceinline__ void put_column(float *to, const f32x8 (&x)[4], int e) {
-    *reinterpret_cast<f32x4 *>(to) = f32x4{x[0][e], x[1][e], x[2][e], x[3][e]};
-}
-
 __device__ __forceinline__ u32x2 bf16_pack4(f32x4 x) {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     const bf16x4 b = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
     return __builtin_bit_cast(u32x2, b);
 }
 
-// LDS tiles, in blocks of 8 elements (one lane's operand slots). Blocks, and rows, are exchanged so that
-// the 16 lanes that read together (16 rows, one block) and the rows and columns that one
-// store fills spread over the 64 banks of 4 bytes.
-// Row tile [token][LD keys]: block b of row i lies at b ^ swap(i). Keys are permuted so that a block
-// holds what the state's accumulators hold of it: block 4s + g is keys 32s + 4g + 0..3 and
-// 32s + 16 + 4g + 0..3.
+// LDS tiles [token][LD], in blocks of 8 elements (one lane's operand slots). Block b of row i lies at
+// b ^ swap(i), so that the 16 lanes that read one block of 16 rows, and those that read 4 blocks of
+// 4 rows, spread over the 64 banks of 4 bytes.
 template <typename E, int LD>
-__device__ __forceinline__ int row_swap_of(int row) {
-    constexpr int NB = LD / 8, shift = LD * sizeof(E) == 128 ? 1 : 0;  // two rows in the width of the banks
-    return (row >> shift) & (NB < 16 ? NB - 1 : 15);
+__device__ __forceinline__ int swap_of(int row) {
+    constexpr int NB = LD / 8;
+    if constexpr (sizeof(E) == 2)
+        return (NB >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    else
+        return NB >= 8 ? row & 7 : (row >> 1) & 3;
 }
-// byte offset of a lane's fragment (row lr, block lg); (row 16 t + lr, block 4 ks + lg) is row_frag of it
+template <typename E>
+__device__ __forceinline__ E *at_byte(E *tile, int byte) {
+    return reinterpret_cast<E *>(reinterpret_cast<char *>(tile) + byte);
+}
+// Row fragment t, ks of a lane: row 16 t + lr, elements 32 ks + 8 lg .. + 7. base: for t = ks = 0, in bytes
 template <typename E, int LD>
 __device__ __forceinline__ int row_base(int lr, int lg) {
-    return (lr * LD + ((lg ^ row_swap_of<E, LD>(lr)) << 3)) * (int)sizeof(E);
+    return (lr * LD + ((lg ^ swap_of<E, LD>(lr)) << 3)) * (int)sizeof(E);
 }
 template <typename E, int LD>
-__device__ __forceinline__ typename Ops<E>::frag row_frag(const E *tile, int base, int t, int ks) {
-    const char *p = reinterpret_cast<const char *>(tile + 128 * (ks >> 2) + 16 * LD * t);
-    return *reinterpret_cast<const typename Ops<E>::frag *>(p + (base ^ (32 * (ks & 3) * (int)sizeof(E))));
+__device__ __forceinline__ typename Ops<E>::frag row_frag(E *tile, int base, int t, int ks) {
+    return *reinterpret_cast<const typename Ops<E>::frag *>(
+        at_byte(tile + 128 * (ks >> 2) + 16 * LD * t, base ^ (32 * (ks & 3) * (int)sizeof(E))));
 }
-// Transposed tile [key or value][C tokens]: column n = 8m + e lies at row 8m + (e ^ (m & 1)), its block b at
-// b ^ (e / 2) ^ 4 (m & 1) ^ (m / 2).
-template <typename E, int C>
+__device__ __forceinline__ bf16x8 transposed(uint16_t *p, uint16_t *q) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)q);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// Column fragment t, ks of a lane: tokens 32 ks + 8 lg .. + 7 of key key_of(t, lr >> 2, lr & 3), where
+// key_of gives rows 4 g + r of the two row tiles 2s, 2s + 1 the keys 32 s + 8 g + 0..7
+__device__ __forceinline__ int key_of(int t, int g, int r) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r; }
+template <typename E, int LD>
 __device__ __forceinline__ int col_base(int lr, int lg) {
-    const int m = lr >> 3, f = ((lr >> 1) & 3) | (m << 2);
-    return ((lr ^ m) * C + (((lg ^ f) & (C / 8 - 1)) << 3)) * (int)sizeof(E);
+    if constexpr (sizeof(E) == 2) {
+        const int row = 8 * lg + (lr >> 2);
+        return (row * LD + (((lr & 3) ^ swap_of<E, LD>(row)) << 3)) * 2;
+    } else {
+        return (8 * lg * LD + ((lr >> 2) << 3) + (lr & 3)) * 4;
+    }
 }
-template <typename E, int C>
-__device__ __forceinline__ typename Ops<E>::frag col_frag(const E *tile, int base, int t, int ks) {
-    const char *p = reinterpret_cast<const char *>(tile + 16 * C * t);
-    return *reinterpret_cast<const typename Ops<E>::frag *>(p + (base ^ (8 * ((4 * ks ^ t) & (C / 8 - 1)) * (int)sizeof(E))));
+template <typename E, int LD>
+__device__ __forceinline__ typename Ops<E>::frag col_frag(E *tile, int base, int t, int ks) {
+    const int s = t >> 1, h = 4 * (t & 1);
+    if constexpr (sizeof(E) == 2) {
+        E *p = tile + 32 * ks * LD + h + 128 * (s >> 2);
+        return transposed(at_byte(p, base ^ (64 * (s & 3))), at_byte(p + 4 * LD, base ^ (64 * (s & 3) + 16)));
+    } else {
+        f32x8 x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = *at_byte(tile + e * LD + h + 64 * (s >> 1), base ^ (32 * (e ^ (4 * (s & 1)))));
+        return x;
+    }
+}
+// The same of value 16 w + lr, of a tile of 64 values
+template <typename E>
+__device__ __forceinline__ int val_base(int lr, int lg, int w) {
+    if constexpr (sizeof(E) == 2) {
+        const int row = 8 * lg + (lr >> 2);
+        return (row * kVT + (((2 * w + ((lr >> 1) & 1)) ^ swap_of<E, kVT>(row)) << 3) + 4 * (lr & 1)) * 2;
+    } else {
+        return (8 * lg * kVT + ((2 * w + (lr >> 3)) << 3) + (lr & 7)) * 4;
+    }
+}
+template <typename E>
+__device__ __forceinline__ typename Ops<E>::frag val_frag(E *tile, int base, int ks) {
+    if constexpr (sizeof(E) == 2) {
+        E *p = tile + 32 * ks * kVT;
+        return transposed(at_byte(p, base), at_byte(p + 4 * kVT, base ^ 16));
+    } else {
+        f32x8 x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = *at_byte(tile + e * kVT, base ^ (32 * e));
+        return x;
+    }
 }
 
 // A value the compiler cannot see through: addresses formed from it are formed where they
@@ -282,9 +313,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     constexpr bool kDec = MODE == kDecay, kSt = MODE == kState || MODE == kStateU, kU = kDec || MODE == kStateU;
     constexpr int NA = kDec ? O::NU : O::NA, NS = kDec ? O::NU : O::NS;
     __shared__ __align__(16) E Qs[kSt ? 8 : C * KD];
-    __shared__ __align__(16) E Ks[kSt ? 8 : C * KD];
-    __shared__ __align__(16) E Kc[KD * C];
-    __shared__ __align__(16) E Vc[kVT * C];
+    __shared__ __align__(16) E Ks[C * KD];
+    __shared__ __align__(16) E Vs[C * kVT];
     __shared__ __align__(16) E As[kSt ? 8 : NA * C * C];
     __shared__ __align__(16) float wt[C], wu[kU ? C : 1];
     __shared__ float pw[C + 1];  // a^n
@@ -308,7 +338,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const int v0 = vt * kVT, col = v0 + 16 * wave + lr;  // this lane's value column
     const int64_t nstate = (int64_t)a.kd * a.vd;
 
-    // the state: rows n = 16 t + 4 lg + r of column col
+    // the state: keys key_of(t, lg, r) of column col
     f32x4 S[KT], U[kU ? KT : 1];
     const auto load_state = [&](f32x4 *to, const float *from) {
         const float *p = from ? from + (a.seg_in ? chain * a.nseg + seg : chain) * nstate : nullptr;
@@ -316,7 +346,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int n = 16 * t + 4 * lg + r;
+                const int n = key_of(t, lg, r);
                 to[t][r] = p && n < a.kd && col < a.vd ? p[n * a.sk + col * a.sv] : 0.f;
             }
     };
@@ -326,7 +356,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int n = 16 * t + 4 * lg + r;
+                const int n = key_of(t, lg, r);
                 if (n < a.kd && col < a.vd) p[n * a.sk + col * a.sv] = from[t][r];
             }
     };
@@ -355,16 +385,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         for (int it = 0; it < IT; ++it) rs[it] = a.sr * pw[16 * it + lr + 1 - rv];
     }
 
-    // Staging units: k and v 4 tokens x 8 columns, q 1 token x 8 columns. Row i of a chunk is its
-    // token i, or nt - 1 - i backwards: at (rv ? nt - 1 - i : i) strides from the first.
-    constexpr int KU = (C / 4) * (KD / 8), KN = (KU + kThreads - 1) / kThreads;
-    constexpr int VU = (C / 4) * (kVT / 8);
-    constexpr int QN = kSt ? 0 : C * (KD / 8) / kThreads;
-    static_assert(VU <= kThreads && (kSt || C * (KD / 8) % kThreads == 0), "staging");
-    constexpr int KR = kThreads / (KD / 8);  // units of one pass over the rows
-    typename O::pack kx[KN][4], vx[4], qx[QN ? QN : 1];
-    const int kn = 8 * (tid % (KD / 8)), kj = 4 * (tid / (KD / 8)), qi = tid / (KD / 8);
-    const int vn = 8 * (tid % (kVT / 8)), vj = 4 * (tid / (kVT / 8));
+    // Staging: 8 columns of a row a thread. Row i of a chunk is its token i, or nt - 1 - i backwards:
+    // at (rv ? nt - 1 - i : i) strides from the first.
+    constexpr int KN = C * (KD / 8) / kThreads, VN = C * (kVT / 8) / kThreads, QN = kSt ? 0 : KN;
+    static_assert(C * (KD / 8) % kThreads == 0 && C * (kVT / 8) % kThreads == 0, "staging");
+    constexpr int KR = kThreads / (KD / 8), VR = kThreads / (kVT / 8);  // rows of one pass
+    typename O::pack kx[KN], vx[VN], qx[QN ? QN : 1];
+    const int kn = 8 * (tid % (KD / 8)), ki = tid / (KD / 8), vn = 8 * (tid % (kVT / 8)), vi = tid / (kVT / 8);
     const unsigned kst = (unsigned)(a.k.heads * a.kd * ES), vst = (unsigned)(a.v.heads * a.vd * ES),
                    qst = kSt ? 0u : (unsigned)(a.q.heads * a.kd * ES);
     const auto first = [&](const Tensor &x, int head, int dim, unsigned stride) {
@@ -375,61 +402,25 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const auto offset = [&](int i, unsigned stride, int n, int dim) {
         return n < dim ? (unsigned)(rv ? -1 - i : i) * stride + (unsigned)(n * ES) : kOutside;
     };
-    const unsigned ko = KU % kThreads == 0 || kj < C ? offset(kj, kst, kn, a.kd) : kOutside,
-                   vo = vj < C ? offset(vj, vst, v0 + vn, a.vd) : kOutside,
-                   qo = kSt ? 0u : offset(qi, qst, kn, a.kd);
+    const unsigned ko = offset(ki, kst, kn, a.kd), vo = offset(vi, vst, v0 + vn, a.vd),
+                   qo = kSt ? 0u : offset(ki, qst, kn, a.kd);
     const auto tokens = [&](int64_t c) { return len - c * C >= C ? C : (len > c * C ? (int)(len - c * C) : 0); };
     const auto span = [&](int nt, unsigned stride, int dim) {
         return nt > 0 ? (unsigned)(nt - 1) * stride + (unsigned)(dim * ES) : 0u;
     };
+    const auto down = [&](int nt, int rows, unsigned stride) { return (unsigned)(rv ? nt - rows : rows) * stride; };
     const auto fetch_k = [&](int nt, int u) {
-        const unsigned n = span(nt, kst, a.kd);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = 4 * KR * u + r;
-            kx[u][r] = load8<E, VEC>(kp, n, ko + (unsigned)(rv ? nt - d : d) * kst, a.kd - kn);
-        }
+        kx[u] = load8<E, VEC>(kp, span(nt, kst, a.kd), ko + down(nt, KR * u, kst), a.kd - kn);
     };
-    const auto fetch_v = [&](int nt) {
-        const unsigned n = span(nt, vst, a.vd);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            vx[r] = load8<E, VEC>(vp, n, vo + (unsigned)(rv ? nt - r : r) * vst, a.vd - v0 - vn);
+    const auto fetch_v = [&](int nt, int u) {
+        vx[u] = load8<E, VEC>(vp, span(nt, vst, a.vd), vo + down(nt, VR * u, vst), a.vd - v0 - vn);
     };
     const auto fetch_q = [&](int nt, int u) {
-        const int d = KR * u;
-        qx[u] = load8<E, VEC>(qp, span(nt, qst, a.kd), qo + (unsigned)(rv ? nt - d : d) * qst,
-                              a.kd - kn);
+        qx[u] = load8<E, VEC>(qp, span(nt, qst, a.kd), qo + down(nt, KR * u, qst), a.kd - kn);
     };
-    // block (kn / 32, (kn % 16) / 4) and the next hold keys kn .. + 3 and kn + 4 .. + 7, in half (kn / 16) % 2
-    const int kblock = 4 * (kn >> 5) + ((kn & 15) >> 2), khalf = 4 * ((kn >> 4) & 1);
-    const auto put_row = [&](E *tile, int row, int swap, const typename O::pack &x) {
-        put4(tile + row * KD + ((kblock ^ swap) << 3) + khalf, x, 0);
-        put4(tile + row * KD + ((kblock ^ swap ^ 1) << 3) + khalf, x, 1);
-    };
-    const auto put_columns = [&](E *tile, int n, int j, const typename O::pack(&x)[4]) {
-        const int m = n >> 3, f = ((m & 1) << 2) ^ (m >> 1);
-        const int at = opaque(((n + (m & 1)) * C + ((((j >> 3) ^ f) & (C / 8 - 1)) << 3) + (j & 4)) * ES);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            put_column(reinterpret_cast<E *>(reinterpret_cast<char *>(tile) + (at ^ ((e * C + (((e >> 1) & (C / 8 - 1)) << 3)) * ES))),
-                       x, e);
-    };
-    const auto stage_k = [&](int u) {
-        const int j = kj + 4 * KR * u;
-        if (KU % kThreads == 0 || j < C) {
-            if constexpr (!kSt) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) put_row(Ks, j + r, row_swap_of<E, KD>(kj + r), kx[u][r]);
-            }
-            put_columns(Kc, kn, j, kx[u]);
-        }
-    };
-    const auto stage_v = [&]() {
-        if (VU == kThreads || tid < VU) put_columns(Vc, vn, vj, vx);
-    };
-    const auto stage_q = [&](int u) { put_row(Qs, qi + KR * u, row_swap_of<E, KD>(qi + KR * u), qx[u]); };
-    static_assert(4 * KR % 16 == 0, "a unit's rows keep their block exchange");
+    const auto put = [&](E *to, const typename O::pack &x) { *reinterpret_cast<typename O::pack *>(to) = x; };
+    const auto k_at = [&](int u) { return (ki + KR * u) * KD + (((kn >> 3) ^ swap_of<E, KD>(ki + KR * u)) << 3); };
+    const auto v_at = [&](int u) { return (vi + VR * u) * kVT + (((vn >> 3) ^ swap_of<E, kVT>(vi + VR * u)) << 3); };
     // The next chunk's tensors are loaded while this one is computed. Two states of 256 keys, and
     // loads by single elements of 128, leave no registers for that: there each piece is loaded and staged by itself.
     constexpr bool kAhead = KD == 256 ? !kDec : VEC || KD != 128 || MODE != kOut || ES == 4;
@@ -441,7 +432,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const auto fetch_kv = [&](int nt) {
 #pragma unroll
         for (int u = 0; u < KN; ++u) fetch_k(nt, u);
-        fetch_v(nt);
+#pragma unroll
+        for (int u = 0; u < VN; ++u) fetch_v(nt, u);
     };
     const auto fetch_qs = [&](int nt) {
 #pragma unroll
@@ -454,24 +446,28 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 fetch_k(nt, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            stage_k(u);
+            put(Ks + k_at(u), kx[u]);
         }
-        if (!kAhead) {
-            fetch_v(nt);
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < VN; ++u) {
+            if (!kAhead) {
+                fetch_v(nt, u);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            put(Vs + v_at(u), vx[u]);
         }
-        stage_v();
 #pragma unroll
         for (int u = 0; u < QN; ++u) {
             if (!kAhead) {
                 fetch_q(nt, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            stage_q(u);
+            put(Qs + k_at(u), qx[u]);
         }
     };
 
-    const int qb0 = row_base<E, KD>(lr, lg), ab0 = row_base<E, C>(lr, lg), cb0 = col_base<E, C>(lr, lg);
+    const int qb0 = row_base<E, KD>(lr, lg), ab0 = row_base<E, C>(lr, lg), cb0 = col_base<E, KD>(lr, lg),
+              vb0 = val_base<E>(lr, lg, wave);
     const int p0 = v0 + 16 * wave + 4 * lg;  // the 4 values of this lane's outputs
     const unsigned oes = ES == 4 || a.o32 ? 4 : 2, ost = (unsigned)(a.H * a.vd) * oes;
     const int64_t ofirst = (bi * a.L * a.H + h) * (int64_t)a.vd;
@@ -486,7 +482,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         fetch_qs(tokens(c0));
     }
     int nt_of = -1;                          // the tokens that these are for:
-    float at = 1.f, at_lo = 0.f, atn = 0.f;  // a^nt in two parts, nt a^nt, and the tables wt, wu
+    double whole = 1.0, drift = 0.0;         // a^nt, nt a^nt, and the tables wt, wu
+    float atn = 0.f;
     const auto stage_all = [&](int nt) {
         stage(nt);
         if (nt != nt_of) {
@@ -496,10 +493,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 wt[tid] = tid < nt ? a.su * pw[n] : 0.f;
                 if constexpr (kU) wu[tid] = tid < nt ? a.su * pw[n] * (float)n : 0.f;
             }
-            const double p = power(ld, nt);
-            at = uniform((float)p);
-            at_lo = uniform((float)(p - (double)at));
-            atn = uniform((float)(p * (double)nt));
+            whole = power(ld, nt);
+            atn = uniform((float)(whole * (double)nt));
         }
     };
     if (nc > 0) stage_all(tokens(c0));
@@ -511,11 +506,11 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
             advance(way);
             if (kAhead) fetch_kv(tokens(c + way));
         }
-        const int qb = opaque(qb0), ab = opaque(ab0), cb = opaque(cb0);
+        const int qb = opaque(qb0), ab = opaque(ab0), cb = opaque(cb0), vb = opaque(vb0);
         frag vf[JS];
 #pragma unroll
         for (int ks = 0; ks < JS; ++ks)
-            vf[ks] = col_frag<E, C>(Vc, cb, wave, ks);
+            vf[ks] = val_frag<E>(Vs, vb, ks);
 
         f32x4 acc[IT];
         if constexpr (!kSt) {
@@ -580,7 +575,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[r] = sc[t][r] * mask[t][r];
                 O::template store4<NA>(
-                    As + (16 * srow(t) + lr) * C + ((jb ^ row_swap_of<E, C>(lr)) << 3) + 4 * (lg & 1), C * C, x);
+                    As + (16 * srow(t) + lr) * C + ((jb ^ swap_of<E, C>(lr)) << 3) + 4 * (lg & 1), C * C, x);
             }
 #pragma unroll
             for (int it = 0; it < IT; ++it)
@@ -595,13 +590,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 
         // the state behind the chunk
         {
-            frag wv[JS][O::NW], wv2[kU ? JS : 1][O::NW], kf[2][2][JS];
-            const auto read = [&](int t) {
+            // a step: four key tiles and 32 tokens, whose fragments are read during the step before
+            constexpr int TS = 4, NSTEP = KT / TS * JS;
+            frag wv[JS][O::NW], wv2[kU ? JS : 1][O::NW], kf[2][TS];
+            const auto read = [&](int step) {
 #pragma unroll
-                for (int ks = 0; ks < JS; ++ks)
-#pragma unroll
-                    for (int d = 0; d < 2; ++d)
-                        kf[kAhead ? (t >> 1) & 1 : 0][d][ks] = col_frag<E, C>(Kc, cb, t + d, ks);
+                for (int d = 0; d < TS; ++d)
+                    kf[kAhead ? step & 1 : 0][d] = col_frag<E, KD>(Ks, cb, TS * (step / JS) + d, step % JS);
             };
             if (kAhead) read(0);
 #pragma unroll
@@ -616,32 +611,32 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     O::template parts<O::NW>(x, wv2[ks]);
                 }
             }
+            // a^nt rounded so that the errors of the chunks cancel: of their product no more than one remains
+            const float at = uniform((float)(whole + drift));
+            drift += whole - (double)at;
 #pragma unroll
-            for (int t = 0; t < KT; t += 2) {
-                if (!kAhead) read(t);
-                else if (t + 2 < KT) read(t + 2);
+            for (int step = 0; step < NSTEP; ++step) {
+                const int t = TS * (step / JS), ks = step % JS;
+                if (!kAhead) read(step);
+                else if (step + 1 < NSTEP) read(step + 1);
                 __builtin_amdgcn_sched_barrier(0);
+                if (ks == 0) {
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
+                    for (int d = 0; d < TS; ++d)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = S[t + d][r];
-                        if constexpr (kU) {
-                            const float u = U[t + d][r];
-                            U[t + d][r] = __builtin_fmaf(u, at_lo, at * u) + atn * x;
+                        for (int r = 0; r < 4; ++r) {
+                            if constexpr (kU) U[t + d][r] = at * U[t + d][r] + atn * S[t + d][r];
+                            S[t + d][r] *= at;
                         }
-                        S[t + d][r] = __builtin_fmaf(x, at_lo, at * x);
+                }
+#pragma unroll
+                for (int n = O::NW - 1; n >= 0; --n)
+#pragma unroll
+                    for (int d = 0; d < TS; ++d) {
+                        const frag k = kf[kAhead ? step & 1 : 0][d];
+                        S[t + d] = O::mfma(k, wv[ks][n], S[t + d]);
+                        if constexpr (kU) U[t + d] = O::mfma(k, wv2[ks][n], U[t + d]);
                     }
-#pragma unroll
-                for (int ks = 0; ks < JS; ++ks)
-#pragma unroll
-                    for (int n = O::NW - 1; n >= 0; --n)
-#pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-                            const frag k = kf[kAhead ? (t >> 1) & 1 : 0][d][ks];
-                            S[t + d] = O::mfma(k, wv[ks][n], S[t + d]);
-                            if constexpr (kU) U[t + d] = O::mfma(k, wv2[ks][n], U[t + d]);
-                        }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -680,8 +675,10 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     }
                 } else {
                     f32x4 x = acc[it];
+                    if (nt < C) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[r] = i < nt ? x[r] : 0.f;
+                        for (int r = 0; r < 4; ++r) x[r] = i < nt ? x[r] : 0.f;
+                    }
                     if constexpr (VEC) {
                         const auto rsrc =
                             __builtin_amdgcn_make_buffer_rsrc(static_cast<char *>(a.o) + obase * oes, 0,
@@ -722,7 +719,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int n = 16 * t + 4 * lg + r;
+                    const int n = key_of(t, lg, r);
                     if (n < a.kd && col < a.vd) dsum += (double)U[t][r] * p[(int64_t)n * a.sk + (int64_t)col * a.sv];
                 }
         }
