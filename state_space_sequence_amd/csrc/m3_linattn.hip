@@ -200,13 +200,15 @@ __device__ __forceinline__ u32x2 bf16_pack4(f32x4 x) {
 }
 
 // LDS tiles [token][LD], in blocks of 8 elements (one lane's operand slots). Block b of row i lies at
-// b ^ swap(i), so that the 16 lanes that read one block of 16 rows, and those that read 4 blocks of
-// 4 rows, spread over the 64 banks of 4 bytes.
+// b ^ swap(i), so that the lanes that read one block of 16 rows, and those that read 4 blocks of
+// 4 rows, spread over the 64 banks of 4 bytes. 16-byte reads are served to 16 lanes at a time, of two
+// lane groups: rows 0-3 and 12-15 of one with rows 4-11 of the next, so the low bits of these rows' swaps
+// have to stay apart when one block number is odd (0, 1 against 2, 3).
 template <typename E, int LD>
 __device__ __forceinline__ int swap_of(int row) {
     constexpr int NB = LD / 8;
     if constexpr (sizeof(E) == 2)
-        return (NB >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+        return (NB >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2) | ((((row >> 2) ^ (row >> 3)) & 1) << 1) | ((row >> 3) & 1);
     else
         return NB >= 8 ? row & 7 : (row >> 1) & 3;
 }
@@ -248,7 +250,7 @@ __device__ __forceinline__ typename Ops<E>::frag col_frag(E *tile, int base, int
     const int s = t >> 1, h = 4 * (t & 1);
     if constexpr (sizeof(E) == 2) {
         E *p = tile + 32 * ks * LD + h + 128 * (s >> 2);
-        return transposed(at_byte(p, base ^ (64 * (s & 3))), at_byte(p + 4 * LD, base ^ (64 * (s & 3) + 16)));
+        return transposed(at_byte(p, base ^ (64 * (s & 3))), at_byte(p + 4 * LD, base ^ (64 * (s & 3) + 32)));
     } else {
         f32x8 x;
 #pragma unroll
@@ -271,7 +273,7 @@ template <typename E>
 __device__ __forceinline__ typename Ops<E>::frag val_frag(E *tile, int base, int ks) {
     if constexpr (sizeof(E) == 2) {
         E *p = tile + 32 * ks * kVT;
-        return transposed(at_byte(p, base), at_byte(p + 4 * kVT, base ^ 16));
+        return transposed(at_byte(p, base), at_byte(p + 4 * kVT, base ^ 32));
     } else {
         f32x8 x;
 #pragma unroll
@@ -471,6 +473,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const int p0 = v0 + 16 * wave + 4 * lg;  // the 4 values of this lane's outputs
     const unsigned oes = ES == 4 || a.o32 ? 4 : 2, ost = (unsigned)(a.H * a.vd) * oes;
     const int64_t ofirst = (bi * a.L * a.H + h) * (int64_t)a.vd;
+    const auto row_of = [&](int i, int nt) { return rv ? nt - 1 - i : i; };
+    const unsigned oo = (unsigned)row_of(lr, C) * ost + p0 * oes;
     double dsum = 0.0;
 
     const int64_t nc = c_hi > c_lo ? c_hi - c_lo : 0;
@@ -481,6 +485,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         fetch_kv(tokens(c0));
         fetch_qs(tokens(c0));
     }
+    char *op = kSt || kDec ? nullptr : static_cast<char *>(a.o) + ofirst * oes + (nc > 0 ? c0 : 0) * C * (int64_t)ost;
     int nt_of = -1;                          // the tokens that these are for:
     double whole = 1.0, drift = 0.0;         // a^nt, nt a^nt, and the tables wt, wu
     float atn = 0.f;
@@ -660,47 +665,50 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         }
         if (s + 1 < nc) stage_all(tokens(c + way));
         if constexpr (!kSt) {
-            const int rows = a.L - c * C < C ? (int)(a.L - c * C) : C;  // written: zeros behind the length
-            const int64_t obase = ofirst + c * C * (int64_t)(a.H * a.vd);
-            float csum = 0.f;
+            if constexpr (kDec) {
+                float csum = 0.f;
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int i = 16 * it + lr, row = rv && i < nt ? nt - 1 - i : i;
-                if constexpr (kDec) {
+                for (int it = 0; it < IT; ++it) {
+                    const int i = 16 * it + lr;
+                    const int64_t from = ofirst + (c * C + row_of(i, nt)) * (int64_t)(a.H * a.vd) + p0;
                     if (i < nt) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (p0 + r < a.vd)
-                                csum += acc[it][r] * ld_io<ES == 2>(a.dy, obase + (int64_t)row * a.H * a.vd + p0 + r);
+                            if (p0 + r < a.vd) csum += acc[it][r] * ld_io<ES == 2>(a.dy, from + r);
                     }
+                }
+                dsum += (double)csum;
+            } else if (VEC && nt == C) {
+                const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(op, 0, (int)((C - 1) * ost + a.vd * oes), 0x00020000);
+                unsigned to = oo;
+                const unsigned down16 = (rv ? -16u : 16u) * ost;
+                if (p0 >= a.vd) {
+                } else if (oes == 4) {
+#pragma unroll
+                    for (int it = 0; it < IT; ++it, to += down16)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), rsrc, to, 0, 0);
                 } else {
-                    f32x4 x = acc[it];
-                    if (nt < C) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] = i < nt ? x[r] : 0.f;
-                    }
-                    if constexpr (VEC) {
-                        const auto rsrc =
-                            __builtin_amdgcn_make_buffer_rsrc(static_cast<char *>(a.o) + obase * oes, 0,
-                                                              (int)((unsigned)(rows - 1) * ost + a.vd * oes), 0x00020000);
-                        const unsigned to = p0 < a.vd ? (unsigned)row * ost + p0 * oes : kOutside;
-                        if (oes == 4) {
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rsrc, to, 0, 0);
-                        } else {
-                            __builtin_amdgcn_raw_buffer_store_b64(bf16_pack4(x), rsrc, to, 0, 0);
+                    for (int it = 0; it < IT; ++it, to += down16)
+                        __builtin_amdgcn_raw_buffer_store_b64(bf16_pack4(acc[it]), rsrc, to, 0, 0);
+                }
+            } else {
+                const int rows = a.L - c * C < C ? (int)(a.L - c * C) : C;  // written: zeros behind the length
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    const int i = 16 * it + lr, row = i < nt ? row_of(i, nt) : i;
+                    char *to = op + (int64_t)row * ost + p0 * oes;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = i < nt ? acc[it][r] : 0.f;
+                        if (row < rows && p0 + r < a.vd) {
+                            if (oes == 4) reinterpret_cast<float *>(to)[r] = x;
+                            else reinterpret_cast<__bf16 *>(to)[r] = (__bf16)x;
                         }
-                    } else if (row < rows) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (p0 + r < a.vd) {
-                                const int64_t to = obase + (int64_t)row * a.H * a.vd + p0 + r;
-                                if (oes == 4) static_cast<float *>(a.o)[to] = x[r];
-                                else static_cast<__bf16 *>(a.o)[to] = (__bf16)x[r];
-                            }
                     }
                 }
             }
-            if constexpr (kDec) dsum += (double)csum;
+            op += way * (int64_t)C * ost;
         }
     }
 
