@@ -425,21 +425,11 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const auto v_at = [&](int u) { return (vi + VR * u) * kVT + (((vn >> 3) ^ swap_of<E, kVT>(vi + VR * u)) << 3); };
     // The next chunk's tensors are loaded while this one is computed. Two states of 256 keys, and
     // loads by single elements of 128, leave no registers for that: there each piece is loaded and staged by itself.
-    constexpr bool kAhead = KD == 256 ? !kDec : VEC || KD != 128 || MODE != kOut || ES == 4;
+    constexpr bool kAhead = KD == 256 ? !kDec : VEC || KD != 128 || ES == 4;
     const auto advance = [&](int64_t chunks) {
         kp += chunks * C * (int64_t)kst;
         vp += chunks * C * (int64_t)vst;
         if (!kSt) qp += chunks * C * (int64_t)qst;
-    };
-    const auto fetch_kv = [&](int nt) {
-#pragma unroll
-        for (int u = 0; u < KN; ++u) fetch_k(nt, u);
-#pragma unroll
-        for (int u = 0; u < VN; ++u) fetch_v(nt, u);
-    };
-    const auto fetch_qs = [&](int nt) {
-#pragma unroll
-        for (int u = 0; u < QN; ++u) fetch_q(nt, u);
     };
     const auto stage = [&](int nt) {
 #pragma unroll
@@ -482,8 +472,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const int way = rv ? -1 : 1;
     if (nc > 0) advance(c0);
     if (kAhead && nc > 0) {
-        fetch_kv(tokens(c0));
-        fetch_qs(tokens(c0));
+        const int nt = tokens(c0);
+#pragma unroll
+        for (int u = 0; u < KN; ++u) fetch_k(nt, u);
+#pragma unroll
+        for (int u = 0; u < VN; ++u) fetch_v(nt, u);
+#pragma unroll
+        for (int u = 0; u < QN; ++u) fetch_q(nt, u);
     }
     char *op = kSt || kDec ? nullptr : static_cast<char *>(a.o) + ofirst * oes + (nc > 0 ? c0 : 0) * C * (int64_t)ost;
     int nt_of = -1;                          // the tokens that these are for:
@@ -507,21 +502,25 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         const int64_t c = c0 + way * s;
         const int nt = tokens(c);
         __syncthreads();  // the chunk's tiles are there, the last one's scores have been read
-        if (s + 1 < nc) {
-            advance(way);
-            if (kAhead) fetch_kv(tokens(c + way));
+        const bool more = s + 1 < nc;
+        const int nt_next = more ? tokens(c + way) : 0;
+        advance(way);  // (behind the last chunk nothing is valid, and nothing read)
+        if (kSt && kAhead) {
+#pragma unroll
+            for (int u = 0; u < KN; ++u) fetch_k(nt_next, u);
         }
         const int qb = opaque(qb0), ab = opaque(ab0), cb = opaque(cb0), vb = opaque(vb0);
         frag vf[JS];
+        const auto read_v = [&]() {
 #pragma unroll
-        for (int ks = 0; ks < JS; ++ks)
-            vf[ks] = val_frag<E>(Vs, vb, ks);
-
+            for (int ks = 0; ks < JS; ++ks) vf[ks] = val_frag<E>(Vs, vb, ks);
+        };
         f32x4 acc[IT];
+        if constexpr (kSt) read_v();
         if constexpr (!kSt) {
             // Scores, transposed (rows j, column i = this lane's token of the strip), and the carried
-            // state's part of the outputs (rows are values, column i). The fragments of one are read
-            // while the other is computed.
+            // state's part of the outputs (rows are values, column i). A step's fragments are read, and
+            // pieces of the next chunk's k loaded, while the step before is computed.
             f32x4 sc[JW], ac2[kDec ? IT : 1];
 #pragma unroll
             for (int t = 0; t < JW; ++t) sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -532,21 +531,26 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 for (int it = 0; it < IT; ++it) ac2[it] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
             constexpr int QA = IT == 4 ? 2 : 1;
-            frag qs[QA], kf[JW], qf[IT];
-            const auto read_q = [&](int ks) {
+            frag qs[2][QA], kf[2][JW], qf[2][IT];
+            const auto read = [&](int ks, int b) {
 #pragma unroll
-                for (int it = 0; it < IT; ++it) qf[it] = row_frag<E, KD>(Qs, qb, it, ks);
-            };
-            const auto read_s = [&](int ks) {
-                qs[0] = row_frag<E, KD>(Qs, qb, sa, ks);
-                if constexpr (QA == 2) qs[1] = row_frag<E, KD>(Qs, qb, sc_, ks);
+                for (int it = 0; it < IT; ++it) qf[b][it] = row_frag<E, KD>(Qs, qb, it, ks);
+                qs[b][0] = row_frag<E, KD>(Qs, qb, sa, ks);
+                if constexpr (QA == 2) qs[b][1] = row_frag<E, KD>(Qs, qb, sc_, ks);
 #pragma unroll
-                for (int t = 0; t < JW; ++t) kf[t] = row_frag<E, KD>(Ks, qb, scol(t), ks);
+                for (int t = 0; t < JW; ++t) kf[b][t] = row_frag<E, KD>(Ks, qb, scol(t), ks);
             };
-            read_q(0);
-            read_s(0);
+            if (kAhead) read(0, 0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
+                const int b = kAhead ? ks & 1 : 0;
+                if (!kAhead) read(ks, 0);
+                else if (ks + 1 < KS) read(ks + 1, b ^ 1);
+                if (kAhead) {
+#pragma unroll
+                    for (int u = 0; u < KN; ++u)
+                        if (u % KS == ks) fetch_k(nt_next, u);
+                }
                 __builtin_amdgcn_sched_barrier(0);
                 float x[8];
                 frag sp[NS], up[kDec ? NS : 1];
@@ -559,20 +563,17 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     O::template parts<NS>(x, up);
                 }
 #pragma unroll
+                for (int t = 0; t < JW; ++t) sc[t] = O::mfma(kf[b][t], qs[b][t == 2 ? 1 : 0], sc[t]);
+#pragma unroll
                 for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
                     for (int it = 0; it < IT; ++it) {
-                        acc[it] = O::mfma(sp[n], qf[it], acc[it]);
-                        if constexpr (kDec) ac2[it] = O::mfma(up[n], qf[it], ac2[it]);
+                        acc[it] = O::mfma(sp[n], qf[b][it], acc[it]);
+                        if constexpr (kDec) ac2[it] = O::mfma(up[n], qf[b][it], ac2[it]);
                     }
                 __builtin_amdgcn_sched_barrier(0);
-                if (ks + 1 < KS) read_q(ks + 1);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int t = 0; t < JW; ++t) sc[t] = O::mfma(kf[t], qs[t == 2 ? 1 : 0], sc[t]);
-                __builtin_amdgcn_sched_barrier(0);
-                if (ks + 1 < KS) read_s(ks + 1);
             }
+            read_v();
 #pragma unroll
             for (int t = 0; t < JW; ++t) {
                 const int jb = 2 * scol(t) + (lg >> 1);
@@ -590,8 +591,6 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     else acc[it][r] *= rs[it];
                 }
         }
-
-        if (kAhead && s + 1 < nc) fetch_qs(tokens(c + way));  // (here, where the registers for it are free)
 
         // the state behind the chunk
         {
@@ -624,6 +623,14 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 const int t = TS * (step / JS), ks = step % JS;
                 if (!kAhead) read(step);
                 else if (step + 1 < NSTEP) read(step + 1);
+                if (kAhead) {
+#pragma unroll
+                    for (int u = 0; u < VN; ++u)
+                        if (u % NSTEP == step) fetch_v(nt_next, u);
+#pragma unroll
+                    for (int u = 0; u < QN; ++u)
+                        if (u % NSTEP == step) fetch_q(nt_next, u);
+                }
                 __builtin_amdgcn_sched_barrier(0);
                 if (ks == 0) {
 #pragma unroll
@@ -663,7 +670,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     for (int it = 2 * ks; it < IT; ++it) acc[it] = O::mfma(vf[ks], af[n][it], acc[it]);
             }
         }
-        if (s + 1 < nc) stage_all(tokens(c + way));
+        if (more) stage_all(nt_next);
         if constexpr (!kSt) {
             if constexpr (kDec) {
                 float csum = 0.f;
