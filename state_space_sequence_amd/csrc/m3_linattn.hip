@@ -47,7 +47,7 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kVT = 64;  // value columns of a workgroup
 constexpr int kMaxDim = 256;
-constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxGrid = 0xffffff;  // workgroups along x: 2^32 threads
 
 // kOut: outputs. kState, kStateU: segment states (and their derivatives) only. kDecay: d log_decay
 enum Mode { kOut = 0, kState = 1, kStateU = 2, kDecay = 3 };
@@ -761,9 +761,7 @@ struct ChainArgs {
     bool rev;
 };
 
-__global__ __launch_bounds__(kThreads) void linattn_chain_kernel(const ChainArgs a) {
-    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (e >= a.chains * a.nstate) return;
+__device__ __forceinline__ void chain_element(const ChainArgs &a, int64_t e) {
     const int64_t chain = e / a.nstate, i = e % a.nstate, bi = chain / a.H;
     int64_t len = a.L;
     if (a.lengths) {
@@ -788,6 +786,11 @@ __global__ __launch_bounds__(kThreads) void linattn_chain_kernel(const ChainArgs
         }
         s = p * s + own;
     }
+}
+
+__global__ __launch_bounds__(kThreads) void linattn_chain_kernel(const ChainArgs a) {
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < a.chains * a.nstate; e += (int64_t)gridDim.x * kThreads)
+        chain_element(a, e);
 }
 
 // out[row][g][d] = sum over the heads of group g of part[row][h][d]
@@ -875,7 +878,7 @@ m3_status lin_check(const m3_shape *s, uint32_t flags) {
     if (s->io_dtype != M3_F32 && s->io_dtype != M3_BF16) return M3_ERR_INVALID_ARG;
     if (s->flags & ~flags) return M3_ERR_INVALID_ARG;
     if (s->rank != 1 || s->dstate > kMaxDim || s->headdim > kMaxDim || s->nheads > 65536) return M3_ERR_UNSUPPORTED;
-    if (s->batch > (1LL << 31) || s->seqlen > (1LL << 31) || s->batch * s->nheads > kMaxGrid / 4 ||
+    if (s->batch > (1LL << 31) || s->seqlen > (1LL << 31) || s->batch * s->nheads > kMaxGrid ||
         (s->seqlen > 0 && s->batch > (1LL << 40) / s->seqlen))
         return M3_ERR_UNSUPPORTED;
     return M3_OK;
@@ -885,7 +888,8 @@ m3_status lin_plan(const m3_shape *s, LinPlan *p) {
     const m3_status st = lin_check(s, 0);
     if (st != M3_OK) return st;
     *p = make_lin_plan(*s);
-    if (p->chains * p->nseg > kMaxGrid / 4) return M3_ERR_UNSUPPORTED;
+    // one workgroup a chain, segment and tile of values or keys
+    if (p->chains * p->nseg * tiles(s->headdim > s->dstate ? s->headdim : s->dstate) > kMaxGrid) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
 
@@ -935,8 +939,8 @@ hipError_t chain_states(const Args &a, const LinPlan &p, float *st, float *ut, c
     c.st = st; c.ut = ut; c.init = init; c.log_decay = a.log_decay; c.lengths = a.lengths;
     c.chains = p.chains; c.nstate = (int64_t)a.kd * a.vd; c.L = a.L; c.seg_tokens = p.seg_chunks * p.C;
     c.H = a.H; c.nseg = p.nseg; c.rev = rev;
-    const int64_t n = c.chains * c.nstate, grid = (n + kThreads - 1) / kThreads;
-    if (grid > kMaxGrid) return hipErrorInvalidValue;
+    int64_t grid = (c.chains * c.nstate + kThreads - 1) / kThreads;
+    if (grid > 65536) grid = 65536;
     hipLaunchKernelGGL(linattn_chain_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, c);
     return hipGetLastError();
 }

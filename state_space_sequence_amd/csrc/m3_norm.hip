@@ -1,0 +1,797 @@
+// Group norm with an activation, channels last: forward and gradients (gfx950).
+//
+//   u = (x - mean) r w + b,  r = 1/sqrt(var + eps);  y = act(u), or u act(z) with a gate
+//   du = dy act'(u) | dy act(z);  dz = dy u act'(z);  d = du w
+//   dx = r (d - mean(d) - xh mean(d xh)),  xh = (x - mean) r;  dw = sum du xh;  db = sum du
+// Bound by HBM: x (z, dy) read and y (dx, dz) written once.
+//
+// Tokens by themselves (one position a row): the lanes of a group (L of them, each with 16 bytes of
+// its channels) hold it in registers, so one pass is enough: the variance is taken of
+// the differences to the mean, and the sums go across lanes by DPP moves. A lane keeps
+// its channels from row to row: weights, and the sums for dw and db, stay in registers.
+//
+// Sequences: partial sums of a slice of the positions (a thread keeps its channels), joined in a
+// fixed order by one workgroup a group, then one elementwise pass. Slices' means and
+// squared differences are joined, not raw squares, which would lose the variance of
+// values far from 0. The backward needs the sums of du and du xh of every channel
+// only: the group's means of d and d xh are their products with w.
+#include <math.h>
+
+#include "m3_internal.h"
+#include "m3_norm.h"
+
+namespace m3i {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxGrid = 0xffffff;  // workgroups along x: 2^32 threads
+
+struct NormArgs {
+    const void *x, *z;
+    const float *w, *b;
+    const int *lengths;
+    void *y;
+    const void *dy;  // backward
+    void *dx, *dz;
+    float *dw, *db;
+    int64_t n, S;  // rows, positions
+    int C, G, D;
+    float eps;
+    bool silu;
+    // tokens: rows of a workgroup. sequences: positions of a slice, slices, partial sums a slice
+    int64_t rows_wg, slice;
+    int nslice, pg;
+    float *part;   // partial sums
+    float *stats;  // [n, G, 4]: mean, 1/std, mean of d, mean of d xh
+};
+
+template <bool BF16>
+__device__ __forceinline__ float sigmoid(float x) {
+    // (bf16 outputs: the hardware exponential's error, |x| 2^-24, is far below their rounding)
+    const float e = BF16 ? __builtin_amdgcn_exp2f(-1.4426950408889634f * x) : expf(-x);
+    return __builtin_amdgcn_rcpf(1.f + e);
+}
+template <bool BF16>
+__device__ __forceinline__ float act(float x, bool silu) {
+    return silu ? x * sigmoid<BF16>(x) : x;
+}
+// value and slope
+template <bool BF16>
+__device__ __forceinline__ void act2(float x, bool silu, float &v, float &s) {
+    v = x;
+    s = 1.f;
+    if (silu) {
+        const float g = sigmoid<BF16>(x);
+        v = x * g;
+        s = g * (1.f + x * (1.f - g));
+    }
+}
+
+// V consecutive elements from p + i: one 16-byte access, or (V == 1, or !VEC) single ones, `live` of them
+template <bool BF16, int V, bool VEC>
+__device__ __forceinline__ void load(const void *p, int64_t i, int live, float (&x)[V]) {
+    if constexpr (VEC && V > 1) {
+        u32x4 w = {0, 0, 0, 0};
+        if constexpr (BF16) {
+            if (live > 0) w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        } else {
+            if (live > 0) w = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = e < live ? ld_io<BF16>(p, i + e) : 0.f;
+    }
+}
+
+template <bool BF16, int V, bool VEC>
+__device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V]) {
+    if constexpr (VEC && V > 1) {
+        if (live > 0) {
+            u32x4 w;
+            if constexpr (BF16) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 v = {x[2 * e], x[2 * e + 1]};
+                    w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2));
+                }
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(x[e]);
+                *reinterpret_cast<u32x4 *>(static_cast<float *>(p) + i) = w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < live) {
+                if constexpr (BF16) static_cast<__bf16 *>(p)[i + e] = (__bf16)x[e];
+                else static_cast<float *>(p)[i + e] = x[e];
+            }
+    }
+}
+
+template <int V, bool VEC>
+__device__ __forceinline__ void load_w(const float *p, int64_t i, int live, float none, float (&x)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = p && (VEC ? live > 0 : e < live) ? p[i + e] : none;
+}
+
+// ------------------------------------------------------------------ tokens ---
+// Slots of L lanes, one group each: slots of a pass cover groups blockIdx.y * slots .. or, with
+// fewer groups than slots, several rows. CH pieces of L * V channels a group.
+template <bool BF16, int L, int CH, bool VEC>
+struct Slot {
+    static constexpr int V = BF16 ? 8 : 4, N = kThreads / L;
+    int g, row0, rows;  // group, first row's offset, rows of a pass (0: an idle slot)
+    int live[CH];       // channels of this lane's pieces
+    int c[CH];          // their first channel
+    __device__ __forceinline__ Slot(const NormArgs &a) {
+        const int s = threadIdx.x / L, l = threadIdx.x % L;
+        const int per = a.G < N ? N / a.G : 1;
+        g = a.G < N ? s % a.G : (int)blockIdx.y * N + s;
+        row0 = a.G < N ? s / a.G : 0;
+        rows = per;
+        const bool idle = a.G < N ? row0 >= per : g >= a.G;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int at = (k * L + l) * V, left = a.D - at;
+            live[k] = idle || left <= 0 ? 0 : (left < V ? left : V);
+            c[k] = g * a.D + at;
+        }
+        if (idle) rows = 0;
+    }
+};
+
+template <bool BF16, int L, int CH, bool VEC>
+__device__ __forceinline__ void token_stats(const NormArgs &a, const Slot<BF16, L, CH, VEC> &s,
+                                            const float (&x)[CH][BF16 ? 8 : 4], float &mean, float &r) {
+    constexpr int V = BF16 ? 8 : 4;
+    const float inv = 1.f / (float)a.D;
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) t += x[k][e];
+    mean = group_sum<L>(t) * inv;
+    t = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float d = (VEC ? s.live[k] > 0 : e < s.live[k]) ? x[k][e] - mean : 0.f;
+            t = __builtin_fmaf(d, d, t);
+        }
+    r = 1.f / sqrtf(group_sum<L>(t) * inv + a.eps);
+}
+
+template <bool BF16, int L, int CH, bool VEC, bool GATE>
+__global__ __launch_bounds__(kThreads) void token_fwd_kernel(const NormArgs a) {
+    constexpr int V = BF16 ? 8 : 4;
+    const Slot<BF16, L, CH, VEC> s(a);
+    float w[CH][V], b[CH][V];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        load_w<V, VEC>(a.w, s.c[k], s.live[k], 1.f, w[k]);
+        load_w<V, VEC>(a.b, s.c[k], s.live[k], 0.f, b[k]);
+    }
+    const int64_t first = (int64_t)blockIdx.x * a.rows_wg, end = first + a.rows_wg < a.n ? first + a.rows_wg : a.n;
+    const int step = a.G < s.N ? s.N / a.G : 1;
+    for (int64_t row = first + s.row0; row - s.row0 < end; row += step) {
+        const bool here = s.rows && row < end;
+        float x[CH][V], z[GATE ? CH : 1][V];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int live = here ? s.live[k] : 0;
+            load<BF16, V, VEC>(a.x, row * a.C + s.c[k], live, x[k]);
+            if constexpr (GATE) load<BF16, V, VEC>(a.z, row * a.C + s.c[k], live, z[k]);
+        }
+        float mean, r;
+        token_stats<BF16, L, CH, VEC>(a, s, x, mean, r);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            float y[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float u = __builtin_fmaf((x[k][e] - mean) * r, w[k][e], b[k][e]);
+                if constexpr (GATE) y[e] = u * act<BF16>(z[k][e], a.silu);
+                else y[e] = act<BF16>(u, a.silu);
+            }
+            store<BF16, V, VEC>(a.y, row * a.C + s.c[k], here ? s.live[k] : 0, y);
+        }
+    }
+}
+
+// part: [gridDim.x * rows of a pass][2][C]
+template <bool BF16, int L, int CH, bool VEC, bool GATE>
+__global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
+    constexpr int V = BF16 ? 8 : 4;
+    const Slot<BF16, L, CH, VEC> s(a);
+    float w[CH][V], b[CH][V], dw[CH][V], db[CH][V];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        load_w<V, VEC>(a.w, s.c[k], s.live[k], 1.f, w[k]);
+        load_w<V, VEC>(a.b, s.c[k], s.live[k], 0.f, b[k]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[k][e] = db[k][e] = 0.f;
+    }
+    const float inv = 1.f / (float)a.D;
+    const int64_t first = (int64_t)blockIdx.x * a.rows_wg, end = first + a.rows_wg < a.n ? first + a.rows_wg : a.n;
+    const int step = a.G < s.N ? s.N / a.G : 1;
+    for (int64_t row = first + s.row0; row - s.row0 < end; row += step) {
+        const bool here = s.rows && row < end;
+        float x[CH][V], z[GATE ? CH : 1][V], d[CH][V];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int live = here ? s.live[k] : 0;
+            load<BF16, V, VEC>(a.x, row * a.C + s.c[k], live, x[k]);
+            load<BF16, V, VEC>(a.dy, row * a.C + s.c[k], live, d[k]);
+            if constexpr (GATE) load<BF16, V, VEC>(a.z, row * a.C + s.c[k], live, z[k]);
+        }
+        float mean, r;
+        token_stats<BF16, L, CH, VEC>(a, s, x, mean, r);
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const bool in = here && (VEC ? s.live[k] > 0 : e < s.live[k]);
+                const float xh = (x[k][e] - mean) * r, u = __builtin_fmaf(xh, w[k][e], b[k][e]);
+                float du, v, sl;
+                if constexpr (GATE) {
+                    act2<BF16>(z[k][e], a.silu, v, sl);
+                    z[k][e] = d[k][e] * u * sl;  // dz
+                    du = d[k][e] * v;
+                } else {
+                    act2<BF16>(u, a.silu, v, sl);
+                    du = d[k][e] * sl;
+                }
+                du = in ? du : 0.f;
+                x[k][e] = in ? xh : 0.f;
+                dw[k][e] = __builtin_fmaf(du, x[k][e], dw[k][e]);
+                db[k][e] += du;
+                d[k][e] = du * w[k][e];
+                sa += d[k][e];
+                sb = __builtin_fmaf(d[k][e], x[k][e], sb);
+            }
+        }
+        sa = group_sum<L>(sa) * inv;
+        sb = group_sum<L>(sb) * inv;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int live = here ? s.live[k] : 0;
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[k][e] = r * (d[k][e] - sa - x[k][e] * sb);
+            store<BF16, V, VEC>(a.dx, row * a.C + s.c[k], live, d[k]);
+            if constexpr (GATE) store<BF16, V, VEC>(a.dz, row * a.C + s.c[k], live, z[k]);
+        }
+    }
+    if (s.rows && a.part) {
+        float *p = a.part + ((int64_t)blockIdx.x * s.rows + s.row0) * 2 * a.C;
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (VEC ? s.live[k] > 0 : e < s.live[k]) {
+                    p[s.c[k] + e] = dw[k][e];
+                    p[a.C + s.c[k] + e] = db[k][e];
+                }
+    }
+}
+
+// --------------------------------------------------------------- sequences ---
+// A workgroup has one slice of a row's positions and 256 vectors of V channels, or, with fewer
+// vectors, pg positions at a time.
+template <int V>
+struct Lane {
+    int64_t row, p0, p1;  // row, positions of the slice (those of the length)
+    int c, slice, po, step;
+    bool idle;
+    __device__ __forceinline__ Lane(const NormArgs &a, bool whole) {
+        const int cv = a.C / V;
+        row = blockIdx.x / a.nslice;
+        slice = blockIdx.x % a.nslice;
+        int v;
+        if (a.pg > 1 || cv <= kThreads) {
+            v = threadIdx.x % cv;
+            po = threadIdx.x / cv;
+        } else {
+            v = blockIdx.y * kThreads + threadIdx.x;
+            po = 0;
+        }
+        step = a.pg;
+        idle = v >= cv || po >= a.pg;
+        c = v * V;
+        int64_t len = a.S;
+        if (a.lengths && !whole) {
+            const int64_t l = a.lengths[row];
+            len = l < 0 ? 0 : (l < a.S ? l : a.S);
+        }
+        p0 = slice * a.slice;
+        p1 = p0 + a.slice < len ? p0 + a.slice : len;
+    }
+};
+
+__device__ __forceinline__ int64_t length_of(const NormArgs &a, int64_t row) {
+    if (!a.lengths) return a.S;
+    const int64_t l = a.lengths[row];
+    return l < 0 ? 0 : (l < a.S ? l : a.S);
+}
+
+// mean and squared differences of a thread's values: part [n, nslice, pg, C / V, 2]
+template <bool BF16, int V>
+__global__ __launch_bounds__(kThreads) void seq_stats_kernel(const NormArgs a) {
+    const Lane<V> t(a, false);
+    if (t.idle) return;
+    constexpr int B = 8;  // positions taken together
+    float mean = 0.f, m2 = 0.f, n = 0.f;
+    for (int64_t p = t.p0 + t.po; p < t.p1; p += B * t.step) {
+        float x[B][V], s = 0.f, cnt = 0.f;
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int64_t at = p + k * t.step;
+            load<BF16, V, true>(a.x, (t.row * a.S + at) * a.C + t.c, at < t.p1 ? V : 0, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (p + k * t.step < t.p1) cnt += V;
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += x[k][e];
+        }
+        const float m = s / cnt;
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const bool in = p + k * t.step < t.p1;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float d = in ? x[k][e] - m : 0.f;
+                q = __builtin_fmaf(d, d, q);
+            }
+        }
+        const float all = n + cnt, d = m - mean, f = cnt / all;
+        m2 += q + d * d * n * f;
+        mean += d * f;
+        n = all;
+    }
+    const int64_t at = ((int64_t)blockIdx.x * a.pg + t.po) * (a.C / V) + t.c / V;
+    *reinterpret_cast<f32x2 *>(a.part + 2 * at) = f32x2{mean, m2};
+}
+
+__device__ __forceinline__ double wg_sum(double v, double *sums) {
+    __syncthreads();
+    sums[threadIdx.x] = v;
+    __syncthreads();
+    for (int k = kThreads / 2; k > 0; k >>= 1) {
+        if ((int)threadIdx.x < k) sums[threadIdx.x] += sums[threadIdx.x + k];
+        __syncthreads();
+    }
+    return sums[0];
+}
+
+// one workgroup a (row, group): stats <- mean, 1/std
+template <int V>
+__global__ __launch_bounds__(kThreads) void seq_join_kernel(const NormArgs a) {
+    __shared__ double sums[kThreads];
+    const int64_t row = blockIdx.x / a.G;
+    const int g = blockIdx.x % a.G, dv = a.D / V, cv = a.C / V;
+    const int64_t len = length_of(a, row), total = (int64_t)a.nslice * a.pg * dv;
+    const auto count = [&](int64_t i) {  // values of partial i
+        const int64_t sp = i / dv, slice = sp / a.pg, po = sp % a.pg;
+        const int64_t p0 = slice * a.slice, p1 = p0 + a.slice < len ? p0 + a.slice : len;
+        const int64_t n = p1 - p0 - po;
+        return n > 0 ? (double)((n + a.pg - 1) / a.pg * V) : 0.0;
+    };
+    const auto partial = [&](int64_t i) {
+        return *reinterpret_cast<const f32x2 *>(
+            a.part + 2 * ((row * a.nslice * a.pg + i / dv) * cv + g * dv + i % dv));
+    };
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < total; i += kThreads) {
+        const double c = count(i);
+        if (c > 0.0) s += c * (double)partial(i)[0];
+    }
+    const double n = (double)len * a.D, mean = n > 0.0 ? wg_sum(s, sums) / n : 0.0;
+    double q = 0.0;
+    for (int64_t i = threadIdx.x; i < total; i += kThreads) {
+        const double c = count(i);
+        if (c > 0.0) {
+            const f32x2 p = partial(i);
+            const double d = (double)p[0] - mean;
+            q += (double)p[1] + c * d * d;
+        }
+    }
+    const double var = n > 0.0 ? wg_sum(q, sums) / n : 0.0;
+    if (threadIdx.x == 0) {
+        float *o = a.stats + 4 * (int64_t)blockIdx.x;
+        o[0] = (float)mean;
+        o[1] = (float)(1.0 / sqrt(var + (double)a.eps));
+    }
+}
+
+template <bool BF16, int V, bool GATE>
+__global__ __launch_bounds__(kThreads) void seq_fwd_kernel(const NormArgs a) {
+    const Lane<V> t(a, true);
+    if (t.idle) return;
+    const int64_t len = length_of(a, t.row);
+    const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
+    const float mean = st[0], r = st[1];
+    float w[V], b[V];
+    load_w<V, true>(a.w, t.c, V, 1.f, w);
+    load_w<V, true>(a.b, t.c, V, 0.f, b);
+    for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
+        const int64_t at = (t.row * a.S + p) * a.C + t.c;
+        const int live = p < len ? V : 0;
+        float x[V], z[V], y[V];
+        load<BF16, V, true>(a.x, at, live, x);
+        if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float u = __builtin_fmaf((x[e] - mean) * r, w[e], b[e]);
+            if constexpr (GATE) y[e] = u * act<BF16>(z[e], a.silu);
+            else y[e] = act<BF16>(u, a.silu);
+            if (!live) y[e] = 0.f;
+        }
+        store<BF16, V, true>(a.y, at, V, y);
+    }
+}
+
+// du of V values; with a gate z becomes dz, x becomes xh
+template <bool BF16, int V, bool GATE>
+__device__ __forceinline__ void seq_du(const NormArgs &a, float mean, float r, const float (&w)[V], const float (&b)[V],
+                                       float (&x)[V], float (&z)[V], float (&d)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float xh = (x[e] - mean) * r, u = __builtin_fmaf(xh, w[e], b[e]);
+        float v, sl;
+        act2<BF16>(GATE ? z[e] : u, a.silu, v, sl);
+        if constexpr (GATE) z[e] = d[e] * u * sl;
+        d[e] = GATE ? d[e] * v : d[e] * sl;
+        x[e] = xh;
+    }
+}
+
+// sums of du xh and du of every channel: part [n, nslice, pg][2][C]
+template <bool BF16, int V, bool GATE>
+__global__ __launch_bounds__(kThreads) void seq_sums_kernel(const NormArgs a) {
+    const Lane<V> t(a, false);
+    if (t.idle) return;
+    const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
+    const float mean = st[0], r = st[1];
+    float w[V], b[V], dw[V], db[V];
+    load_w<V, true>(a.w, t.c, V, 1.f, w);
+    load_w<V, true>(a.b, t.c, V, 0.f, b);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+    for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
+        const int64_t at = (t.row * a.S + p) * a.C + t.c;
+        float x[V], z[V], d[V];
+        load<BF16, V, true>(a.x, at, V, x);
+        load<BF16, V, true>(a.dy, at, V, d);
+        if constexpr (GATE) load<BF16, V, true>(a.z, at, V, z);
+        seq_du<BF16, V, GATE>(a, mean, r, w, b, x, z, d);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            dw[e] = __builtin_fmaf(d[e], x[e], dw[e]);
+            db[e] += d[e];
+        }
+    }
+    float *o = a.part + ((int64_t)blockIdx.x * a.pg + t.po) * 2 * a.C + t.c;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        o[e] = dw[e];
+        o[a.C + e] = db[e];
+    }
+}
+
+// one workgroup a (row, group): stats <- means of d and d xh
+__global__ __launch_bounds__(kThreads) void seq_join_sums_kernel(const NormArgs a) {
+    __shared__ double sums[kThreads];
+    const int64_t row = blockIdx.x / a.G;
+    const int g = blockIdx.x % a.G;
+    const int64_t len = length_of(a, row), total = (int64_t)a.nslice * a.pg * a.D;
+    double sa = 0.0, sb = 0.0;
+    for (int64_t i = threadIdx.x; i < total; i += kThreads) {
+        const int c = g * a.D + (int)(i % a.D);
+        const float *p = a.part + (row * a.nslice * a.pg + i / a.D) * 2 * a.C + c;
+        const double w = a.w ? a.w[c] : 1.f;
+        sb += w * (double)p[0];
+        sa += w * (double)p[a.C];
+    }
+    const double n = (double)len * a.D, ta = wg_sum(sa, sums), tb = wg_sum(sb, sums);
+    if (threadIdx.x == 0) {
+        float *o = a.stats + 4 * (int64_t)blockIdx.x;
+        o[2] = n > 0.0 ? (float)(ta / n) : 0.f;
+        o[3] = n > 0.0 ? (float)(tb / n) : 0.f;
+    }
+}
+
+template <bool BF16, int V, bool GATE>
+__global__ __launch_bounds__(kThreads) void seq_bwd_kernel(const NormArgs a) {
+    const Lane<V> t(a, true);
+    if (t.idle) return;
+    const int64_t len = length_of(a, t.row);
+    const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
+    const float mean = st[0], r = st[1], ma = st[2], mb = st[3];
+    float w[V], b[V];
+    load_w<V, true>(a.w, t.c, V, 1.f, w);
+    load_w<V, true>(a.b, t.c, V, 0.f, b);
+    for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
+        const int64_t at = (t.row * a.S + p) * a.C + t.c;
+        const int live = p < len ? V : 0;
+        float x[V], z[V], d[V];
+        load<BF16, V, true>(a.x, at, live, x);
+        load<BF16, V, true>(a.dy, at, live, d);
+        if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z);
+        seq_du<BF16, V, GATE>(a, mean, r, w, b, x, z, d);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            d[e] = live ? r * (d[e] * w[e] - ma - x[e] * mb) : 0.f;
+            if constexpr (GATE) z[e] = live ? z[e] : 0.f;
+        }
+        store<BF16, V, true>(a.dx, at, V, d);
+        if constexpr (GATE) store<BF16, V, true>(a.dz, at, V, z);
+    }
+}
+
+// dw, db <- sums over the partials [rows][2][C]: 64 of the 2 C columns a workgroup, 4 runs of rows
+__global__ __launch_bounds__(kThreads) void channel_sums_kernel(const float *part, int64_t rows, int C, float *dw,
+                                                                float *db) {
+    __shared__ double sums[kThreads];
+    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+    double s = 0.0;
+    if (i < 2 * (int64_t)C)
+        for (int64_t r = threadIdx.x / 64; r < rows; r += 4) s += (double)part[r * 2 * C + i];
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x < 64 && i < 2 * (int64_t)C) {
+        const double t = (sums[threadIdx.x] + sums[threadIdx.x + 64]) + (sums[threadIdx.x + 128] + sums[threadIdx.x + 192]);
+        if (i < C) {
+            if (dw) dw[i] = (float)t;
+        } else if (db) {
+            db[i - C] = (float)t;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launch ---
+struct NormPlan {
+    bool token;
+    int L, CH;            // tokens
+    int64_t rows_wg, gx;  // tokens: rows of a workgroup, workgroups along the rows
+    int gy, pass;         // tokens: workgroups along the groups, rows of a pass
+    int64_t slice;        // sequences
+    int nslice, pg, vblocks, V;
+    size_t part_bytes, stats_bytes;
+};
+
+size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
+    NormPlan p{};
+    const int V = s.io_dtype == M3_BF16 ? 8 : 4;
+    const int64_t C = s.channels, G = s.groups, D = C / G;
+    p.token = s.positions == 1 && !lengths && D <= 4 * 64 * V;
+    if (p.token) {
+        const int64_t vecs = ceil_div(D, V);
+        p.L = 1;
+        while (p.L < vecs && p.L < 64) p.L *= 2;
+        p.CH = vecs <= 64 ? 1 : (vecs <= 128 ? 2 : 4);
+        const int slots = kThreads / p.L;
+        p.pass = G < slots ? (int)(slots / G) : 1;
+        p.gy = G < slots ? 1 : (int)ceil_div(G, slots);
+        // Rows of a workgroup: enough passes to pay for the weights (and the partial sums), few
+        // enough that the workgroups fill the 256 CUs several times over
+        int64_t passes = ceil_div(s.rows, (int64_t)p.pass * 4096) * p.gy;
+        const int64_t most = bwd ? 64 : 16;
+        passes = passes < 1 ? 1 : (passes > most ? most : passes);
+        if (bwd && ceil_div(s.rows, p.pass * passes) > 2048) passes = ceil_div(s.rows, (int64_t)p.pass * 2048);
+        if (ceil_div(s.rows, p.pass * passes) > (1 << 20)) passes = ceil_div(s.rows, (int64_t)p.pass << 20);
+        p.rows_wg = p.pass * passes;
+        p.gx = ceil_div(s.rows, p.rows_wg);
+        if (bwd) p.part_bytes = up((size_t)(p.gx * p.pass) * 2 * C * 4);
+        return p;
+    }
+    p.V = D % V == 0 ? V : 1;
+    const int64_t cv = C / p.V;
+    p.pg = cv < kThreads ? (int)(kThreads / cv) : 1;
+    p.vblocks = cv < kThreads ? 1 : (int)ceil_div(cv, kThreads);
+    int64_t n = ceil_div(2048, (s.rows > 0 ? s.rows : 1) * p.vblocks);
+    const int64_t most = ceil_div(s.positions, 8 * p.pg);  // eight positions a thread at least
+    n = n > most ? most : n;
+    n = n < 1 ? 1 : n;
+    p.slice = ceil_div(ceil_div(s.positions, n), p.pg) * p.pg;
+    if (p.slice < 1) p.slice = 1;
+    p.nslice = s.positions > 0 ? (int)ceil_div(s.positions, p.slice) : 1;
+    const size_t parts = (size_t)s.rows * p.nslice * p.pg;
+    p.part_bytes = up(parts * 8 * (bwd ? C : cv));
+    p.stats_bytes = up((size_t)s.rows * G * 16);
+    return p;
+}
+
+bool al16(const void *p) { return (((uintptr_t)p) & 15u) == 0; }
+
+m3_status norm_check(const m3_norm_shape *s) {
+    if (!s) return M3_ERR_INVALID_ARG;
+    if (s->rows < 0 || s->positions < 0 || s->channels < 1 || s->groups < 1 || s->channels % s->groups != 0)
+        return M3_ERR_INVALID_ARG;
+    if (s->io_dtype != M3_F32 && s->io_dtype != M3_BF16) return M3_ERR_INVALID_ARG;
+    if (s->activation != M3_ACT_NONE && s->activation != M3_ACT_SILU) return M3_ERR_INVALID_ARG;
+    if (!(s->eps >= 0.f) || !isfinite(s->eps) || s->flags) return M3_ERR_INVALID_ARG;
+    if (s->channels > (1 << 20) || s->rows > (1LL << 31) || s->positions > (1LL << 40) ||
+        (s->positions > 0 && s->rows > (1LL << 40) / s->positions))
+        return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+// the launches of one plan stay within a grid
+m3_status norm_plan(const m3_norm_shape *s, bool lengths, bool bwd, NormPlan *p) {
+    const m3_status st = norm_check(s);
+    if (st != M3_OK) return st;
+    *p = make_plan(*s, lengths, bwd);
+    const int64_t x = p->token ? p->gx : s->rows * p->nslice;
+    const int64_t y = p->token ? p->gy : p->vblocks;
+    if (x > kMaxGrid || y > 65535 || (!p->token && s->rows > kMaxGrid / s->groups))
+        return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+template <bool BF16, int L, int CH, bool VEC>
+void launch_token(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
+    const dim3 g((unsigned)p.gx, (unsigned)p.gy), t(kThreads);
+    if (bwd) {
+        if (a.z) hipLaunchKernelGGL((token_bwd_kernel<BF16, L, CH, VEC, true>), g, t, 0, s, a);
+        else hipLaunchKernelGGL((token_bwd_kernel<BF16, L, CH, VEC, false>), g, t, 0, s, a);
+    } else {
+        if (a.z) hipLaunchKernelGGL((token_fwd_kernel<BF16, L, CH, VEC, true>), g, t, 0, s, a);
+        else hipLaunchKernelGGL((token_fwd_kernel<BF16, L, CH, VEC, false>), g, t, 0, s, a);
+    }
+}
+
+template <bool BF16, bool VEC>
+hipError_t launch_token_dims(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
+    switch (p.L * p.CH) {
+        case 1: launch_token<BF16, 1, 1, VEC>(a, p, bwd, s); break;
+        case 2: launch_token<BF16, 2, 1, VEC>(a, p, bwd, s); break;
+        case 4: launch_token<BF16, 4, 1, VEC>(a, p, bwd, s); break;
+        case 8: launch_token<BF16, 8, 1, VEC>(a, p, bwd, s); break;
+        case 16: launch_token<BF16, 16, 1, VEC>(a, p, bwd, s); break;
+        case 32: launch_token<BF16, 32, 1, VEC>(a, p, bwd, s); break;
+        case 64: launch_token<BF16, 64, 1, VEC>(a, p, bwd, s); break;
+        case 128: launch_token<BF16, 64, 2, VEC>(a, p, bwd, s); break;
+        case 256: launch_token<BF16, 64, 4, VEC>(a, p, bwd, s); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_tokens(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
+    return a.D % (BF16 ? 8 : 4) == 0 ? launch_token_dims<BF16, true>(a, p, bwd, s)
+                                     : launch_token_dims<BF16, false>(a, p, bwd, s);
+}
+
+hipError_t launch_channel_sums(const NormArgs &a, int64_t rows, hipStream_t s) {
+    if (!a.dw && !a.db) return hipSuccess;
+    hipLaunchKernelGGL(channel_sums_kernel, dim3((unsigned)((2 * (int64_t)a.C + 63) / 64)), dim3(kThreads), 0, s, a.part,
+                       rows, a.C, a.dw, a.db);
+    return hipGetLastError();
+}
+
+template <bool BF16, int V>
+hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
+    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), t(kThreads), j((unsigned)(a.n * a.G));
+    hipError_t e;
+    hipLaunchKernelGGL((seq_stats_kernel<BF16, V>), g, t, 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((seq_join_kernel<V>), j, t, 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (!bwd) {
+        if (a.z) hipLaunchKernelGGL((seq_fwd_kernel<BF16, V, true>), g, t, 0, s, a);
+        else hipLaunchKernelGGL((seq_fwd_kernel<BF16, V, false>), g, t, 0, s, a);
+        return hipGetLastError();
+    }
+    if (a.z) hipLaunchKernelGGL((seq_sums_kernel<BF16, V, true>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((seq_sums_kernel<BF16, V, false>), g, t, 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(seq_join_sums_kernel, j, t, 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.z) hipLaunchKernelGGL((seq_bwd_kernel<BF16, V, true>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((seq_bwd_kernel<BF16, V, false>), g, t, 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    return launch_channel_sums(a, a.n * a.nslice * a.pg, s);
+}
+
+m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, void *workspace, hipStream_t hs) {
+    a.n = s.rows; a.S = s.positions; a.C = (int)s.channels; a.G = (int)s.groups; a.D = a.C / a.G;
+    a.eps = s.eps; a.silu = s.activation == M3_ACT_SILU;
+    a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = p.nslice; a.pg = p.pg;
+    a.part = static_cast<float *>(workspace);
+    a.stats = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.part_bytes);
+    const bool bf16 = s.io_dtype == M3_BF16;
+    hipError_t e = hipSuccess;
+    if (a.n * a.S == 0) {
+        if (bwd) e = launch_channel_sums(a, 0, hs);  // zeros
+    } else if (p.token) {
+        if (bwd && !a.dw && !a.db) a.part = nullptr;
+        e = bf16 ? launch_tokens<true>(a, p, bwd, hs) : launch_tokens<false>(a, p, bwd, hs);
+        if (bwd && e == hipSuccess) e = launch_channel_sums(a, p.gx * p.pass, hs);
+    } else if (bf16) {
+        e = p.V > 1 ? launch_seq<true, 8>(a, p, bwd, hs) : launch_seq<true, 1>(a, p, bwd, hs);
+    } else {
+        e = p.V > 1 ? launch_seq<false, 4>(a, p, bwd, hs) : launch_seq<false, 1>(a, p, bwd, hs);
+    }
+    return e == hipSuccess ? M3_OK : M3_ERR_HIP;
+}
+
+}  // namespace
+}  // namespace m3i
+
+using namespace m3i;
+
+extern "C" {
+
+size_t m3_group_norm_workspace_bytes(const m3_norm_shape *shape, int lengths) {
+    NormPlan p;
+    return norm_plan(shape, lengths != 0, false, &p) == M3_OK ? p.part_bytes + p.stats_bytes : 0;
+}
+
+size_t m3_group_norm_bwd_workspace_bytes(const m3_norm_shape *shape, int lengths) {
+    NormPlan p;
+    return norm_plan(shape, lengths != 0, true, &p) == M3_OK ? p.part_bytes + p.stats_bytes : 0;
+}
+
+m3_status m3_group_norm_fwd(const m3_norm_shape *shape, const m3_norm_io *io, void *workspace, size_t ws_bytes,
+                            void *stream) {
+    m3_status st = norm_check(shape);
+    if (st != M3_OK) return st;
+    if (!io) return M3_ERR_INVALID_ARG;
+    NormPlan p;
+    if ((st = norm_plan(shape, io->lengths != nullptr, false, &p)) != M3_OK) return st;
+    if (shape->rows * shape->positions > 0 && (!io->x || !io->y)) return M3_ERR_INVALID_ARG;
+    const void *ptrs[] = {io->x, io->z, io->weight, io->bias, io->lengths, io->y, workspace};
+    for (const void *q : ptrs)
+        if (!al16(q)) return M3_ERR_MISALIGNED;
+    const size_t need = p.part_bytes + p.stats_bytes;
+    if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    NormArgs a{};
+    a.x = io->x; a.z = io->z; a.w = io->weight; a.b = io->bias; a.lengths = io->lengths; a.y = io->y;
+    return run(*shape, p, a, false, workspace, reinterpret_cast<hipStream_t>(stream));
+}
+
+m3_status m3_group_norm_bwd(const m3_norm_shape *shape, const m3_norm_io *io, const m3_norm_grads *gr, void *workspace,
+                            size_t ws_bytes, void *stream) {
+    m3_status st = norm_check(shape);
+    if (st != M3_OK) return st;
+    if (!io || !gr) return M3_ERR_INVALID_ARG;
+    NormPlan p;
+    if ((st = norm_plan(shape, io->lengths != nullptr, true, &p)) != M3_OK) return st;
+    if (shape->rows * shape->positions > 0 &&
+        (!io->x || !gr->dy || !gr->dx || (io->z == nullptr) != (gr->dz == nullptr)))
+        return M3_ERR_INVALID_ARG;
+    const void *ptrs[] = {io->x, io->z, io->weight, io->bias, io->lengths, gr->dy, gr->dx, gr->dz,
+                          gr->dweight, gr->dbias, workspace};
+    for (const void *q : ptrs)
+        if (!al16(q)) return M3_ERR_MISALIGNED;
+    const size_t need = p.part_bytes + p.stats_bytes;
+    if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    NormArgs a{};
+    a.x = io->x; a.z = io->z; a.w = io->weight; a.b = io->bias; a.lengths = io->lengths;
+    a.dy = gr->dy; a.dx = gr->dx; a.dz = gr->dz; a.dw = gr->dweight; a.db = gr->dbias;
+    return run(*shape, p, a, true, workspace, reinterpret_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

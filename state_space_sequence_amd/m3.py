@@ -68,6 +68,20 @@ class LinattnStepIO(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "log_decay", "h", "y")] + [("scale", ctypes.c_float)]
 
 
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("positions", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class NormIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "z", "weight", "bias", "lengths", "y")]
+
+
+class NormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "dx", "dz", "dweight", "dbias")]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("nsegments", ctypes.c_int32),
                 ("workgroups", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
@@ -130,6 +144,15 @@ def _load():
     lib.m3_linattn_bwd_workspace_bytes.argtypes = [ctypes.POINTER(Shape)]
     lib.m3_linattn_step.restype = ctypes.c_int
     lib.m3_linattn_step.argtypes = [ctypes.POINTER(Shape), ctypes.POINTER(LinattnStepIO), ctypes.c_void_p]
+    for name, struct in (("fwd", None), ("bwd", NormGrads)):
+        f = getattr(lib, "m3_group_norm_" + name)
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.POINTER(NormShape), ctypes.POINTER(NormIO)] + (
+            [ctypes.POINTER(struct)] if struct else []) + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    for name in ("m3_group_norm_workspace_bytes", "m3_group_norm_bwd_workspace_bytes"):
+        f = getattr(lib, name)
+        f.restype = ctypes.c_size_t
+        f.argtypes = [ctypes.POINTER(NormShape), ctypes.c_int]
     return lib
 
 
@@ -697,6 +720,104 @@ def linattn_step(q, k, v, log_decay, h, *, scale=None, y=None, stream=None):
                        float(N ** -0.5 if scale is None else scale))
     _launch(lib.m3_linattn_step, q.device, stream, ctypes.byref(shape), ctypes.byref(io))
     return y
+
+
+# ----------------------------------------- group norm with an activation ---
+M3_ACT = {"none": 0, "silu": 1}
+
+
+def _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths):
+    """Checked shape and specs of a group norm of x [..., C]."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: expected a torch.Tensor")
+    iot = _io_dtype(x)
+    if x.dim() < 2:
+        raise ValueError("x: expected [..., channels] of at least 2 dimensions, got shape %s" % (tuple(x.shape),))
+    if activation not in M3_ACT:
+        raise ValueError("activation must be 'none' or 'silu'")
+    C = x.shape[-1]
+    if isinstance(groups, bool) or not isinstance(groups, int) or groups < 1 or C < 1 or C % groups:
+        raise ValueError("groups: %r does not divide the %d channels" % (groups, C))
+    rows, positions = 1, 1
+    if over == "token":
+        if lengths is not None:
+            raise ValueError("lengths: only with over='sequence' (a token's norm sees no other token)")
+        for n in x.shape[:-1]:
+            rows *= int(n)
+    elif over == "sequence":
+        if x.dim() < 3:
+            raise ValueError("x: expected [batch, ..., channels] with over='sequence', got shape %s" % (tuple(x.shape),))
+        rows = int(x.shape[0])
+        for n in x.shape[1:-1]:
+            positions *= int(n)
+    else:
+        raise ValueError("over must be 'token' or 'sequence'")
+    f32 = torch.float32
+    specs = [("x", x, tuple(x.shape), x.dtype), ("z", z, tuple(x.shape), x.dtype), ("weight", weight, (C,), f32),
+             ("bias", bias, (C,), f32), ("lengths", lengths, (rows,), torch.int32)]
+    return NormShape(rows, positions, C, groups, iot, M3_ACT[activation], eps, 0), specs
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, *, z=None, activation="silu", eps=1e-5, over="token",
+                   lengths=None, y=None, workspace=None, stream=None):
+    """Group norm with an activation, channels last (m3_group_norm_fwd): x [..., C] in
+    `groups` equal groups of channels, y = act(u) with u = (x - mean) / sqrt(var + eps) * weight
+    + bias, or u * act(z) with a gate z. over="token": statistics of each token by itself;
+    over="sequence": x [b, ..., C], statistics over all positions of a row, of the first lengths[i]
+    where lengths [b] int32 is given (y is 0 behind them). weight, bias [C] fp32. Returns y."""
+    shape, specs = _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths)
+    ws = int(lib.m3_group_norm_workspace_bytes(ctypes.byref(shape), lengths is not None))
+    _expect_all(specs + [("y", y, tuple(x.shape), x.dtype),
+                         ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
+                x.get_device())
+    with _owned_by(stream):
+        if y is None:
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if ws and workspace is None:
+            workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
+    io = NormIO(_ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(y))
+    wsb = 0 if workspace is None else workspace.numel()
+    _launch(lib.m3_group_norm_fwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), _ptr(workspace), wsb)
+    return y
+
+
+def group_norm_bwd(x, groups, dy, weight=None, bias=None, *, z=None, activation="silu", eps=1e-5, over="token",
+                   lengths=None, grads=None, workspace=None, stream=None):
+    """Gradients of <dy, y> of group_norm_fwd (m3_group_norm_bwd). Returns a dict: x, and z
+    with a gate, in the dtype of x; weight and bias [C] in fp32 where they were given. grads: such
+    a dict to write into (x, and z with a gate, required)."""
+    shape, specs = _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths)
+    _need("dy", dy)
+    C, f32 = x.shape[-1], torch.float32
+    ws = int(lib.m3_group_norm_bwd_workspace_bytes(ctypes.byref(shape), lengths is not None))
+    _expect_all(specs + [("dy", dy, tuple(x.shape), x.dtype),
+                         ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
+                x.get_device())
+    with _owned_by(stream):
+        if grads is None:
+            grads = {"x": torch.empty_like(x, memory_format=torch.contiguous_format)}
+            if z is not None:
+                grads["z"] = torch.empty_like(grads["x"])
+            if weight is not None:
+                grads["weight"] = torch.empty((C,), dtype=f32, device=x.device)
+            if bias is not None:
+                grads["bias"] = torch.empty((C,), dtype=f32, device=x.device)
+        if ws and workspace is None:
+            workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
+    want = {"x": (tuple(x.shape), x.dtype), "z": (tuple(x.shape), x.dtype), "weight": ((C,), f32), "bias": ((C,), f32)}
+    for name, t in grads.items():
+        if name not in want or (name == "z" and z is None):
+            raise ValueError("grads: unknown entry %r" % name)
+        _expect("grads[%r]" % name, t, want[name][0], want[name][1], x.get_device())
+    _need("grads['x']", grads.get("x"))
+    if z is not None:
+        _need("grads['z']", grads.get("z"))
+    io = NormIO(_ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(lengths), None)
+    gs = NormGrads(_ptr(dy), _ptr(grads["x"]), _ptr(grads.get("z")), _ptr(grads.get("weight")), _ptr(grads.get("bias")))
+    wsb = 0 if workspace is None else workspace.numel()
+    _launch(lib.m3_group_norm_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs),
+            _ptr(workspace), wsb)
+    return grads
 
 
 # ------------------------------------------------------ calibration probes ---
