@@ -43,11 +43,12 @@ struct NormArgs {
     int C, G, D;
     float eps;
     bool silu;
-    // tokens: rows of a workgroup. sequences: positions of a slice, slices, partial sums a slice
+    // tokens: rows of a workgroup. sequences: positions of a slice, slices; vectors of a workgroup,
+    // positions it takes at a time, workgroups that share a group
     int64_t rows_wg, slice;
-    int nslice, pg;
-    float *part;   // partial sums
-    float *stats;  // [n, G, 4]: mean, 1/std, mean of d, mean of d xh
+    int nslice, vb, pg, pieces;
+    float *part, *chan;  // partial sums: of groups, of channels (tokens and sequences)
+    float *stats;        // [n, G, 4]: mean, 1/std, mean of d, mean of d xh
 };
 
 template <bool BF16>
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(kThreads) void token_fwd_kernel(const NormArgs a) {
     }
 }
 
-// part: [gridDim.x * rows of a pass][2][C]
+// chan: [gridDim.x * rows of a pass][2][C]
 template <bool BF16, int L, int CH, bool VEC, bool GATE>
 __global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
     constexpr int V = BF16 ? 8 : 4;
@@ -278,8 +279,8 @@ __global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
             if constexpr (GATE) store<BF16, V, VEC>(a.dz, row * a.C + s.c[k], live, z[k]);
         }
     }
-    if (s.rows && a.part) {
-        float *p = a.part + ((int64_t)blockIdx.x * s.rows + s.row0) * 2 * a.C;
+    if (s.rows && a.chan) {
+        float *p = a.chan + ((int64_t)blockIdx.x * s.rows + s.row0) * 2 * a.C;
 #pragma unroll
         for (int k = 0; k < CH; ++k)
 #pragma unroll
@@ -292,37 +293,112 @@ __global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
 }
 
 // --------------------------------------------------------------- sequences ---
-// A workgroup has one slice of a row's positions and 256 vectors of V channels, or, with fewer
-// vectors, pg positions at a time.
+// A workgroup has one slice of a row's positions and vb vectors of V channels: whole groups (dv vectors
+// each), or a piece of up to 256 vectors of one group. With fewer vectors than threads, pg positions at a time.
 template <int V>
 struct Lane {
     int64_t row, p0, p1;  // row, positions of the slice (those of the length)
-    int c, slice, po, step;
+    int64_t len;
+    int c, po, step;
+    int lv, run;   // this thread's vector in its group's part here, and the vectors of that part
+    int64_t entry; // where the part's partial sums go
     bool idle;
     __device__ __forceinline__ Lane(const NormArgs &a, bool whole) {
-        const int cv = a.C / V;
-        row = blockIdx.x / a.nslice;
-        slice = blockIdx.x % a.nslice;
-        int v;
-        if (a.pg > 1 || cv <= kThreads) {
-            v = threadIdx.x % cv;
-            po = threadIdx.x / cv;
-        } else {
-            v = blockIdx.y * kThreads + threadIdx.x;
-            po = 0;
-        }
+        const int dv = a.D / V, cv = a.C / V, slice = (int)(blockIdx.x % (unsigned)a.nslice);
+        row = blockIdx.x / (unsigned)a.nslice;
+        const int lane = (int)threadIdx.x % a.vb;
+        po = (int)threadIdx.x / a.vb;
         step = a.pg;
-        idle = v >= cv || po >= a.pg;
+        int v, g, piece = 0;
+        if (a.pieces == 1) {
+            v = (int)blockIdx.y * a.vb + lane;
+            g = v / dv;
+            lv = lane % dv;
+            run = dv;
+        } else {
+            g = (int)blockIdx.y / a.pieces;
+            piece = (int)blockIdx.y % a.pieces;
+            lv = lane;
+            v = g * dv + piece * a.vb + lane;
+            run = dv - piece * a.vb < a.vb ? dv - piece * a.vb : a.vb;
+        }
+        idle = v >= cv || po >= a.pg || lv >= run;
         c = v * V;
-        int64_t len = a.S;
-        if (a.lengths && !whole) {
+        entry = ((row * a.G + g) * a.nslice + slice) * a.pieces + piece;
+        len = a.S;
+        if (a.lengths) {
             const int64_t l = a.lengths[row];
             len = l < 0 ? 0 : (l < a.S ? l : a.S);
         }
         p0 = slice * a.slice;
-        p1 = p0 + a.slice < len ? p0 + a.slice : len;
+        const int64_t most = whole ? a.S : len;
+        p1 = p0 + a.slice < most ? p0 + a.slice : most;
+    }
+    // v summed over the threads of this one's group, in a fixed order; every thread of the workgroup takes part
+    __device__ __forceinline__ float sum(const NormArgs &a, float v, float *lds) const {
+        __syncthreads();
+        lds[threadIdx.x] = idle ? 0.f : v;
+        __syncthreads();
+        if (po == 0)
+            for (int k = 1; k < a.pg; ++k) lds[threadIdx.x] += lds[threadIdx.x + k * a.vb];
+        for (int k = kThreads / 2; k > 0; k >>= 1) {
+            __syncthreads();
+            if (po == 0 && !idle && lv < k && lv + k < run) lds[threadIdx.x] += lds[threadIdx.x + k];
+        }
+        __syncthreads();
+        return lds[threadIdx.x % a.vb - (idle ? 0 : lv)];
     }
 };
+
+// values, mean and squared differences of a group's part of a slice: part [n, G, nslice, pieces, 4]
+template <bool BF16, int V>
+__global__ __launch_bounds__(kThreads) void seq_stats_kernel(const NormArgs a) {
+    __shared__ float lds[kThreads];
+    const Lane<V> t(a, false);
+    constexpr int B = 8;  // positions taken together
+    float mean = 0.f, m2 = 0.f, n = 0.f;
+    if (!t.idle)
+        for (int64_t p = t.p0 + t.po; p < t.p1; p += B * t.step) {
+            float x[B][V], s = 0.f, cnt = 0.f;
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int64_t at = p + k * t.step;
+                load<BF16, V, true>(a.x, (t.row * a.S + at) * a.C + t.c, at < t.p1 ? V : 0, x[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (p + k * t.step < t.p1) cnt += V;
+#pragma unroll
+                for (int e = 0; e < V; ++e) s += x[k][e];
+            }
+            const float m = s / cnt;
+            float q = 0.f;
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const bool in = p + k * t.step < t.p1;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = in ? x[k][e] - m : 0.f;
+                    q = __builtin_fmaf(d, d, q);
+                }
+            }
+            const float all = n + cnt, d = m - mean, f = cnt / all;
+            m2 += q + d * d * n * f;
+            mean += d * f;
+            n = all;
+        }
+    // the group's part: its mean as a difference to one thread's, so that nothing is lost far from 0
+    const float all = t.sum(a, n, lds);
+    __syncthreads();
+    lds[threadIdx.x] = mean;
+    __syncthreads();
+    const float ref = lds[(int)threadIdx.x % a.vb - (t.idle ? 0 : t.lv)];
+    const float d = n > 0.f ? mean - ref : 0.f;
+    const float sum_d = t.sum(a, n * d, lds), off = all > 0.f ? sum_d / all : 0.f;
+    const float sq = t.sum(a, n > 0.f ? m2 + n * (d - off) * (d - off) : 0.f, lds);
+    if (!t.idle && t.po == 0 && t.lv == 0)
+        *reinterpret_cast<f32x4 *>(a.part + 4 * t.entry) = f32x4{all, ref + off, sq, 0.f};
+}
 
 __device__ __forceinline__ int64_t length_of(const NormArgs &a, int64_t row) {
     if (!a.lengths) return a.S;
@@ -330,94 +406,34 @@ __device__ __forceinline__ int64_t length_of(const NormArgs &a, int64_t row) {
     return l < 0 ? 0 : (l < a.S ? l : a.S);
 }
 
-// mean and squared differences of a thread's values: part [n, nslice, pg, C / V, 2]
-template <bool BF16, int V>
-__global__ __launch_bounds__(kThreads) void seq_stats_kernel(const NormArgs a) {
-    const Lane<V> t(a, false);
-    if (t.idle) return;
-    constexpr int B = 8;  // positions taken together
-    float mean = 0.f, m2 = 0.f, n = 0.f;
-    for (int64_t p = t.p0 + t.po; p < t.p1; p += B * t.step) {
-        float x[B][V], s = 0.f, cnt = 0.f;
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int64_t at = p + k * t.step;
-            load<BF16, V, true>(a.x, (t.row * a.S + at) * a.C + t.c, at < t.p1 ? V : 0, x[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            if (p + k * t.step < t.p1) cnt += V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) s += x[k][e];
-        }
-        const float m = s / cnt;
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const bool in = p + k * t.step < t.p1;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = in ? x[k][e] - m : 0.f;
-                q = __builtin_fmaf(d, d, q);
-            }
-        }
-        const float all = n + cnt, d = m - mean, f = cnt / all;
-        m2 += q + d * d * n * f;
-        mean += d * f;
-        n = all;
-    }
-    const int64_t at = ((int64_t)blockIdx.x * a.pg + t.po) * (a.C / V) + t.c / V;
-    *reinterpret_cast<f32x2 *>(a.part + 2 * at) = f32x2{mean, m2};
+__device__ __forceinline__ double wave_sum64(double v) {
+    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    return v;
 }
 
-__device__ __forceinline__ double wg_sum(double v, double *sums) {
-    __syncthreads();
-    sums[threadIdx.x] = v;
-    __syncthreads();
-    for (int k = kThreads / 2; k > 0; k >>= 1) {
-        if ((int)threadIdx.x < k) sums[threadIdx.x] += sums[threadIdx.x + k];
-        __syncthreads();
-    }
-    return sums[0];
-}
-
-// one workgroup a (row, group): stats <- mean, 1/std
-template <int V>
+// one wave a (row, group): stats <- mean, 1/std
 __global__ __launch_bounds__(kThreads) void seq_join_kernel(const NormArgs a) {
-    __shared__ double sums[kThreads];
-    const int64_t row = blockIdx.x / a.G;
-    const int g = blockIdx.x % a.G, dv = a.D / V, cv = a.C / V;
-    const int64_t len = length_of(a, row), total = (int64_t)a.nslice * a.pg * dv;
-    const auto count = [&](int64_t i) {  // values of partial i
-        const int64_t sp = i / dv, slice = sp / a.pg, po = sp % a.pg;
-        const int64_t p0 = slice * a.slice, p1 = p0 + a.slice < len ? p0 + a.slice : len;
-        const int64_t n = p1 - p0 - po;
-        return n > 0 ? (double)((n + a.pg - 1) / a.pg * V) : 0.0;
-    };
-    const auto partial = [&](int64_t i) {
-        return *reinterpret_cast<const f32x2 *>(
-            a.part + 2 * ((row * a.nslice * a.pg + i / dv) * cv + g * dv + i % dv));
-    };
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < total; i += kThreads) {
-        const double c = count(i);
-        if (c > 0.0) s += c * (double)partial(i)[0];
+    const int64_t rg = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    if (rg >= a.n * a.G) return;
+    const int lane = threadIdx.x % 64, total = a.nslice * a.pieces;
+    const float *part = a.part + 4 * rg * total;
+    double n = 0.0, s = 0.0, q = 0.0;
+    for (int i = lane; i < total; i += 64) {
+        const f32x4 p = *reinterpret_cast<const f32x4 *>(part + 4 * i);
+        n += (double)p[0];
+        s += (double)p[0] * (double)p[1];
     }
-    const double n = (double)len * a.D, mean = n > 0.0 ? wg_sum(s, sums) / n : 0.0;
-    double q = 0.0;
-    for (int64_t i = threadIdx.x; i < total; i += kThreads) {
-        const double c = count(i);
-        if (c > 0.0) {
-            const f32x2 p = partial(i);
-            const double d = (double)p[0] - mean;
-            q += (double)p[1] + c * d * d;
-        }
+    n = wave_sum64(n);
+    const double mean = n > 0.0 ? wave_sum64(s) / n : 0.0;
+    for (int i = lane; i < total; i += 64) {
+        const f32x4 p = *reinterpret_cast<const f32x4 *>(part + 4 * i);
+        const double d = (double)p[1] - mean;
+        q += (double)p[2] + (double)p[0] * d * d;
     }
-    const double var = n > 0.0 ? wg_sum(q, sums) / n : 0.0;
-    if (threadIdx.x == 0) {
-        float *o = a.stats + 4 * (int64_t)blockIdx.x;
-        o[0] = (float)mean;
-        o[1] = (float)(1.0 / sqrt(var + (double)a.eps));
+    const double var = n > 0.0 ? wave_sum64(q) / n : 0.0;
+    if (lane == 0) {
+        a.stats[4 * rg] = (float)mean;
+        a.stats[4 * rg + 1] = (float)(1.0 / sqrt(var + (double)a.eps));
     }
 }
 
@@ -425,7 +441,6 @@ template <bool BF16, int V, bool GATE>
 __global__ __launch_bounds__(kThreads) void seq_fwd_kernel(const NormArgs a) {
     const Lane<V> t(a, true);
     if (t.idle) return;
-    const int64_t len = length_of(a, t.row);
     const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
     const float mean = st[0], r = st[1];
     float w[V], b[V];
@@ -433,7 +448,7 @@ __global__ __launch_bounds__(kThreads) void seq_fwd_kernel(const NormArgs a) {
     load_w<V, true>(a.b, t.c, V, 0.f, b);
     for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
         const int64_t at = (t.row * a.S + p) * a.C + t.c;
-        const int live = p < len ? V : 0;
+        const int live = p < t.len ? V : 0;
         float x[V], z[V], y[V];
         load<BF16, V, true>(a.x, at, live, x);
         if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z);
@@ -463,58 +478,70 @@ __device__ __forceinline__ void seq_du(const NormArgs &a, float mean, float r, c
     }
 }
 
-// sums of du xh and du of every channel: part [n, nslice, pg][2][C]
+// Sums of du xh and du of every channel, chan [n, nslice, pg][2][C], and of d and d xh of a group's
+// part of a slice, part [n, G, nslice, pieces, 4]
 template <bool BF16, int V, bool GATE>
 __global__ __launch_bounds__(kThreads) void seq_sums_kernel(const NormArgs a) {
+    __shared__ float lds[kThreads];
     const Lane<V> t(a, false);
-    if (t.idle) return;
-    const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
-    const float mean = st[0], r = st[1];
-    float w[V], b[V], dw[V], db[V];
-    load_w<V, true>(a.w, t.c, V, 1.f, w);
-    load_w<V, true>(a.b, t.c, V, 0.f, b);
+    float sa = 0.f, sb = 0.f;
+    if (!t.idle) {
+        const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
+        const float mean = st[0], r = st[1];
+        float w[V], b[V], dw[V], db[V];
+        load_w<V, true>(a.w, t.c, V, 1.f, w);
+        load_w<V, true>(a.b, t.c, V, 0.f, b);
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
-    for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
-        const int64_t at = (t.row * a.S + p) * a.C + t.c;
-        float x[V], z[V], d[V];
-        load<BF16, V, true>(a.x, at, V, x);
-        load<BF16, V, true>(a.dy, at, V, d);
-        if constexpr (GATE) load<BF16, V, true>(a.z, at, V, z);
-        seq_du<BF16, V, GATE>(a, mean, r, w, b, x, z, d);
+        for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+        for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
+            const int64_t at = (t.row * a.S + p) * a.C + t.c;
+            float x[V], z[V], d[V];
+            load<BF16, V, true>(a.x, at, V, x);
+            load<BF16, V, true>(a.dy, at, V, d);
+            if constexpr (GATE) load<BF16, V, true>(a.z, at, V, z);
+            seq_du<BF16, V, GATE>(a, mean, r, w, b, x, z, d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                dw[e] = __builtin_fmaf(d[e], x[e], dw[e]);
+                db[e] += d[e];
+            }
+        }
+        float *o = a.chan ? a.chan + ((int64_t)blockIdx.x * a.pg + t.po) * 2 * a.C + t.c : nullptr;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            dw[e] = __builtin_fmaf(d[e], x[e], dw[e]);
-            db[e] += d[e];
+            if (o) {
+                o[e] = dw[e];
+                o[a.C + e] = db[e];
+            }
+            sa = __builtin_fmaf(w[e], db[e], sa);
+            sb = __builtin_fmaf(w[e], dw[e], sb);
         }
     }
-    float *o = a.part + ((int64_t)blockIdx.x * a.pg + t.po) * 2 * a.C + t.c;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        o[e] = dw[e];
-        o[a.C + e] = db[e];
+    sa = t.sum(a, sa, lds);
+    sb = t.sum(a, sb, lds);
+    if (!t.idle && t.po == 0 && t.lv == 0) {
+        a.part[4 * t.entry] = sa;
+        a.part[4 * t.entry + 1] = sb;
     }
 }
 
-// one workgroup a (row, group): stats <- means of d and d xh
+// one wave a (row, group): stats <- means of d and d xh
 __global__ __launch_bounds__(kThreads) void seq_join_sums_kernel(const NormArgs a) {
-    __shared__ double sums[kThreads];
-    const int64_t row = blockIdx.x / a.G;
-    const int g = blockIdx.x % a.G;
-    const int64_t len = length_of(a, row), total = (int64_t)a.nslice * a.pg * a.D;
+    const int64_t rg = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    if (rg >= a.n * a.G) return;
+    const int lane = threadIdx.x % 64, total = a.nslice * a.pieces;
+    const float *part = a.part + 4 * rg * total;
     double sa = 0.0, sb = 0.0;
-    for (int64_t i = threadIdx.x; i < total; i += kThreads) {
-        const int c = g * a.D + (int)(i % a.D);
-        const float *p = a.part + (row * a.nslice * a.pg + i / a.D) * 2 * a.C + c;
-        const double w = a.w ? a.w[c] : 1.f;
-        sb += w * (double)p[0];
-        sa += w * (double)p[a.C];
+    for (int i = lane; i < total; i += 64) {
+        sa += (double)part[4 * i];
+        sb += (double)part[4 * i + 1];
     }
-    const double n = (double)len * a.D, ta = wg_sum(sa, sums), tb = wg_sum(sb, sums);
-    if (threadIdx.x == 0) {
-        float *o = a.stats + 4 * (int64_t)blockIdx.x;
-        o[2] = n > 0.0 ? (float)(ta / n) : 0.f;
-        o[3] = n > 0.0 ? (float)(tb / n) : 0.f;
+    sa = wave_sum64(sa);
+    sb = wave_sum64(sb);
+    const double n = (double)length_of(a, rg / a.G) * a.D;
+    if (lane == 0) {
+        a.stats[4 * rg + 2] = n > 0.0 ? (float)(sa / n) : 0.f;
+        a.stats[4 * rg + 3] = n > 0.0 ? (float)(sb / n) : 0.f;
     }
 }
 
@@ -522,7 +549,6 @@ template <bool BF16, int V, bool GATE>
 __global__ __launch_bounds__(kThreads) void seq_bwd_kernel(const NormArgs a) {
     const Lane<V> t(a, true);
     if (t.idle) return;
-    const int64_t len = length_of(a, t.row);
     const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
     const float mean = st[0], r = st[1], ma = st[2], mb = st[3];
     float w[V], b[V];
@@ -530,7 +556,7 @@ __global__ __launch_bounds__(kThreads) void seq_bwd_kernel(const NormArgs a) {
     load_w<V, true>(a.b, t.c, V, 0.f, b);
     for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
         const int64_t at = (t.row * a.S + p) * a.C + t.c;
-        const int live = p < len ? V : 0;
+        const int live = p < t.len ? V : 0;
         float x[V], z[V], d[V];
         load<BF16, V, true>(a.x, at, live, x);
         load<BF16, V, true>(a.dy, at, live, d);
@@ -546,22 +572,36 @@ __global__ __launch_bounds__(kThreads) void seq_bwd_kernel(const NormArgs a) {
     }
 }
 
-// dw, db <- sums over the partials [rows][2][C]: 64 of the 2 C columns a workgroup, 4 runs of rows
-__global__ __launch_bounds__(kThreads) void channel_sums_kernel(const float *part, int64_t rows, int C, float *dw,
-                                                                float *db) {
-    __shared__ double sums[kThreads];
-    const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+// dw, db <- sums over the partials [rows][2][C]: 32 of the 2 C columns a workgroup, 32 runs of
+// rows, eight loads of each in flight (with 4 runs and one load this took longer than the
+// gradients themselves: 300 us for 2048 rows of 2 x 2048)
+constexpr int kSumCols = 32, kSumRuns = 32;
+
+__global__ __launch_bounds__(kSumCols * kSumRuns) void channel_sums_kernel(const float *part, int64_t rows, int C,
+                                                                            float *dw, float *db) {
+    __shared__ double sums[kSumRuns][kSumCols];
+    const int col = threadIdx.x % kSumCols, run = threadIdx.x / kSumCols;
+    const int64_t i = (int64_t)blockIdx.x * kSumCols + col, width = 2 * (int64_t)C;
     double s = 0.0;
-    if (i < 2 * (int64_t)C)
-        for (int64_t r = threadIdx.x / 64; r < rows; r += 4) s += (double)part[r * 2 * C + i];
-    sums[threadIdx.x] = s;
+    if (i < width)
+        for (int64_t r = run; r < rows; r += 8 * kSumRuns) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = r + k * kSumRuns < rows ? part[(r + k * kSumRuns) * width + i] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += (double)v[k];
+        }
+    sums[run][col] = s;
     __syncthreads();
-    if (threadIdx.x < 64 && i < 2 * (int64_t)C) {
-        const double t = (sums[threadIdx.x] + sums[threadIdx.x + 64]) + (sums[threadIdx.x + 128] + sums[threadIdx.x + 192]);
+    for (int n = kSumRuns / 2; n > 0; n >>= 1) {
+        if (run < n) sums[run][col] += sums[run + n][col];
+        __syncthreads();
+    }
+    if (run == 0 && i < width) {
         if (i < C) {
-            if (dw) dw[i] = (float)t;
+            if (dw) dw[i] = (float)sums[0][col];
         } else if (db) {
-            db[i - C] = (float)t;
+            db[i - C] = (float)sums[0][col];
         }
     }
 }
@@ -573,8 +613,8 @@ struct NormPlan {
     int64_t rows_wg, gx;  // tokens: rows of a workgroup, workgroups along the rows
     int gy, pass;         // tokens: workgroups along the groups, rows of a pass
     int64_t slice;        // sequences
-    int nslice, pg, vblocks, V;
-    size_t part_bytes, stats_bytes;
+    int nslice, vb, pg, pieces, vblocks, V;
+    size_t part_bytes, chan_bytes, stats_bytes, total;
 };
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
@@ -598,27 +638,39 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
         int64_t passes = ceil_div(s.rows, (int64_t)p.pass * 4096) * p.gy;
         const int64_t most = bwd ? 64 : 16;
         passes = passes < 1 ? 1 : (passes > most ? most : passes);
-        if (bwd && ceil_div(s.rows, p.pass * passes) > 2048) passes = ceil_div(s.rows, (int64_t)p.pass * 2048);
+        // (a partial sum is 8 bytes a channel: at most 512 of them)
+        if (bwd && ceil_div(s.rows, p.pass * passes) > 512) passes = ceil_div(s.rows, (int64_t)p.pass * 512);
         if (ceil_div(s.rows, p.pass * passes) > (1 << 20)) passes = ceil_div(s.rows, (int64_t)p.pass << 20);
         p.rows_wg = p.pass * passes;
         p.gx = ceil_div(s.rows, p.rows_wg);
-        if (bwd) p.part_bytes = up((size_t)(p.gx * p.pass) * 2 * C * 4);
+        if (bwd) p.total = p.chan_bytes = up((size_t)(p.gx * p.pass) * 2 * C * 4);
         return p;
     }
     p.V = D % V == 0 ? V : 1;
-    const int64_t cv = C / p.V;
-    p.pg = cv < kThreads ? (int)(kThreads / cv) : 1;
-    p.vblocks = cv < kThreads ? 1 : (int)ceil_div(cv, kThreads);
+    const int64_t cv = C / p.V, dv = D / p.V;
+    if (dv <= kThreads) {
+        const int64_t whole = kThreads / dv * dv;
+        p.vb = (int)(cv < whole ? cv : whole);
+        p.pieces = 1;
+        p.vblocks = (int)ceil_div(cv, p.vb);
+    } else {
+        p.vb = kThreads;
+        p.pieces = (int)ceil_div(dv, kThreads);
+        p.vblocks = (int)(G * p.pieces);
+    }
+    p.pg = kThreads / p.vb;
+    // slices: eight workgroups a CU, of eight positions a thread at least
     int64_t n = ceil_div(2048, (s.rows > 0 ? s.rows : 1) * p.vblocks);
-    const int64_t most = ceil_div(s.positions, 8 * p.pg);  // eight positions a thread at least
+    const int64_t most = ceil_div(s.positions, 8 * p.pg);
     n = n > most ? most : n;
     n = n < 1 ? 1 : n;
     p.slice = ceil_div(ceil_div(s.positions, n), p.pg) * p.pg;
     if (p.slice < 1) p.slice = 1;
     p.nslice = s.positions > 0 ? (int)ceil_div(s.positions, p.slice) : 1;
-    const size_t parts = (size_t)s.rows * p.nslice * p.pg;
-    p.part_bytes = up(parts * 8 * (bwd ? C : cv));
+    p.part_bytes = up((size_t)s.rows * G * p.nslice * p.pieces * 16);
+    if (bwd) p.chan_bytes = up((size_t)s.rows * p.nslice * p.pg * 8 * C);
     p.stats_bytes = up((size_t)s.rows * G * 16);
+    p.total = p.part_bytes + p.chan_bytes + p.stats_bytes;
     return p;
 }
 
@@ -644,7 +696,7 @@ m3_status norm_plan(const m3_norm_shape *s, bool lengths, bool bwd, NormPlan *p)
     *p = make_plan(*s, lengths, bwd);
     const int64_t x = p->token ? p->gx : s->rows * p->nslice;
     const int64_t y = p->token ? p->gy : p->vblocks;
-    if (x > kMaxGrid || y > 65535 || (!p->token && s->rows > kMaxGrid / s->groups))
+    if (x > kMaxGrid || y > 65535 || (!p->token && s->rows * s->groups > 4 * kMaxGrid))
         return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
@@ -686,18 +738,19 @@ hipError_t launch_tokens(const NormArgs &a, const NormPlan &p, bool bwd, hipStre
 
 hipError_t launch_channel_sums(const NormArgs &a, int64_t rows, hipStream_t s) {
     if (!a.dw && !a.db) return hipSuccess;
-    hipLaunchKernelGGL(channel_sums_kernel, dim3((unsigned)((2 * (int64_t)a.C + 63) / 64)), dim3(kThreads), 0, s, a.part,
+    hipLaunchKernelGGL(channel_sums_kernel, dim3((unsigned)ceil_div(2 * (int64_t)a.C, kSumCols)),
+                       dim3(kSumCols * kSumRuns), 0, s, a.chan,
                        rows, a.C, a.dw, a.db);
     return hipGetLastError();
 }
 
 template <bool BF16, int V>
 hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
-    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), t(kThreads), j((unsigned)(a.n * a.G));
+    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), t(kThreads), j((unsigned)ceil_div(a.n * a.G, kThreads / 64));
     hipError_t e;
     hipLaunchKernelGGL((seq_stats_kernel<BF16, V>), g, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((seq_join_kernel<V>), j, t, 0, s, a);
+    hipLaunchKernelGGL(seq_join_kernel, j, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (!bwd) {
         if (a.z) hipLaunchKernelGGL((seq_fwd_kernel<BF16, V, true>), g, t, 0, s, a);
@@ -718,15 +771,16 @@ hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_
 m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, void *workspace, hipStream_t hs) {
     a.n = s.rows; a.S = s.positions; a.C = (int)s.channels; a.G = (int)s.groups; a.D = a.C / a.G;
     a.eps = s.eps; a.silu = s.activation == M3_ACT_SILU;
-    a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = p.nslice; a.pg = p.pg;
-    a.part = static_cast<float *>(workspace);
-    a.stats = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.part_bytes);
+    a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = p.nslice; a.vb = p.vb; a.pg = p.pg; a.pieces = p.pieces;
+    char *ws = static_cast<char *>(workspace);
+    a.part = reinterpret_cast<float *>(ws);
+    a.stats = reinterpret_cast<float *>(ws + p.part_bytes);
+    a.chan = bwd && (a.dw || a.db) ? reinterpret_cast<float *>(ws + p.part_bytes + p.stats_bytes) : nullptr;
     const bool bf16 = s.io_dtype == M3_BF16;
     hipError_t e = hipSuccess;
     if (a.n * a.S == 0) {
         if (bwd) e = launch_channel_sums(a, 0, hs);  // zeros
     } else if (p.token) {
-        if (bwd && !a.dw && !a.db) a.part = nullptr;
         e = bf16 ? launch_tokens<true>(a, p, bwd, hs) : launch_tokens<false>(a, p, bwd, hs);
         if (bwd && e == hipSuccess) e = launch_channel_sums(a, p.gx * p.pass, hs);
     } else if (bf16) {
@@ -746,12 +800,12 @@ extern "C" {
 
 size_t m3_group_norm_workspace_bytes(const m3_norm_shape *shape, int lengths) {
     NormPlan p;
-    return norm_plan(shape, lengths != 0, false, &p) == M3_OK ? p.part_bytes + p.stats_bytes : 0;
+    return norm_plan(shape, lengths != 0, false, &p) == M3_OK ? p.total : 0;
 }
 
 size_t m3_group_norm_bwd_workspace_bytes(const m3_norm_shape *shape, int lengths) {
     NormPlan p;
-    return norm_plan(shape, lengths != 0, true, &p) == M3_OK ? p.part_bytes + p.stats_bytes : 0;
+    return norm_plan(shape, lengths != 0, true, &p) == M3_OK ? p.total : 0;
 }
 
 m3_status m3_group_norm_fwd(const m3_norm_shape *shape, const m3_norm_io *io, void *workspace, size_t ws_bytes,
@@ -765,7 +819,7 @@ m3_status m3_group_norm_fwd(const m3_norm_shape *shape, const m3_norm_io *io, vo
     const void *ptrs[] = {io->x, io->z, io->weight, io->bias, io->lengths, io->y, workspace};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;
-    const size_t need = p.part_bytes + p.stats_bytes;
+    const size_t need = p.total;
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
     NormArgs a{};
     a.x = io->x; a.z = io->z; a.w = io->weight; a.b = io->bias; a.lengths = io->lengths; a.y = io->y;
@@ -786,7 +840,7 @@ m3_status m3_group_norm_bwd(const m3_norm_shape *shape, const m3_norm_io *io, co
                           gr->dweight, gr->dbias, workspace};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;
-    const size_t need = p.part_bytes + p.stats_bytes;
+    const size_t need = p.total;
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
     NormArgs a{};
     a.x = io->x; a.z = io->z; a.w = io->weight; a.b = io->bias; a.lengths = io->lengths;
