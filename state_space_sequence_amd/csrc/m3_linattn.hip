@@ -467,8 +467,10 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const unsigned oo = (unsigned)row_of(lr, C) * ost + p0 * oes;
     double dsum = 0.0;
 
-    const int64_t nc = c_hi > c_lo ? c_hi - c_lo : 0;
-    const int64_t c0 = rv ? c_hi - 1 : c_lo;
+    // chunks that hold tokens; what lies behind the length is only filled with zeros
+    const int64_t c_live = (len + C - 1) / C, c_end = c_hi < c_live ? c_hi : c_live;
+    const int64_t nc = c_end > c_lo ? c_end - c_lo : 0;
+    const int64_t c0 = rv ? c_end - 1 : c_lo;
     const int way = rv ? -1 : 1;
     if (nc > 0) advance(c0);
     if (kAhead && nc > 0) {
@@ -685,32 +687,47 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                     }
                 }
                 dsum += (double)csum;
-            } else if (VEC && nt == C) {
-                const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(op, 0, (int)((C - 1) * ost + a.vd * oes), 0x00020000);
-                unsigned to = oo;
-                const unsigned down16 = (rv ? -16u : 16u) * ost;
-                if (p0 >= a.vd) {
-                } else if (oes == 4) {
-#pragma unroll
-                    for (int it = 0; it < IT; ++it, to += down16)
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), rsrc, to, 0, 0);
-                } else {
-#pragma unroll
-                    for (int it = 0; it < IT; ++it, to += down16)
-                        __builtin_amdgcn_raw_buffer_store_b64(bf16_pack4(acc[it]), rsrc, to, 0, 0);
-                }
             } else {
                 const int rows = a.L - c * C < C ? (int)(a.L - c * C) : C;  // written: zeros behind the length
+                if constexpr (VEC) {
+                    // (rows behind the last lie outside the buffer, and are dropped)
+                    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                        op, 0, (int)((unsigned)(rows - 1) * ost + (unsigned)(a.vd * oes)), 0x00020000);
+                    unsigned to[IT];
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const int i = 16 * it + lr, row = i < nt ? row_of(i, nt) : i;
-                    char *to = op + (int64_t)row * ost + p0 * oes;
+                    for (int it = 0; it < IT; ++it) to[it] = oo + (rv ? -16u : 16u) * it * ost;
+                    if (nt < C) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = i < nt ? acc[it][r] : 0.f;
-                        if (row < rows && p0 + r < a.vd) {
-                            if (oes == 4) reinterpret_cast<float *>(to)[r] = x;
-                            else reinterpret_cast<__bf16 *>(to)[r] = (__bf16)x;
+                        for (int it = 0; it < IT; ++it) {
+                            const int i = 16 * it + lr;
+                            to[it] = (unsigned)(i < nt ? row_of(i, nt) : i) * ost + (unsigned)(p0 * oes);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[it][r] = i < nt ? acc[it][r] : 0.f;
+                        }
+                    }
+                    if (p0 < a.vd) {
+                        if (oes == 4) {
+#pragma unroll
+                            for (int it = 0; it < IT; ++it)
+                                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), rsrc, to[it], 0, 0);
+                        } else {
+#pragma unroll
+                            for (int it = 0; it < IT; ++it)
+                                __builtin_amdgcn_raw_buffer_store_b64(bf16_pack4(acc[it]), rsrc, to[it], 0, 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) {
+                        const int i = 16 * it + lr, row = i < nt ? row_of(i, nt) : i;
+                        char *to = op + (int64_t)row * ost + p0 * oes;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float x = i < nt ? acc[it][r] : 0.f;
+                            if (row < rows && p0 + r < a.vd) {
+                                if (oes == 4) reinterpret_cast<float *>(to)[r] = x;
+                                else reinterpret_cast<__bf16 *>(to)[r] = (__bf16)x;
+                            }
                         }
                     }
                 }
@@ -719,6 +736,24 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
         }
     }
 
+    if constexpr (MODE == kOut) {
+        const int64_t from = (c_end > c_lo ? c_end : c_lo) * C, to = c_hi * C < a.L ? c_hi * C : a.L;
+        constexpr int PV = VEC ? 8 : 1;  // values of one store
+        for (int64_t e = tid; e < (to - from) * (kVT / PV); e += kThreads) {
+            const int p = v0 + PV * (int)(e % (kVT / PV));
+            char *at = static_cast<char *>(a.o) + (ofirst + (from + e / (kVT / PV)) * (int64_t)(a.H * a.vd) + p) * oes;
+            if (p < a.vd) {
+                if constexpr (VEC) {
+                    *reinterpret_cast<u32x4 *>(at) = u32x4{0, 0, 0, 0};
+                    if (oes == 4) reinterpret_cast<u32x4 *>(at)[1] = u32x4{0, 0, 0, 0};
+                } else if (oes == 4) {
+                    *reinterpret_cast<float *>(at) = 0.f;
+                } else {
+                    *reinterpret_cast<uint16_t *>(at) = 0;
+                }
+            }
+        }
+    }
     if constexpr (kSt) {
         store_state(S, a.s_out, chain * a.nseg + seg);
         if constexpr (kU) store_state(U, a.u_out, chain * a.nseg + seg);

@@ -586,30 +586,56 @@ def _owned_by(stream):
 
 def _launch(fn, device, stream, *args):
     """fn(*args, stream) on the tensors' device, whichever device is current."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device_index != device.index:
-        raise ValueError("stream: on device %d, expected %d (the device of the inputs)" % (s.device_index, device.index))
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, ctypes.c_void_p(s.cuda_stream))
+    index = device.index
+    s = torch.cuda.current_stream(index) if stream is None else stream
+    if s.device_index != index:
+        raise ValueError("stream: on device %d, expected %d (the device of the inputs)" % (s.device_index, index))
+    if index == torch.cuda.current_device():
+        rc = fn(*args, s.cuda_stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, ctypes.c_void_p(s.cuda_stream))
-    _check(rc)
+            rc = fn(*args, s.cuda_stream)
+    if rc != M3_OK:
+        raise M3Error(rc)
+
+
+def _arg(name, t, shape, dtype, device):
+    """The pointer of a tensor of exactly this shape and dtype (or one of a tuple of
+    dtypes) on the device of that index; None for None. The checks of _expect and _ptr in
+    one pass: small calls cost as much on the host as on the GPU."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.get_device() != device:
+        raise ValueError("%s: on device %d, expected %d (the device of the inputs)" % (name, t.get_device(), device))
+    if not t.is_contiguous():
+        raise ValueError("%s: tensors must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _on_gpu(device):
+    if device < 0:
+        raise ValueError("tensors must live on the GPU")
+
+
+def _workspace(workspace, device):
+    """(pointer, bytes) of a caller's workspace, or (None, 0)."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor, got %s" % type(workspace).__name__)
+    return _arg("workspace", workspace, (workspace.numel(),), torch.uint8, device), workspace.numel()
 
 
 def _linattn_dims(q, k, v, ndim):
     """(lead, H, G, N, P) of q [*lead, H, N], k [*lead, G, N], v [*lead, G, P]."""
     qs, _, vs = _dims5("q", q, ndim), _dims5("k", k, ndim), _dims5("v", v, ndim)
-    lead, H, N, G, P = qs[:-2], qs[-2], qs[-1], vs[-2], vs[-1]
-    _io_dtype(q)
-    return lead, H, G, N, P
-
-
-def _linattn_specs(q, k, v, log_decay, h0, lengths, lead, H, G, N, P):
-    io, f32 = q.dtype, torch.float32
-    return [("q", q, lead + (H, N), io), ("k", k, lead + (G, N), io), ("v", v, lead + (G, P), io),
-            ("log_decay", log_decay, (H,), f32), ("h0", h0, (lead[0], H, P, N), f32),
-            ("lengths", lengths, (lead[0],), torch.int32)]
+    return qs[:-2], qs[-2], vs[-2], qs[-1], vs[-1]
 
 
 def linattn_shape(q, v, nsegments=0) -> Shape:
@@ -633,26 +659,29 @@ def linattn_fwd(q, k, v, log_decay, *, scale=None, h0=None, lengths=None, y=None
     h // (H // G)), log_decay [H] fp32 <= 0, h0 [b,H,P,N] fp32, lengths [b] int32: row i has
     lengths[i] tokens, y is 0 behind them and the state is the one after them. scale
     defaults to N ** -0.5. Returns (y [b,L,H,P], h_final [b,H,P,N] fp32 or None)."""
-    lead, H, G, N, P = _linattn_dims(q, k, v, 4)
-    b, L = lead
+    (b, L), H, G, N, P = _linattn_dims(q, k, v, 4)
+    iot, io, f32, dev = _io_dtype(q), q.dtype, torch.float32, q.get_device()
     _need("log_decay", log_decay)
-    _expect_all(_linattn_specs(q, k, v, log_decay, h0, lengths, lead, H, G, N, P)
-                + [("y", y, (b, L, H, P), q.dtype), ("h_final", h_final, (b, H, P, N), torch.float32),
-                   ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
-                q.get_device())
-    shape = linattn_shape(q, v, nsegments)
-    ws = linattn_workspace_bytes(shape)
+    ptrs = LinattnIO(_arg("q", q, (b, L, H, N), io, dev), _arg("k", k, (b, L, G, N), io, dev),
+                     _arg("v", v, (b, L, G, P), io, dev), _arg("log_decay", log_decay, (H,), f32, dev),
+                     _arg("h0", h0, (b, H, P, N), f32, dev), _arg("lengths", lengths, (b,), torch.int32, dev),
+                     _arg("y", y, (b, L, H, P), io, dev), _arg("h_final", h_final, (b, H, P, N), f32, dev),
+                     N ** -0.5 if scale is None else scale)
+    ws, wsb = _workspace(workspace, dev)
+    _on_gpu(dev)
+    shape = make_shape(b, L, H, G, P, N, 1, 1, iot, 0.0, 0, nsegments)
+    need = lib.m3_linattn_workspace_bytes(ctypes.byref(shape))
     with _owned_by(stream):
         if y is None:
-            y = torch.empty((b, L, H, P), dtype=q.dtype, device=q.device)
+            y = torch.empty((b, L, H, P), dtype=io, device=q.device)
+            ptrs.y = y.data_ptr()
         if h_final is None and want_state:
-            h_final = torch.empty((b, H, P, N), dtype=torch.float32, device=q.device)
-        if ws and workspace is None:
-            workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
-    io = LinattnIO(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0), _ptr(lengths), _ptr(y), _ptr(h_final),
-                   float(N ** -0.5 if scale is None else scale))
-    wsb = 0 if workspace is None else workspace.numel()
-    _launch(lib.m3_linattn_fwd, q.device, stream, ctypes.byref(shape), ctypes.byref(io), _ptr(workspace), wsb)
+            h_final = torch.empty((b, H, P, N), dtype=f32, device=q.device)
+            ptrs.h_final = h_final.data_ptr()
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws, wsb = workspace.data_ptr(), need
+    _launch(lib.m3_linattn_fwd, q.device, stream, ctypes.byref(shape), ctypes.byref(ptrs), ws, wsb)
     return y, h_final
 
 
@@ -662,63 +691,59 @@ def linattn_bwd(q, k, v, log_decay, dy, *, scale=None, h0=None, lengths=None, dh
     dict: q, k, v in the dtype of the inputs (k and v summed over the heads that share
     them), log_decay [H] and h0 [b,H,P,N] in fp32 where wanted. grads: such a dict to
     write into; the entries q, k, v are required, the others are the ones wanted."""
-    lead, H, G, N, P = _linattn_dims(q, k, v, 4)
-    b, L = lead
+    (b, L), H, G, N, P = _linattn_dims(q, k, v, 4)
+    iot, io, f32, dev = _io_dtype(q), q.dtype, torch.float32, q.get_device()
     _need("log_decay", log_decay)
     _need("dy", dy)
-    f32 = torch.float32
-    _expect_all(_linattn_specs(q, k, v, log_decay, h0, lengths, lead, H, G, N, P)
-                + [("dy", dy, (b, L, H, P), q.dtype), ("dh_final", dh_final, (b, H, P, N), f32),
-                   ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
-                q.get_device())
-    shape = linattn_shape(q, v, nsegments)
-    dev = q.device
-    ws = linattn_bwd_workspace_bytes(shape)
+    sq, sk, sv, sh = (b, L, H, N), (b, L, G, N), (b, L, G, P), (b, H, P, N)
+    ptrs = LinattnIO(_arg("q", q, sq, io, dev), _arg("k", k, sk, io, dev), _arg("v", v, sv, io, dev),
+                     _arg("log_decay", log_decay, (H,), f32, dev), _arg("h0", h0, sh, f32, dev),
+                     _arg("lengths", lengths, (b,), torch.int32, dev), None, None, N ** -0.5 if scale is None else scale)
+    gs = LinattnGrads(_arg("dy", dy, (b, L, H, P), io, dev), _arg("dh_final", dh_final, sh, f32, dev))
+    ws, wsb = _workspace(workspace, dev)
+    shape = make_shape(b, L, H, G, P, N, 1, 1, iot, 0.0, 0, nsegments)
+    need = lib.m3_linattn_bwd_workspace_bytes(ctypes.byref(shape))
     with _owned_by(stream):
         if grads is None:
-            grads = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v)}
+            empty = lambda s, t: torch.empty(s, dtype=t, device=q.device)  # noqa: E731
+            grads = {"q": empty(sq, io), "k": empty(sk, io), "v": empty(sv, io)}
             if want_dlog_decay:
-                grads["log_decay"] = torch.empty((H,), dtype=f32, device=dev)
+                grads["log_decay"] = empty((H,), f32)
             if want_dh0:
-                grads["h0"] = torch.empty((b, H, P, N), dtype=f32, device=dev)
-        if workspace is None and ws:
-            workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
-    want = {"q": (q.shape, q.dtype), "k": (k.shape, q.dtype), "v": (v.shape, q.dtype), "log_decay": ((H,), f32),
-            "h0": ((b, H, P, N), f32)}
+                grads["h0"] = empty(sh, f32)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws, wsb = workspace.data_ptr(), need
+    want = {"q": (sq, io), "k": (sk, io), "v": (sv, io), "log_decay": ((H,), f32), "h0": (sh, f32)}
     for name, t in grads.items():
         if name not in want:
             raise ValueError("grads: unknown entry %r" % name)
-        _expect("grads[%r]" % name, t, tuple(want[name][0]), want[name][1], q.get_device())
+        setattr(gs, "d" + name, _arg("grads[%r]" % name, t, *want[name], dev))
     for name in "qkv":
         _need("grads[%r]" % name, grads.get(name))
-    io = LinattnIO(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0), _ptr(lengths), None, None,
-                   float(N ** -0.5 if scale is None else scale))
-    gs = LinattnGrads(_ptr(dy), _ptr(dh_final), _ptr(grads["q"]), _ptr(grads["k"]), _ptr(grads["v"]),
-                      _ptr(grads.get("log_decay")), _ptr(grads.get("h0")))
-    wsb = 0 if workspace is None else workspace.numel()
-    _launch(lib.m3_linattn_bwd, dev, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs), _ptr(workspace),
-            wsb)
+    _on_gpu(dev)
+    _launch(lib.m3_linattn_bwd, q.device, stream, ctypes.byref(shape), ctypes.byref(ptrs), ctypes.byref(gs), ws, wsb)
     return grads
 
 
 def linattn_step(q, k, v, log_decay, h, *, scale=None, y=None, stream=None):
     """One token of linattn_fwd (m3_linattn_step): q [b,H,N], k [b,G,N], v [b,G,P], the state
     h [b,H,P,N] (fp32 or bf16) updated in place. Returns y [b,H,P]."""
-    lead, H, G, N, P = _linattn_dims(q, k, v, 3)
-    b = lead[0]
+    (b,), H, G, N, P = _linattn_dims(q, k, v, 3)
+    iot, io, dev = _io_dtype(q), q.dtype, q.get_device()
     _need("log_decay", log_decay)
     _need("h", h)
-    _expect_all(_linattn_specs(q, k, v, log_decay, None, None, lead, H, G, N, P)
-                + [("h", h, (b, H, P, N), (torch.float32, torch.bfloat16)), ("y", y, (b, H, P), q.dtype)],
-                q.get_device())
-    shape = make_shape(b, 1, H, G, P, N, 1, 1, _io_dtype(q), 0.0,
-                       M3_FLAG_BF16_STATE if h.dtype == torch.bfloat16 else 0)
+    ptrs = LinattnStepIO(_arg("q", q, (b, H, N), io, dev), _arg("k", k, (b, G, N), io, dev),
+                         _arg("v", v, (b, G, P), io, dev), _arg("log_decay", log_decay, (H,), torch.float32, dev),
+                         _arg("h", h, (b, H, P, N), (torch.float32, torch.bfloat16), dev),
+                         _arg("y", y, (b, H, P), io, dev), N ** -0.5 if scale is None else scale)
+    _on_gpu(dev)
+    shape = make_shape(b, 1, H, G, P, N, 1, 1, iot, 0.0, M3_FLAG_BF16_STATE if h.dtype is torch.bfloat16 else 0)
     if y is None:
         with _owned_by(stream):
-            y = torch.empty((b, H, P), dtype=q.dtype, device=q.device)
-    io = LinattnStepIO(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h), _ptr(y),
-                       float(N ** -0.5 if scale is None else scale))
-    _launch(lib.m3_linattn_step, q.device, stream, ctypes.byref(shape), ctypes.byref(io))
+            y = torch.empty((b, H, P), dtype=io, device=q.device)
+        ptrs.y = y.data_ptr()
+    _launch(lib.m3_linattn_step, q.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
     return y
 
 
@@ -727,7 +752,7 @@ M3_ACT = {"none": 0, "silu": 1}
 
 
 def _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths):
-    """Checked shape and specs of a group norm of x [..., C]."""
+    """The shape and the inputs of a group norm of x [..., C], checked."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x: expected a torch.Tensor")
     iot = _io_dtype(x)
@@ -752,10 +777,10 @@ def _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths):
             positions *= int(n)
     else:
         raise ValueError("over must be 'token' or 'sequence'")
-    f32 = torch.float32
-    specs = [("x", x, tuple(x.shape), x.dtype), ("z", z, tuple(x.shape), x.dtype), ("weight", weight, (C,), f32),
-             ("bias", bias, (C,), f32), ("lengths", lengths, (rows,), torch.int32)]
-    return NormShape(rows, positions, C, groups, iot, M3_ACT[activation], eps, 0), specs
+    f32, dev, s = torch.float32, x.get_device(), x.shape
+    io = NormIO(_arg("x", x, s, x.dtype, dev), _arg("z", z, s, x.dtype, dev), _arg("weight", weight, (C,), f32, dev),
+                _arg("bias", bias, (C,), f32, dev), _arg("lengths", lengths, (rows,), torch.int32, dev))
+    return NormShape(rows, positions, C, groups, iot, M3_ACT[activation], eps, 0), io
 
 
 def group_norm_fwd(x, groups, weight=None, bias=None, *, z=None, activation="silu", eps=1e-5, over="token",
@@ -765,19 +790,20 @@ def group_norm_fwd(x, groups, weight=None, bias=None, *, z=None, activation="sil
     + bias, or u * act(z) with a gate z. over="token": statistics of each token by itself;
     over="sequence": x [b, ..., C], statistics over all positions of a row, of the first lengths[i]
     where lengths [b] int32 is given (y is 0 behind them). weight, bias [C] fp32. Returns y."""
-    shape, specs = _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths)
-    ws = int(lib.m3_group_norm_workspace_bytes(ctypes.byref(shape), lengths is not None))
-    _expect_all(specs + [("y", y, tuple(x.shape), x.dtype),
-                         ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
-                x.get_device())
+    shape, io = _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths)
+    dev = x.get_device()
+    io.y = _arg("y", y, x.shape, x.dtype, dev)
+    ws, wsb = _workspace(workspace, dev)
+    _on_gpu(dev)
+    need = lib.m3_group_norm_workspace_bytes(ctypes.byref(shape), lengths is not None)
     with _owned_by(stream):
         if y is None:
-            y = torch.empty_like(x, memory_format=torch.contiguous_format)
-        if ws and workspace is None:
-            workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
-    io = NormIO(_ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(y))
-    wsb = 0 if workspace is None else workspace.numel()
-    _launch(lib.m3_group_norm_fwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), _ptr(workspace), wsb)
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            io.y = y.data_ptr()
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws, wsb = workspace.data_ptr(), need
+    _launch(lib.m3_group_norm_fwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ws, wsb)
     return y
 
 
@@ -786,37 +812,35 @@ def group_norm_bwd(x, groups, dy, weight=None, bias=None, *, z=None, activation=
     """Gradients of <dy, y> of group_norm_fwd (m3_group_norm_bwd). Returns a dict: x, and z
     with a gate, in the dtype of x; weight and bias [C] in fp32 where they were given. grads: such
     a dict to write into (x, and z with a gate, required)."""
-    shape, specs = _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths)
+    shape, io = _norm_call(x, groups, weight, bias, z, activation, eps, over, lengths)
     _need("dy", dy)
-    C, f32 = x.shape[-1], torch.float32
-    ws = int(lib.m3_group_norm_bwd_workspace_bytes(ctypes.byref(shape), lengths is not None))
-    _expect_all(specs + [("dy", dy, tuple(x.shape), x.dtype),
-                         ("workspace", workspace, (None if workspace is None else workspace.numel(),), torch.uint8)],
-                x.get_device())
+    C, f32, dev = x.shape[-1], torch.float32, x.get_device()
+    gs = NormGrads(_arg("dy", dy, x.shape, x.dtype, dev))
+    ws, wsb = _workspace(workspace, dev)
+    need = lib.m3_group_norm_bwd_workspace_bytes(ctypes.byref(shape), lengths is not None)
     with _owned_by(stream):
         if grads is None:
-            grads = {"x": torch.empty_like(x, memory_format=torch.contiguous_format)}
+            empty = lambda s, t: torch.empty(s, dtype=t, device=x.device)  # noqa: E731
+            grads = {"x": empty(x.shape, x.dtype)}
             if z is not None:
-                grads["z"] = torch.empty_like(grads["x"])
+                grads["z"] = empty(x.shape, x.dtype)
             if weight is not None:
-                grads["weight"] = torch.empty((C,), dtype=f32, device=x.device)
+                grads["weight"] = empty((C,), f32)
             if bias is not None:
-                grads["bias"] = torch.empty((C,), dtype=f32, device=x.device)
-        if ws and workspace is None:
-            workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
-    want = {"x": (tuple(x.shape), x.dtype), "z": (tuple(x.shape), x.dtype), "weight": ((C,), f32), "bias": ((C,), f32)}
+                grads["bias"] = empty((C,), f32)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws, wsb = workspace.data_ptr(), need
+    want = {"x": (x.shape, x.dtype), "z": (x.shape, x.dtype), "weight": ((C,), f32), "bias": ((C,), f32)}
     for name, t in grads.items():
         if name not in want or (name == "z" and z is None):
             raise ValueError("grads: unknown entry %r" % name)
-        _expect("grads[%r]" % name, t, want[name][0], want[name][1], x.get_device())
+        setattr(gs, "d" + name, _arg("grads[%r]" % name, t, *want[name], dev))
     _need("grads['x']", grads.get("x"))
     if z is not None:
         _need("grads['z']", grads.get("z"))
-    io = NormIO(_ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(lengths), None)
-    gs = NormGrads(_ptr(dy), _ptr(grads["x"]), _ptr(grads.get("z")), _ptr(grads.get("weight")), _ptr(grads.get("bias")))
-    wsb = 0 if workspace is None else workspace.numel()
-    _launch(lib.m3_group_norm_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs),
-            _ptr(workspace), wsb)
+    _on_gpu(dev)
+    _launch(lib.m3_group_norm_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs), ws, wsb)
     return grads
 
 
