@@ -15,10 +15,11 @@
 //   dk: backwards, (q, k, v) = (v, dy, q), the state transposed
 //   dv: backwards, (q, k, v) = (k, q, dy)
 // and d log_decay is sum_t scale dy_t . (U_t^T q_t) with U = dS / d log_decay,
-// U_t = a (U_{t-1} + S_{t-1}), carried the same way by a forward pass that forms
-// out with the weights n a^n in place of a^n and takes its product with dy: every
-// weight stays local to its chunk, where sums of t (q.dq - k.dk) over a whole
-// sequence would cancel.
+// U_t = a (U_{t-1} + S_{t-1}), carried the same way by a forward pass of its own. Per chunk that is
+//   sum_{j<i} (i - j) a^{i-j} (q_i . k_j)(dy_i . v_j) + <S, sum_i (i+1) a^{i+1} q_i dy_i^T> + <U, sum_i a^{i+1} q_i dy_i^T>
+// whose first products are exact, and whose states enter in fp32: no operand but the weighted
+// dy is split. Every weight stays local to its chunk, where sums of t (q.dq - k.dk)
+// over a whole sequence would cancel.
 //
 // A workgroup of 4 waves owns one chain (batch, head), 64 of its values (columns of S) and one
 // segment of the tokens. Wave w owns 16 columns: its part of S never leaves its
@@ -69,11 +70,12 @@ struct Args {
     float *s_out;        // kOut: [chains], the state after the last segment, or NULL. kState: [chains, nseg]
     float *u_out;        // kState: [chains, nseg] or NULL
     bool seg_in;
-    const void *dy;         // kDecay: [b, L, H, vd]
+    Tensor dy;              // kDecay
     const float *dh_final;  // kDecay: [chains] or NULL
-    double *part;           // kDecay: [H, b * nseg * nvt]
+    double *part;           // kDecay: [H, b * nseg * nvt * nkt]
     int64_t b, L, nchunks, seg_chunks;
     int H, kd, vd, nseg, nvt;
+    int nkt;  // kDecay: tiles of 64 keys, a workgroup each (d log_decay is a sum over keys and values); else 1
     int sk, sv;  // strides of a key and a value in a stored state
     float si, sr, su;
 };
@@ -92,7 +94,6 @@ struct Ops<uint16_t> {
     static constexpr int NS = 2;   // parts of a state operand
     static constexpr int NA = 2;   // parts of a score
     static constexpr int NW = 3;   // parts of a weighted value, whose sums are stored in fp32
-    static constexpr int NU = 3;   // parts of a state operand of d log_decay, an fp32 output
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -134,7 +135,7 @@ template <>
 struct Ops<float> {
     typedef f32x8 frag;
     typedef f32x8 pack;
-    static constexpr int C = 32, NS = 1, NA = 1, NW = 1, NU = 1;
+    static constexpr int C = 32, NS = 1, NA = 1, NW = 1;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
@@ -307,24 +308,46 @@ __device__ __forceinline__ float uniform(float x) {
     return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
 
+__device__ __forceinline__ double uniform64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
+// the passes of one launch (of the same key tiles): workgroups 0 .. ends[0] - 1 run the first, and so on
+struct Passes {
+    Args a[3];
+    unsigned ends[3];
+    int n;
+};
+
 template <typename E, int KD, int MODE, bool VEC>
-__global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void linattn_kernel(const Args a) {
+__global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(const Passes passes) {
+    // (each pass in the order of its own: see xcd_order)
+    const int role = MODE != kOut || blockIdx.x < passes.ends[0] ? 0 : (blockIdx.x < passes.ends[1] ? 1 : 2);
+    const unsigned begin = role ? passes.ends[role - 1] : 0u;
+    Args a = passes.a[0];  // (indexed by a variable, the arguments would be copied to memory)
+    if (role == 1) a = passes.a[1];
+    if (role == 2) a = passes.a[2];
     typedef Ops<E> O;
     typedef typename O::frag frag;
     constexpr int C = O::C, KT = KD / 16, KS = KD / 32, JS = C / 32, IT = C / 16, ES = sizeof(E);
     constexpr bool kDec = MODE == kDecay, kSt = MODE == kState || MODE == kStateU, kU = kDec || MODE == kStateU;
-    constexpr int NA = kDec ? O::NU : O::NA, NS = kDec ? O::NU : O::NS;
+    constexpr int NA = O::NA, NS = O::NS;
     __shared__ __align__(16) E Qs[kSt ? 8 : C * KD];
     __shared__ __align__(16) E Ks[C * KD];
     __shared__ __align__(16) E Vs[C * kVT];
-    __shared__ __align__(16) E As[kSt ? 8 : NA * C * C];
-    __shared__ __align__(16) float wt[C], wu[kU ? C : 1];
+    __shared__ __align__(16) E As[MODE != kOut ? 8 : NA * C * C];
+    __shared__ __align__(16) E Ds[kDec ? C * kVT : 8];  // dy
+    __shared__ __align__(16) float wt[C], wu[kU ? C : 1], wd[kDec ? 2 : 1][kDec ? C : 1];
     __shared__ float pw[C + 1];  // a^n
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, lr = lane & 15, lg = lane >> 4;
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int vt = (int)(id % (unsigned)a.nvt);
-    const unsigned rest = id / (unsigned)a.nvt, chains = (unsigned)a.b * (unsigned)a.H;
+    const unsigned id = xcd_order(blockIdx.x - begin, passes.ends[role] - begin);
+    const unsigned tile = id % (unsigned)(a.nvt * a.nkt), rest = id / (unsigned)(a.nvt * a.nkt);
+    const int vt = (int)tile / a.nkt, k0 = kDec ? (int)tile % a.nkt * KD : 0;  // the first key
+    const int kdim = a.kd - k0;
+    const unsigned chains = (unsigned)a.b * (unsigned)a.H;
     const int64_t chain = rest % chains;
     const int seg = (int)(rest / chains);
     const int64_t bi = (unsigned)chain / (unsigned)a.H;
@@ -342,28 +365,52 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 
     // the state: keys key_of(t, lg, r) of column col
     f32x4 S[KT], U[kU ? KT : 1];
-    const auto load_state = [&](f32x4 *to, const float *from) {
-        const float *p = from ? from + (a.seg_in ? chain * a.nseg + seg : chain) * nstate : nullptr;
+    // (a stored state has up to 2^16 values: byte offsets from its first, and the buffer's bounds check for
+    // keys and values that do not exist)
+    const bool wide = a.sk == 1 && a.kd % 4 == 0;  // 4 keys at a time
+    const auto state_at = [&](int c, int t, int r) {  // c: col
+        const int n = k0 + key_of(t, lg, r);
+        return n < a.kd && c < a.vd ? (unsigned)(n * a.sk + c * a.sv) * 4u : kOutside;
+    };
+    const auto state_rows = [&](const float *p, int64_t at) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(p) + at * nstate, 0, (int)(nstate * 4), 0x00020000);
+    };
+    const auto load_state = [&](f32x4 *to, const float *from, int64_t at) {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+        for (int t = 0; t < KT; ++t) to[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (from == nullptr) return;
+        const auto rsrc = state_rows(from, at);
+        const int c = opaque(col);
+        if (wide) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = key_of(t, lg, r);
-                to[t][r] = p && n < a.kd && col < a.vd ? p[n * a.sk + col * a.sv] : 0.f;
-            }
+            for (int t = 0; t < KT; ++t)
+                to[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, state_at(c, t, 0), 0, 0));
+        } else {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    to[t][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, state_at(c, t, r), 0, 0));
+        }
     };
     const auto store_state = [&](const f32x4 *from, float *to, int64_t at) {
-        float *p = to + at * nstate;
+        const auto rsrc = state_rows(to, at);
+        const int c = opaque(col);
+        if (wide) {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+            for (int t = 0; t < KT; ++t)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, from[t]), rsrc, state_at(c, t, 0), 0, 0);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = key_of(t, lg, r);
-                if (n < a.kd && col < a.vd) p[n * a.sk + col * a.sv] = from[t][r];
-            }
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(from[t][r]), rsrc, state_at(c, t, r), 0, 0);
+        }
     };
-    load_state(S, kSt ? nullptr : a.s_in);
-    if constexpr (kU) load_state(U, kSt ? nullptr : a.u_in);
+    const int64_t in_at = a.seg_in ? chain * a.nseg + seg : chain;
+    load_state(S, kSt ? nullptr : a.s_in, in_at);
+    if constexpr (kU) load_state(U, kSt ? nullptr : a.u_in, in_at);
 
     if (tid <= C) pw[tid] = (float)power(ld, tid);
     __syncthreads();
@@ -374,7 +421,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     const int ta = IT == 4 ? (wave == 1 ? 2 : 0) : wave & 1, tc = IT == 4 ? (wave == 0 ? 0 : 4 - wave) : ta;
     const auto srow = [&](int t) { return t == 2 ? sc_ : sa; };
     const auto scol = [&](int t) { return t == 2 ? tc : ta + t; };
-    float mask[kSt ? 1 : JW][4], rs[kSt ? 1 : IT];
+    float mask[kSt ? 1 : JW][4], rs[MODE != kOut ? 1 : IT];
     if constexpr (!kSt) {
 #pragma unroll
         for (int t = 0; t < JW; ++t)
@@ -383,8 +430,16 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 const int n = 16 * srow(t) + lr - 16 * scol(t) - 4 * lg - r;
                 mask[t][r] = n < 0 ? 0.f : a.si * pw[n < 0 ? 0 : n] * (kDec ? (float)n : 1.f);
             }
+        if constexpr (MODE == kOut) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it) rs[it] = a.sr * pw[16 * it + lr + 1 - rv];
+            for (int it = 0; it < IT; ++it) rs[it] = a.sr * pw[16 * it + lr + 1 - rv];
+        }
+    }
+    if constexpr (kDec) {
+        if (tid < C) {
+            wd[0][tid] = a.sr * pw[tid + 1];
+            wd[1][tid] = a.sr * pw[tid + 1] * (float)(tid + 1);
+        }
     }
 
     // Staging: 8 columns of a row a thread. Row i of a chunk is its token i, or nt - 1 - i backwards:
@@ -392,44 +447,49 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     constexpr int KN = C * (KD / 8) / kThreads, VN = C * (kVT / 8) / kThreads, QN = kSt ? 0 : KN;
     static_assert(C * (KD / 8) % kThreads == 0 && C * (kVT / 8) % kThreads == 0, "staging");
     constexpr int KR = kThreads / (KD / 8), VR = kThreads / (kVT / 8);  // rows of one pass
-    typename O::pack kx[KN], vx[VN], qx[QN ? QN : 1];
+    typename O::pack kx[KN], vx[VN], qx[QN ? QN : 1], dx[kDec ? VN : 1];
     const int kn = 8 * (tid % (KD / 8)), ki = tid / (KD / 8), vn = 8 * (tid % (kVT / 8)), vi = tid / (kVT / 8);
     const unsigned kst = (unsigned)(a.k.heads * a.kd * ES), vst = (unsigned)(a.v.heads * a.vd * ES),
-                   qst = kSt ? 0u : (unsigned)(a.q.heads * a.kd * ES);
+                   qst = kSt ? 0u : (unsigned)(a.q.heads * a.kd * ES), dst = kDec ? (unsigned)(a.dy.heads * a.vd * ES) : 0u;
     const auto first = [&](const Tensor &x, int head, int dim, unsigned stride) {
         return static_cast<const char *>(x.p) + bi * a.L * (int64_t)stride + (int64_t)head * dim * ES;
     };
-    const char *kp = first(a.k, h / a.k.per, a.kd, kst), *vp = first(a.v, h / a.v.per, a.vd, vst),
-               *qp = kSt ? nullptr : first(a.q, h / a.q.per, a.kd, qst);
+    const char *kp = first(a.k, h / a.k.per, a.kd, kst) + k0 * ES, *vp = first(a.v, h / a.v.per, a.vd, vst),
+               *qp = kSt ? nullptr : first(a.q, h / a.q.per, a.kd, qst) + k0 * ES,
+               *dp = kDec ? first(a.dy, h / a.dy.per, a.vd, dst) : nullptr;
     const auto offset = [&](int i, unsigned stride, int n, int dim) {
         return n < dim ? (unsigned)(rv ? -1 - i : i) * stride + (unsigned)(n * ES) : kOutside;
     };
-    const unsigned ko = offset(ki, kst, kn, a.kd), vo = offset(vi, vst, v0 + vn, a.vd),
-                   qo = kSt ? 0u : offset(ki, qst, kn, a.kd);
+    const unsigned ko = offset(ki, kst, kn, kdim), vo = offset(vi, vst, v0 + vn, a.vd),
+                   qo = kSt ? 0u : offset(ki, qst, kn, kdim), dof = kDec ? offset(vi, dst, v0 + vn, a.vd) : 0u;
     const auto tokens = [&](int64_t c) { return len - c * C >= C ? C : (len > c * C ? (int)(len - c * C) : 0); };
     const auto span = [&](int nt, unsigned stride, int dim) {
         return nt > 0 ? (unsigned)(nt - 1) * stride + (unsigned)(dim * ES) : 0u;
     };
     const auto down = [&](int nt, int rows, unsigned stride) { return (unsigned)(rv ? nt - rows : rows) * stride; };
     const auto fetch_k = [&](int nt, int u) {
-        kx[u] = load8<E, VEC>(kp, span(nt, kst, a.kd), ko + down(nt, KR * u, kst), a.kd - kn);
+        kx[u] = load8<E, VEC>(kp, span(nt, kst, kdim), ko + down(nt, KR * u, kst), kdim - kn);
     };
     const auto fetch_v = [&](int nt, int u) {
         vx[u] = load8<E, VEC>(vp, span(nt, vst, a.vd), vo + down(nt, VR * u, vst), a.vd - v0 - vn);
     };
     const auto fetch_q = [&](int nt, int u) {
-        qx[u] = load8<E, VEC>(qp, span(nt, qst, a.kd), qo + down(nt, KR * u, qst), a.kd - kn);
+        qx[u] = load8<E, VEC>(qp, span(nt, qst, kdim), qo + down(nt, KR * u, qst), kdim - kn);
+    };
+    const auto fetch_d = [&](int nt, int u) {
+        if constexpr (kDec) dx[u] = load8<E, VEC>(dp, span(nt, dst, a.vd), dof + down(nt, VR * u, dst), a.vd - v0 - vn);
     };
     const auto put = [&](E *to, const typename O::pack &x) { *reinterpret_cast<typename O::pack *>(to) = x; };
     const auto k_at = [&](int u) { return (ki + KR * u) * KD + (((kn >> 3) ^ swap_of<E, KD>(ki + KR * u)) << 3); };
     const auto v_at = [&](int u) { return (vi + VR * u) * kVT + (((vn >> 3) ^ swap_of<E, kVT>(vi + VR * u)) << 3); };
-    // The next chunk's tensors are loaded while this one is computed. Two states of 256 keys, and
-    // loads by single elements of 128, leave no registers for that: there each piece is loaded and staged by itself.
-    constexpr bool kAhead = KD == 256 ? !kDec : VEC || KD != 128 || ES == 4;
+    // The next chunk's tensors are loaded while this one is computed. Loads by single elements of
+    // 128 keys leave no registers for that: there each piece is loaded and staged by itself.
+    constexpr bool kAhead = VEC || (KD != 128 && !kDec) || ES == 4;
     const auto advance = [&](int64_t chunks) {
         kp += chunks * C * (int64_t)kst;
         vp += chunks * C * (int64_t)vst;
         if (!kSt) qp += chunks * C * (int64_t)qst;
+        if (kDec) dp += chunks * C * (int64_t)dst;
     };
     const auto stage = [&](int nt) {
 #pragma unroll
@@ -447,6 +507,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 __builtin_amdgcn_sched_barrier(0);
             }
             put(Vs + v_at(u), vx[u]);
+            if constexpr (kDec) {
+                if (!kAhead) {
+                    fetch_d(nt, u);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                put(Ds + v_at(u), dx[u]);
+            }
         }
 #pragma unroll
         for (int u = 0; u < QN; ++u) {
@@ -459,7 +526,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     };
 
     const int qb0 = row_base<E, KD>(lr, lg), ab0 = row_base<E, C>(lr, lg), cb0 = col_base<E, KD>(lr, lg),
-              vb0 = val_base<E>(lr, lg, wave);
+              vb0 = val_base<E>(lr, lg, wave), rb0 = row_base<E, kVT>(lr, lg);
     const int p0 = v0 + 16 * wave + 4 * lg;  // the 4 values of this lane's outputs
     const unsigned oes = ES == 4 || a.o32 ? 4 : 2, ost = (unsigned)(a.H * a.vd) * oes;
     const int64_t ofirst = (bi * a.L * a.H + h) * (int64_t)a.vd;
@@ -478,11 +545,16 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
         for (int u = 0; u < KN; ++u) fetch_k(nt, u);
 #pragma unroll
-        for (int u = 0; u < VN; ++u) fetch_v(nt, u);
+        for (int u = 0; u < VN; ++u) {
+            fetch_v(nt, u);
+            fetch_d(nt, u);
+        }
 #pragma unroll
         for (int u = 0; u < QN; ++u) fetch_q(nt, u);
     }
-    char *op = kSt || kDec ? nullptr : static_cast<char *>(a.o) + ofirst * oes + (nc > 0 ? c0 : 0) * C * (int64_t)ost;
+    char *op = MODE != kOut ? nullptr : static_cast<char *>(a.o) + ofirst * oes + (nc > 0 ? c0 : 0) * C * (int64_t)ost;
+    // (formed here: in the loop the constants of exp would take registers of every step)
+    const double p_full = uniform64(power(ld, C)), p_part = uniform64(power(ld, len % C));
     int nt_of = -1;                          // the tokens that these are for:
     double whole = 1.0, drift = 0.0;         // a^nt, nt a^nt, and the tables wt, wu
     float atn = 0.f;
@@ -495,7 +567,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 wt[tid] = tid < nt ? a.su * pw[n] : 0.f;
                 if constexpr (kU) wu[tid] = tid < nt ? a.su * pw[n] * (float)n : 0.f;
             }
-            whole = power(ld, nt);
+            whole = nt == C ? p_full : p_part;
             atn = uniform((float)(whole * (double)nt));
         }
     };
@@ -511,27 +583,89 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
             for (int u = 0; u < KN; ++u) fetch_k(nt_next, u);
         }
-        const int qb = opaque(qb0), ab = opaque(ab0), cb = opaque(cb0), vb = opaque(vb0);
+        const int qb = opaque(qb0), ab = opaque(ab0), cb = opaque(cb0), vb = opaque(vb0), rb = opaque(rb0);
         frag vf[JS];
         const auto read_v = [&]() {
 #pragma unroll
             for (int ks = 0; ks < JS; ++ks) vf[ks] = val_frag<E>(Vs, vb, ks);
         };
-        f32x4 acc[IT];
+        f32x4 acc[MODE == kOut ? IT : 1];
+        float csum = 0.f;
         if constexpr (kSt) read_v();
-        if constexpr (!kSt) {
+        if constexpr (kDec) {
+            // q.k and dy.v of this wave's tiles (rows j, column i)
+            f32x4 qk[JW], dv[JW];
+#pragma unroll
+            for (int t = 0; t < JW; ++t) qk[t] = dv[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                if (kAhead) {
+#pragma unroll
+                    for (int u = 0; u < KN; ++u)
+                        if (u % KS == ks) fetch_k(nt_next, u);
+                }
+#pragma unroll
+                for (int t = 0; t < JW; ++t)
+                    qk[t] = O::mfma(row_frag<E, KD>(Ks, qb, scol(t), ks), row_frag<E, KD>(Qs, qb, srow(t), ks), qk[t]);
+                if (ks % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks < kVT / 32; ++ks)
+#pragma unroll
+                for (int t = 0; t < JW; ++t)
+                    dv[t] = O::mfma(row_frag<E, kVT>(Vs, rb, scol(t), ks), row_frag<E, kVT>(Ds, rb, srow(t), ks), dv[t]);
+#pragma unroll
+            for (int t = 0; t < JW; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) csum += mask[t][r] == 0.f ? 0.f : mask[t][r] * qk[t][r] * dv[t][r];
+            __builtin_amdgcn_sched_barrier(0);
+            // q^T (weighted dy), four key tiles at a time, against the states
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                frag wv[JS][O::NW];
+#pragma unroll
+                for (int ks = 0; ks < JS; ++ks) {
+                    const frag df = val_frag<E>(Ds, vb, ks);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = wd[n][32 * ks + 8 * lg + e] * O::value(df, e);
+                    O::template parts<O::NW>(x, wv[ks]);
+                }
+#pragma unroll
+                for (int t = 0; t < KT; t += 4) {
+                    f32x4 g[4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) g[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < JS; ++ks) {
+                        frag kf[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) kf[d] = col_frag<E, KD>(Qs, cb, t + d, ks);
+#pragma unroll
+                        for (int p = O::NW - 1; p >= 0; --p)
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) g[d] = O::mfma(kf[d], wv[ks][p], g[d]);
+                    }
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) csum += (n ? S : U)[t + d][r] * g[d][r];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            dsum += (double)csum;
+            read_v();
+        }
+        if constexpr (MODE == kOut) {
             // Scores, transposed (rows j, column i = this lane's token of the strip), and the carried
             // state's part of the outputs (rows are values, column i). A step's fragments are read, and
             // pieces of the next chunk's k loaded, while the step before is computed.
-            f32x4 sc[JW], ac2[kDec ? IT : 1];
+            f32x4 sc[JW];
 #pragma unroll
             for (int t = 0; t < JW; ++t) sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (kDec) {
-#pragma unroll
-                for (int it = 0; it < IT; ++it) ac2[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
             constexpr int QA = IT == 4 ? 2 : 1;
             frag qs[2][QA], kf[2][JW], qf[2][IT];
             const auto read = [&](int ks, int b) {
@@ -555,24 +689,16 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 float x[8];
-                frag sp[NS], up[kDec ? NS : 1];
+                frag sp[NS];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = S[2 * ks + (e >> 2)][e & 3];
                 O::template parts<NS>(x, sp);
-                if constexpr (kDec) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = U[2 * ks + (e >> 2)][e & 3];
-                    O::template parts<NS>(x, up);
-                }
 #pragma unroll
                 for (int t = 0; t < JW; ++t) sc[t] = O::mfma(kf[b][t], qs[b][t == 2 ? 1 : 0], sc[t]);
 #pragma unroll
                 for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        acc[it] = O::mfma(sp[n], qf[b][it], acc[it]);
-                        if constexpr (kDec) ac2[it] = O::mfma(up[n], qf[b][it], ac2[it]);
-                    }
+                    for (int it = 0; it < IT; ++it) acc[it] = O::mfma(sp[n], qf[b][it], acc[it]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             read_v();
@@ -588,75 +714,71 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
 #pragma unroll
             for (int it = 0; it < IT; ++it)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (kDec) acc[it][r] = rs[it] * (acc[it][r] * (float)(16 * it + lr + 1) + ac2[it][r]);
-                    else acc[it][r] *= rs[it];
-                }
+                for (int r = 0; r < 4; ++r) acc[it][r] *= rs[it];
         }
 
         // the state behind the chunk
         {
-            // a step: four key tiles and 32 tokens, whose fragments are read during the step before
+            // A step: four key tiles and 32 tokens, whose fragments are read during the step before. U, which needs the
+            // old S, goes first, then S.
             constexpr int TS = 4, NSTEP = KT / TS * JS;
-            frag wv[JS][O::NW], wv2[kU ? JS : 1][O::NW], kf[2][TS];
+            frag kf[2][TS];
             const auto read = [&](int step) {
 #pragma unroll
                 for (int d = 0; d < TS; ++d)
                     kf[kAhead ? step & 1 : 0][d] = col_frag<E, KD>(Ks, cb, TS * (step / JS) + d, step % JS);
             };
-            if (kAhead) read(0);
-#pragma unroll
-            for (int ks = 0; ks < JS; ++ks) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = wt[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
-                O::template parts<O::NW>(x, wv[ks]);
-                if constexpr (kU) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = wu[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
-                    O::template parts<O::NW>(x, wv2[ks]);
-                }
-            }
             // a^nt rounded so that the errors of the chunks cancel: of their product no more than one remains
             const float at = uniform((float)(whole + drift));
-            drift += whole - (double)at;
+            drift = uniform64(drift + (whole - (double)at));
 #pragma unroll
-            for (int step = 0; step < NSTEP; ++step) {
-                const int t = TS * (step / JS), ks = step % JS;
-                if (!kAhead) read(step);
-                else if (step + 1 < NSTEP) read(step + 1);
-                if (kAhead) {
+            for (int of_u = kU; of_u >= 0; --of_u) {
+                f32x4 *const X = of_u ? U : S;
+                frag wv[JS][O::NW];
+                if (kAhead) read(0);
 #pragma unroll
-                    for (int u = 0; u < VN; ++u)
-                        if (u % NSTEP == step) fetch_v(nt_next, u);
+                for (int ks = 0; ks < JS; ++ks) {
+                    float x[8];
 #pragma unroll
-                    for (int u = 0; u < QN; ++u)
-                        if (u % NSTEP == step) fetch_q(nt_next, u);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                if (ks == 0) {
-#pragma unroll
-                    for (int d = 0; d < TS; ++d)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if constexpr (kU) U[t + d][r] = at * U[t + d][r] + atn * S[t + d][r];
-                            S[t + d][r] *= at;
-                        }
+                    for (int e = 0; e < 8; ++e) x[e] = (of_u ? wu : wt)[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
+                    O::template parts<O::NW>(x, wv[ks]);
                 }
 #pragma unroll
-                for (int n = O::NW - 1; n >= 0; --n)
+                for (int step = 0; step < NSTEP; ++step) {
+                    const int t = TS * (step / JS), ks = step % JS;
+                    if (!kAhead) read(step);
+                    else if (step + 1 < NSTEP) read(step + 1);
+                    if (kAhead && !of_u) {
 #pragma unroll
-                    for (int d = 0; d < TS; ++d) {
-                        const frag k = kf[kAhead ? step & 1 : 0][d];
-                        S[t + d] = O::mfma(k, wv[ks][n], S[t + d]);
-                        if constexpr (kU) U[t + d] = O::mfma(k, wv2[ks][n], U[t + d]);
+                        for (int u = 0; u < VN; ++u)
+                            if (u % NSTEP == step) {
+                                fetch_v(nt_next, u);
+                                fetch_d(nt_next, u);
+                            }
+#pragma unroll
+                        for (int u = 0; u < QN; ++u)
+                            if (u % NSTEP == step) fetch_q(nt_next, u);
                     }
-                __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (ks == 0) {
+#pragma unroll
+                        for (int d = 0; d < TS; ++d)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                X[t + d][r] = of_u ? at * X[t + d][r] + atn * S[t + d][r] : at * X[t + d][r];
+                    }
+#pragma unroll
+                    for (int n = O::NW - 1; n >= 0; --n)
+#pragma unroll
+                        for (int d = 0; d < TS; ++d)
+                            X[t + d] = O::mfma(kf[kAhead ? step & 1 : 0][d], wv[ks][n], X[t + d]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         __syncthreads();  // the scores are there, the chunk's tiles have been read
 
-        if constexpr (!kSt) {
+        if constexpr (MODE == kOut) {
             // (the blocks of 32 tokens that lie behind a strip hold nothing for it)
 #pragma unroll
             for (int ks = 0; ks < JS; ++ks) {
@@ -673,21 +795,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
             }
         }
         if (more) stage_all(nt_next);
-        if constexpr (!kSt) {
-            if constexpr (kDec) {
-                float csum = 0.f;
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const int i = 16 * it + lr;
-                    const int64_t from = ofirst + (c * C + row_of(i, nt)) * (int64_t)(a.H * a.vd) + p0;
-                    if (i < nt) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (p0 + r < a.vd) csum += acc[it][r] * ld_io<ES == 2>(a.dy, from + r);
-                    }
-                }
-                dsum += (double)csum;
-            } else {
+        if constexpr (MODE == kOut) {
+            {
                 const int rows = a.L - c * C < C ? (int)(a.L - c * C) : C;  // written: zeros behind the length
                 if constexpr (VEC) {
                     // (rows behind the last lie outside the buffer, and are dropped)
@@ -764,14 +873,11 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
     }
     if constexpr (kDec) {
         if (last && a.dh_final) {
-            const float *p = a.dh_final + chain * nstate;
+            load_state(S, a.dh_final, chain);
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int n = key_of(t, lg, r);
-                    if (n < a.kd && col < a.vd) dsum += (double)U[t][r] * p[(int64_t)n * a.sk + (int64_t)col * a.sv];
-                }
+                for (int r = 0; r < 4; ++r) dsum += (double)U[t][r] * (double)S[t][r];
         }
         // sum over the workgroup, in a fixed order
         __shared__ double sums[kThreads];
@@ -781,7 +887,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 || MODE == kDecay ? 1 : 2) void
             if (tid < n) sums[tid] += sums[tid + n];
             __syncthreads();
         }
-        if (tid == 0) a.part[((int64_t)h * a.b + bi) * a.nseg * a.nvt + seg * a.nvt + vt] = sums[0];
+        if (tid == 0) a.part[(((int64_t)h * a.b + bi) * a.nseg + seg) * (a.nvt * a.nkt) + tile] = sums[0];
     }
 }
 
@@ -858,22 +964,39 @@ __global__ __launch_bounds__(kThreads) void linattn_decay_kernel(const double *p
 
 // ------------------------------------------------------------------ launch ---
 template <typename E, int MODE, bool VEC>
-hipError_t launch_dims(const Args &a, int64_t grid, hipStream_t s) {
-    const dim3 g((unsigned)grid), t(kThreads);
-    if (a.kd <= 64) hipLaunchKernelGGL((linattn_kernel<E, 64, MODE, VEC>), g, t, 0, s, a);
-    else if (a.kd <= 128) hipLaunchKernelGGL((linattn_kernel<E, 128, MODE, VEC>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((linattn_kernel<E, 256, MODE, VEC>), g, t, 0, s, a);
+hipError_t launch_dims(const Passes &p, hipStream_t s) {
+    const dim3 g(p.ends[p.n - 1]), t(kThreads);
+    const int kd = p.a[0].kd;
+    if constexpr (MODE == kDecay) hipLaunchKernelGGL((linattn_kernel<E, 64, MODE, VEC>), g, t, 0, s, p);
+    else if (kd <= 64) hipLaunchKernelGGL((linattn_kernel<E, 64, MODE, VEC>), g, t, 0, s, p);
+    else if (kd <= 128) hipLaunchKernelGGL((linattn_kernel<E, 128, MODE, VEC>), g, t, 0, s, p);
+    else hipLaunchKernelGGL((linattn_kernel<E, 256, MODE, VEC>), g, t, 0, s, p);
     return hipGetLastError();
 }
 
 template <int MODE>
+hipError_t launch_passes(Passes &p, bool bf16, hipStream_t s) {
+    bool vec = true;
+    int64_t end = 0;
+    for (int i = 0; i < 3; ++i) {
+        const Args &a = p.a[i];
+        if (i < p.n) {
+            end += a.b * a.H * a.nseg * a.nvt * a.nkt;
+            vec = vec && a.kd % 8 == 0 && a.vd % 8 == 0;
+        }
+        p.ends[i] = (unsigned)end;
+    }
+    if (end == 0) return hipSuccess;
+    if (bf16) return vec ? launch_dims<uint16_t, MODE, true>(p, s) : launch_dims<uint16_t, MODE, false>(p, s);
+    return vec ? launch_dims<float, MODE, true>(p, s) : launch_dims<float, MODE, false>(p, s);
+}
+
+template <int MODE>
 hipError_t launch_pass(const Args &a, bool bf16, hipStream_t s) {
-    const int64_t grid = a.b * a.H * a.nseg * a.nvt;
-    if (grid == 0) return hipSuccess;
-    const bool vec = a.kd % 8 == 0 && a.vd % 8 == 0;
-    if (bf16)
-        return vec ? launch_dims<uint16_t, MODE, true>(a, grid, s) : launch_dims<uint16_t, MODE, false>(a, grid, s);
-    return vec ? launch_dims<float, MODE, true>(a, grid, s) : launch_dims<float, MODE, false>(a, grid, s);
+    Passes p{};
+    p.a[0] = a;
+    p.n = 1;
+    return launch_passes<MODE>(p, bf16, s);
 }
 
 struct LinPlan {
@@ -883,15 +1006,16 @@ struct LinPlan {
 
 int tiles(int64_t d) { return (int)((d + kVT - 1) / kVT); }
 
-// Segments: enough workgroups for two on each of the 256 CUs, of four chunks at least
-LinPlan make_lin_plan(const m3_shape &s) {
+// Segments: enough workgroups for two on each of the 256 CUs, of four chunks at least. A
+// pass has a workgroup a chain and tile of values; the backward runs three passes at once.
+LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
     LinPlan p{};
     p.C = s.io_dtype == M3_BF16 ? Ops<uint16_t>::C : Ops<float>::C;
     p.chains = s.batch * s.nheads;
     p.nchunks = (s.seqlen + p.C - 1) / p.C;
     int64_t n = s.nsegments;
     if (n == 0) {
-        const int64_t have = p.chains * tiles(s.headdim);
+        const int64_t have = p.chains * (bwd ? 2 * tiles(s.dstate) + tiles(s.headdim) : tiles(s.headdim));
         n = have >= 384 || have == 0 ? 1 : 512 / have;
         if (n > p.nchunks / 4) n = p.nchunks / 4;
     }
@@ -919,12 +1043,14 @@ m3_status lin_check(const m3_shape *s, uint32_t flags) {
     return M3_OK;
 }
 
-m3_status lin_plan(const m3_shape *s, LinPlan *p) {
+m3_status lin_plan(const m3_shape *s, bool bwd, LinPlan *p) {
     const m3_status st = lin_check(s, 0);
     if (st != M3_OK) return st;
-    *p = make_lin_plan(*s);
-    // one workgroup a chain, segment and tile of values or keys
-    if (p->chains * p->nseg * tiles(s->headdim > s->dstate ? s->headdim : s->dstate) > kMaxGrid) return M3_ERR_UNSUPPORTED;
+    *p = make_lin_plan(*s, bwd);
+    // one workgroup a chain, segment and tile of values and keys
+    const int64_t wgs = p->chains * p->nseg;
+    if (wgs * tiles(s->headdim) * tiles(s->dstate) > kMaxGrid || wgs * (2 * tiles(s->dstate) + tiles(s->headdim)) > kMaxGrid)
+        return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
 
@@ -946,7 +1072,7 @@ BwdWs bwd_ws(const m3_shape &s, const LinPlan &p) {
         w.dk = up(rows * s.dstate * 4);
         w.dv = up(rows * s.headdim * 4);
     }
-    w.part = up((size_t)p.chains * p.nseg * tiles(s.headdim) * 8);
+    w.part = up((size_t)p.chains * p.nseg * tiles(s.headdim) * tiles(s.dstate) * 8);
     w.total = 3 * w.seg + w.dk + w.dv + w.part;
     return w;
 }
@@ -964,6 +1090,7 @@ Args base_args(const m3_shape &s, const LinPlan &p, const float *log_decay, cons
 void set_dims(Args &a, int64_t kd, int64_t vd, bool swapped) {
     a.kd = (int)kd; a.vd = (int)vd;
     a.nvt = tiles(vd);
+    a.nkt = 1;
     a.sk = swapped ? (int)vd : 1;
     a.sv = swapped ? 1 : (int)kd;
 }
@@ -1135,14 +1262,14 @@ extern "C" {
 
 size_t m3_linattn_workspace_bytes(const m3_shape *shape) {
     LinPlan p;
-    if (lin_plan(shape, &p) != M3_OK || p.nseg == 1) return 0;
+    if (lin_plan(shape, false, &p) != M3_OK || p.nseg == 1) return 0;
     return up((size_t)p.chains * p.nseg * shape->headdim * shape->dstate * 4);
 }
 
 m3_status m3_linattn_fwd(const m3_shape *shape, const m3_linattn_io *io, void *workspace, size_t ws_bytes,
                          void *stream) {
     LinPlan p;
-    const m3_status st = lin_plan(shape, &p);
+    const m3_status st = lin_plan(shape, false, &p);
     if (st != M3_OK) return st;
     if (!io || !isfinite(io->scale)) return M3_ERR_INVALID_ARG;
     const m3_shape &s = *shape;
@@ -1175,13 +1302,13 @@ m3_status m3_linattn_fwd(const m3_shape *shape, const m3_linattn_io *io, void *w
 
 size_t m3_linattn_bwd_workspace_bytes(const m3_shape *shape) {
     LinPlan p;
-    return lin_plan(shape, &p) == M3_OK ? bwd_ws(*shape, p).total : 0;
+    return lin_plan(shape, true, &p) == M3_OK ? bwd_ws(*shape, p).total : 0;
 }
 
 m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m3_linattn_grads *gr, void *workspace,
                          size_t ws_bytes, void *stream) {
     LinPlan p;
-    const m3_status st = lin_plan(shape, &p);
+    const m3_status st = lin_plan(shape, true, &p);
     if (st != M3_OK) return st;
     if (!io || !gr || !isfinite(io->scale)) return M3_ERR_INVALID_ARG;
     const m3_shape &s = *shape;
@@ -1226,16 +1353,24 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         Args dq = f;  // (dy, v, k), the state transposed
         set_dims(dq, s.headdim, s.dstate, true);
         dq.q = dy; dq.k = v; dq.v = k; dq.s_in = s_in; dq.o = gr->dq;
-        if ((e = launch_pass<kOut>(dq, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         Args dk = r;  // (v, dy, q), the state transposed
         set_dims(dk, s.headdim, s.dstate, true);
         dk.q = v; dk.k = dy; dk.v = q; dk.s_in = d_in;
         dk.o32 = per > 1; dk.o = per > 1 ? pk : gr->dk;
-        if ((e = launch_pass<kOut>(dk, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         Args dv = r;  // (k, q, dy)
         dv.s_in = d_in; dv.s_out = gr->dh0;
         dv.o32 = per > 1; dv.o = per > 1 ? pv : gr->dv;
-        if ((e = launch_pass<kOut>(dv, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
+        // all three at once where one kernel fits their keys (P of dq and dk, N of dv)
+        const auto size = [](int64_t d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); };
+        Passes first{}, second{};
+        first.a[0] = dq; first.a[1] = dk; first.a[2] = dv;
+        first.n = size(s.headdim) == size(s.dstate) ? 3 : 2;
+        if ((e = launch_passes<kOut>(first, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
+        if (first.n == 2) {
+            second.a[0] = dv;
+            second.n = 1;
+            if ((e = launch_passes<kOut>(second, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
+        }
         if (per > 1) {
             const int64_t rows = s.batch * s.seqlen;
             if ((e = sum_heads(pk, gr->dk, bf16, rows, G, per, s.dstate, hs)) != hipSuccess ||
@@ -1244,13 +1379,13 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         }
         if (gr->dlog_decay) {
             f.s_in = s_in; f.u_in = split ? seg_u : nullptr;
-            f.dy = gr->dy; f.dh_final = gr->dh_final; f.part = part;
+            f.nkt = tiles(s.dstate); f.dy = dy; f.dh_final = gr->dh_final; f.part = part;
             if ((e = launch_pass<kDecay>(f, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         }
     }
     if (gr->dlog_decay) {
         hipLaunchKernelGGL(linattn_decay_kernel, dim3((unsigned)H), dim3(kThreads), 0, hs, part, gr->dlog_decay,
-                           s.batch * p.nseg * tiles(s.headdim));
+                           s.batch * p.nseg * tiles(s.headdim) * tiles(s.dstate));
         e = hipGetLastError();
     }
     return status(e);
