@@ -1217,12 +1217,13 @@ template <typename E, typename T, int LPR, bool VEC>
 hipError_t launch_step_rows(const StepArgs &a, hipStream_t s) {
     constexpr int RW = kThreads / LPR;
     const m3_linattn_step_io &io = *a.io;
-    // few heads: one row a thread, so that more of the card takes part
+    // Rows of a thread: four (97 us for 8192 states of 64 x 128 in fp32; 99 with eight, 108 with two), or one
+    // where the states are few, so that more of the card takes part
     const bool wide = a.b * a.H >= 1024;
-    const int rows = RW * (wide ? 8 : 1);
+    const int rows = RW * (wide ? 4 : 1);
     const dim3 grid((unsigned)(a.b * a.H), (unsigned)((a.P + rows - 1) / rows)), t(kThreads);
     if (wide)
-        hipLaunchKernelGGL((linattn_step_kernel<E, T, LPR, 8, VEC>), grid, t, 0, s, io.q, io.k, io.v, io.log_decay, io.h,
+        hipLaunchKernelGGL((linattn_step_kernel<E, T, LPR, 4, VEC>), grid, t, 0, s, io.q, io.k, io.v, io.log_decay, io.h,
                            io.y, a.H, a.per, a.P, a.N, io.scale);
     else
         hipLaunchKernelGGL((linattn_step_kernel<E, T, LPR, 1, VEC>), grid, t, 0, s, io.q, io.k, io.v, io.log_decay, io.h,
