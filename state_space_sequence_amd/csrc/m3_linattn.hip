@@ -589,7 +589,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
 #pragma unroll
             for (int ks = 0; ks < JS; ++ks) vf[ks] = val_frag<E>(Vs, vb, ks);
         };
-        f32x4 acc[MODE == kOut ? IT : 1];
+        f32x4 acc[MODE == kOut ? IT : 1], sc[MODE == kOut ? JW : 1];
         float csum = 0.f;
         if constexpr (kSt) read_v();
         if constexpr (kDec) {
@@ -661,7 +661,6 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
             // Scores, transposed (rows j, column i = this lane's token of the strip), and the carried
             // state's part of the outputs (rows are values, column i). A step's fragments are read, and
             // pieces of the next chunk's k loaded, while the step before is computed.
-            f32x4 sc[JW];
 #pragma unroll
             for (int t = 0; t < JW; ++t) sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -676,7 +675,16 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
 #pragma unroll
                 for (int t = 0; t < JW; ++t) kf[b][t] = row_frag<E, KD>(Ks, qb, scol(t), ks);
             };
+            // the state's parts of a step, formed during the step before
+            frag sp[2][NS];
+            const auto split = [&](int ks, int b) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = S[2 * ks + (e >> 2)][e & 3];
+                O::template parts<NS>(x, sp[b]);
+            };
             if (kAhead) read(0, 0);
+            split(0, 0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int b = kAhead ? ks & 1 : 0;
@@ -688,34 +696,39 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
                         if (u % KS == ks) fetch_k(nt_next, u);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                float x[8];
-                frag sp[NS];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = S[2 * ks + (e >> 2)][e & 3];
-                O::template parts<NS>(x, sp);
-#pragma unroll
-                for (int t = 0; t < JW; ++t) sc[t] = O::mfma(kf[b][t], qs[b][t == 2 ? 1 : 0], sc[t]);
+                if (ks + 1 < KS) split(ks + 1, (ks + 1) & 1);
 #pragma unroll
                 for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
-                    for (int it = 0; it < IT; ++it) acc[it] = O::mfma(sp[n], qf[b][it], acc[it]);
+                    for (int it = 0; it < IT; ++it) acc[it] = O::mfma(sp[ks & 1][n], qf[b][it], acc[it]);
+#pragma unroll
+                for (int t = 0; t < JW; ++t) sc[t] = O::mfma(kf[b][t], qs[b][t == 2 ? 1 : 0], sc[t]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             read_v();
-#pragma unroll
-            for (int t = 0; t < JW; ++t) {
-                const int jb = 2 * scol(t) + (lg >> 1);
-                f32x4 x;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = sc[t][r] * mask[t][r];
-                O::template store4<NA>(
-                    As + (16 * srow(t) + lr) * C + ((jb ^ swap_of<E, C>(lr)) << 3) + 4 * (lg & 1), C * C, x);
-            }
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[it][r] *= rs[it];
         }
+        // What is left of the scores and of the state's part of the outputs is done among the products of the update
+        const auto put_scores = [&]() {
+            if constexpr (MODE == kOut) {
+#pragma unroll
+                for (int t = 0; t < JW; ++t) {
+                    const int jb = 2 * scol(t) + (lg >> 1);
+                    f32x4 x;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[r] = sc[t][r] * mask[t][r];
+                    O::template store4<NA>(
+                        As + (16 * srow(t) + lr) * C + ((jb ^ swap_of<E, C>(lr)) << 3) + 4 * (lg & 1), C * C, x);
+                }
+            }
+        };
+        const auto scale_rows = [&]() {
+            if constexpr (MODE == kOut) {
+#pragma unroll
+                for (int it = 0; it < IT; ++it)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[it][r] *= rs[it];
+            }
+        };
 
         // the state behind the chunk
         {
@@ -736,13 +749,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
                 f32x4 *const X = of_u ? U : S;
                 frag wv[JS][O::NW];
                 if (kAhead) read(0);
-#pragma unroll
-                for (int ks = 0; ks < JS; ++ks) {
+                const auto weigh = [&](int ks) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = (of_u ? wu : wt)[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
                     O::template parts<O::NW>(x, wv[ks]);
-                }
+                };
+                weigh(0);
 #pragma unroll
                 for (int step = 0; step < NSTEP; ++step) {
                     const int t = TS * (step / JS), ks = step % JS;
@@ -772,6 +785,9 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
 #pragma unroll
                         for (int d = 0; d < TS; ++d)
                             X[t + d] = O::mfma(kf[kAhead ? step & 1 : 0][d], wv[ks][n], X[t + d]);
+                    if (step == 0 && JS == 2) weigh(1);
+                    if (!of_u && step == (NSTEP > 1 ? 1 : 0)) put_scores();
+                    if (!of_u && step == NSTEP - 1) scale_rows();
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
