@@ -908,7 +908,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
 }
 
 // Segment states into incoming states, in place: st[c][seg] <- the state before the
-// segment (in the order of the sweep), from init [c] or zero. One thread a state element.
+// segment (in the order of the sweep), from init [c] or zero. One thread a state element; the loads
+// of 8 segments are in flight together.
 struct ChainArgs {
     float *st, *ut;
     const float *init, *log_decay;
@@ -928,38 +929,67 @@ __device__ __forceinline__ void chain_element(const ChainArgs &a, int64_t e) {
     const float ld = a.log_decay[chain % a.H];
     const double whole = power(ld, a.seg_tokens);
     double s = a.init ? a.init[e] : 0.f, u = 0.0;
-    for (int k = 0; k < a.nseg; ++k) {
-        const int seg = a.rev ? a.nseg - 1 - k : k;
-        int64_t n = len - seg * a.seg_tokens;
-        n = n < 0 ? 0 : (n < a.seg_tokens ? n : a.seg_tokens);
-        const double p = n == a.seg_tokens ? whole : power(ld, n);
-        const int64_t at = (chain * a.nseg + seg) * a.nstate + i;
-        const float own = a.st[at];
-        a.st[at] = (float)s;
-        if (a.ut) {
-            const float ou = a.ut[at];
-            a.ut[at] = (float)u;
-            u = p * u + p * (double)n * s + ou;
+    constexpr int kAhead = 8;
+    for (int k0 = 0; k0 < a.nseg; k0 += kAhead) {
+        float own[kAhead], ou[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int k = k0 + j < a.nseg ? k0 + j : a.nseg - 1;
+            const int64_t at = (chain * a.nseg + (a.rev ? a.nseg - 1 - k : k)) * a.nstate + i;
+            own[j] = a.st[at];
+            ou[j] = a.ut ? a.ut[at] : 0.f;
         }
-        s = p * s + own;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int k = k0 + j, seg = a.rev ? a.nseg - 1 - k : k;
+            if (k >= a.nseg) break;
+            int64_t n = len - seg * a.seg_tokens;
+            n = n < 0 ? 0 : (n < a.seg_tokens ? n : a.seg_tokens);
+            const double p = n == a.seg_tokens ? whole : power(ld, n);
+            const int64_t at = (chain * a.nseg + seg) * a.nstate + i;
+            a.st[at] = (float)s;
+            if (a.ut) {
+                a.ut[at] = (float)u;
+                u = p * u + p * (double)n * s + ou[j];
+            }
+            s = p * s + own[j];
+        }
     }
 }
 
-__global__ __launch_bounds__(kThreads) void linattn_chain_kernel(const ChainArgs a) {
-    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < a.chains * a.nstate; e += (int64_t)gridDim.x * kThreads)
-        chain_element(a, e);
+struct Chains {
+    ChainArgs a[2];
+    int n;
+};
+
+__global__ __launch_bounds__(kThreads) void linattn_chain_kernel(const Chains c) {
+    const int64_t n = c.a[0].chains * c.a[0].nstate;
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n * c.n; e += (int64_t)gridDim.x * kThreads) {
+        if (e < n) chain_element(c.a[0], e);
+        else chain_element(c.a[1], e - n);
+    }
 }
 
-// out[row][g][d] = sum over the heads of group g of part[row][h][d]
+// out[row][g][d] = sum over the heads of group g of part[row][h][d], for dk and dv
+struct Heads {
+    const float *part[2];
+    void *out[2];
+    int64_t rows;
+    int G, per, d[2];
+};
+
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void linattn_heads_kernel(const float *part, void *out, int64_t rows, int G,
-                                                                 int per, int d) {
-    const int64_t n = rows * G * d;
-    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += (int64_t)gridDim.x * kThreads) {
+__global__ __launch_bounds__(kThreads) void linattn_heads_kernel(const Heads a) {
+    const int64_t n0 = a.rows * a.G * a.d[0], n = n0 + a.rows * a.G * a.d[1];
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+        const bool v = i >= n0;
+        const int64_t e = v ? i - n0 : i;
+        const int d = v ? a.d[1] : a.d[0];
         const int64_t rg = e / d;
-        const float *p = part + rg * per * d + e % d;
+        const float *p = (v ? a.part[1] : a.part[0]) + rg * a.per * d + e % d;
+        void *out = v ? a.out[1] : a.out[0];
         float s = 0.f;
-        for (int k = 0; k < per; ++k) s += p[(int64_t)k * d];
+        for (int k = 0; k < a.per; ++k) s += p[(int64_t)k * d];
         if constexpr (BF16) static_cast<__bf16 *>(out)[e] = (__bf16)s;
         else static_cast<float *>(out)[e] = s;
     }
@@ -982,7 +1012,8 @@ __global__ __launch_bounds__(kThreads) void linattn_decay_kernel(const double *p
 template <typename E, int MODE, bool VEC>
 hipError_t launch_dims(const Passes &p, hipStream_t s) {
     const dim3 g(p.ends[p.n - 1]), t(kThreads);
-    const int kd = p.a[0].kd;
+    int kd = 0;
+    for (int i = 0; i < p.n; ++i) kd = p.a[i].kd > kd ? p.a[i].kd : kd;
     if constexpr (MODE == kDecay) hipLaunchKernelGGL((linattn_kernel<E, 64, MODE, VEC>), g, t, 0, s, p);
     else if (kd <= 64) hipLaunchKernelGGL((linattn_kernel<E, 64, MODE, VEC>), g, t, 0, s, p);
     else if (kd <= 128) hipLaunchKernelGGL((linattn_kernel<E, 128, MODE, VEC>), g, t, 0, s, p);
@@ -1022,8 +1053,15 @@ struct LinPlan {
 
 int tiles(int64_t d) { return (int)((d + kVT - 1) / kVT); }
 
-// Segments: enough workgroups for two on each of the 256 CUs, of four chunks at least. A
-// pass has a workgroup a chain and tile of values; the backward runs three passes at once.
+// Key tiles of the kernels
+int key_size(int64_t d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
+
+// Segments. A pass has a workgroup a chain and tile of values (the backward runs three passes at
+// once), and a CU has room for two, or for one with 256 keys. Splitting reads k and v twice, about 1.45 times
+// the work, and two workgroups of a CU run at 0.6 of the speed of one: two segments that fill the
+// second place cost more than they bring (b4 L2048, 256 workgroups: 95 us in one piece, 124 in
+// two), three or more pay (48 workgroups of L32768: 1310 us in one piece, 415 in ten). Segments have two
+// chunks at least; below six chunks the two launches more cost as much as they save.
 LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
     LinPlan p{};
     p.C = s.io_dtype == M3_BF16 ? Ops<uint16_t>::C : Ops<float>::C;
@@ -1032,8 +1070,11 @@ LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
     int64_t n = s.nsegments;
     if (n == 0) {
         const int64_t have = p.chains * (bwd ? 2 * tiles(s.dstate) + tiles(s.headdim) : tiles(s.headdim));
-        n = have >= 384 || have == 0 ? 1 : 512 / have;
-        if (n > p.nchunks / 4) n = p.nchunks / 4;
+        const bool one = key_size(s.dstate) == 256 || (bwd && key_size(s.headdim) == 256);
+        n = have == 0 ? 1 : (one ? 256 : 512) / have;
+        if (!one && n == 2) n = 1;
+        if (n > p.nchunks / 2) n = p.nchunks / 2;
+        if (p.nchunks < 6) n = 1;
     }
     if (n > p.nchunks) n = p.nchunks;
     if (n < 1) n = 1;
@@ -1111,29 +1152,27 @@ void set_dims(Args &a, int64_t kd, int64_t vd, bool swapped) {
     a.sv = swapped ? 1 : (int)kd;
 }
 
-hipError_t chain_states(const Args &a, const LinPlan &p, float *st, float *ut, const float *init, bool rev,
-                        hipStream_t s) {
+ChainArgs chain_args(const Args &a, const LinPlan &p, float *st, float *ut, const float *init) {
     ChainArgs c{};
     c.st = st; c.ut = ut; c.init = init; c.log_decay = a.log_decay; c.lengths = a.lengths;
     c.chains = p.chains; c.nstate = (int64_t)a.kd * a.vd; c.L = a.L; c.seg_tokens = p.seg_chunks * p.C;
-    c.H = a.H; c.nseg = p.nseg; c.rev = rev;
-    int64_t grid = (c.chains * c.nstate + kThreads - 1) / kThreads;
+    c.H = a.H; c.nseg = p.nseg; c.rev = a.rev;
+    return c;
+}
+
+hipError_t chain_states(const Chains &c, hipStream_t s) {
+    int64_t grid = (c.n * c.a[0].chains * c.a[0].nstate + kThreads - 1) / kThreads;
     if (grid > 65536) grid = 65536;
     hipLaunchKernelGGL(linattn_chain_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, c);
     return hipGetLastError();
 }
 
-hipError_t sum_heads(const float *part, void *out, bool bf16, int64_t rows, int64_t G, int64_t per, int64_t d,
-                     hipStream_t s) {
-    int64_t grid = (rows * G * d + kThreads - 1) / kThreads;
+hipError_t sum_heads(const Heads &h, bool bf16, hipStream_t s) {
+    int64_t grid = (h.rows * h.G * (h.d[0] + h.d[1]) + kThreads - 1) / kThreads;
     if (grid == 0) return hipSuccess;
     if (grid > 65536) grid = 65536;
-    if (bf16)
-        hipLaunchKernelGGL((linattn_heads_kernel<true>), dim3((unsigned)grid), dim3(kThreads), 0, s, part, out, rows,
-                           (int)G, (int)per, (int)d);
-    else
-        hipLaunchKernelGGL((linattn_heads_kernel<false>), dim3((unsigned)grid), dim3(kThreads), 0, s, part, out, rows,
-                           (int)G, (int)per, (int)d);
+    if (bf16) hipLaunchKernelGGL((linattn_heads_kernel<true>), dim3((unsigned)grid), dim3(kThreads), 0, s, h);
+    else hipLaunchKernelGGL((linattn_heads_kernel<false>), dim3((unsigned)grid), dim3(kThreads), 0, s, h);
     return hipGetLastError();
 }
 
@@ -1263,11 +1302,10 @@ hipError_t launch_step(const StepArgs &a, hipStream_t s) {
 
 m3_status status(hipError_t e) { return e == hipSuccess ? M3_OK : M3_ERR_HIP; }
 
-// Segment states of one direction: each segment's own, then chained from init
-hipError_t segment_states(Args a, const LinPlan &p, bool bf16, float *st, float *ut, const float *init, hipStream_t s) {
+// Each segment's own end states in one direction
+hipError_t segment_states(Args a, bool bf16, float *st, float *ut, hipStream_t s) {
     a.s_in = nullptr; a.s_out = st; a.u_out = ut;
-    const hipError_t e = ut ? launch_pass<kStateU>(a, bf16, s) : launch_pass<kState>(a, bf16, s);
-    return e == hipSuccess ? chain_states(a, p, st, ut, init, a.rev, s) : e;
+    return ut ? launch_pass<kStateU>(a, bf16, s) : launch_pass<kState>(a, bf16, s);
 }
 
 }  // namespace
@@ -1307,8 +1345,11 @@ m3_status m3_linattn_fwd(const m3_shape *shape, const m3_linattn_io *io, void *w
     a.s_in = io->h0;
     if (p.nseg > 1) {
         float *seg = static_cast<float *>(workspace);
-        const hipError_t e = segment_states(a, p, bf16, seg, nullptr, io->h0, hs);
-        if (e != hipSuccess) return M3_ERR_HIP;
+        Chains c{};
+        c.a[0] = chain_args(a, p, seg, nullptr, io->h0);
+        c.n = 1;
+        if (segment_states(a, bf16, seg, nullptr, hs) != hipSuccess || chain_states(c, hs) != hipSuccess)
+            return M3_ERR_HIP;
         a.s_in = seg;
         a.seg_in = true;
     }
@@ -1361,9 +1402,14 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         r.rev = true;
         r.q = k; r.k = q; r.v = dy; r.si = r.su = sc; r.sr = 1.f;
         if (split) {
-            e = segment_states(f, p, bf16, seg_s, gr->dlog_decay ? seg_u : nullptr, io->h0, hs);
-            if (e == hipSuccess) e = segment_states(r, p, bf16, seg_d, nullptr, gr->dh_final, hs);
-            if (e != hipSuccess) return M3_ERR_HIP;
+            float *ut = gr->dlog_decay ? seg_u : nullptr;
+            Chains c{};
+            c.a[0] = chain_args(f, p, seg_s, ut, io->h0);
+            c.a[1] = chain_args(r, p, seg_d, nullptr, gr->dh_final);
+            c.n = 2;
+            if (segment_states(f, bf16, seg_s, ut, hs) != hipSuccess ||
+                segment_states(r, bf16, seg_d, nullptr, hs) != hipSuccess || chain_states(c, hs) != hipSuccess)
+                return M3_ERR_HIP;
         }
         const float *s_in = split ? seg_s : io->h0, *d_in = split ? seg_d : gr->dh_final;
         f.seg_in = r.seg_in = split;
@@ -1378,10 +1424,11 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         dv.s_in = d_in; dv.s_out = gr->dh0;
         dv.o32 = per > 1; dv.o = per > 1 ? pv : gr->dv;
         // all three at once where one kernel fits their keys (P of dq and dk, N of dv)
-        const auto size = [](int64_t d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); };
+        // or, larger than some need, all workgroups of one launch run at the same time
+        const int64_t wgs = p.chains * p.nseg * (2 * tiles(s.dstate) + tiles(s.headdim));
         Passes first{}, second{};
         first.a[0] = dq; first.a[1] = dk; first.a[2] = dv;
-        first.n = size(s.headdim) == size(s.dstate) ? 3 : 2;
+        first.n = key_size(s.headdim) == key_size(s.dstate) || wgs <= 512 ? 3 : 2;
         if ((e = launch_passes<kOut>(first, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         if (first.n == 2) {
             second.a[0] = dv;
@@ -1389,10 +1436,8 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
             if ((e = launch_passes<kOut>(second, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         }
         if (per > 1) {
-            const int64_t rows = s.batch * s.seqlen;
-            if ((e = sum_heads(pk, gr->dk, bf16, rows, G, per, s.dstate, hs)) != hipSuccess ||
-                (e = sum_heads(pv, gr->dv, bf16, rows, G, per, s.headdim, hs)) != hipSuccess)
-                return M3_ERR_HIP;
+            const Heads sums = {{pk, pv}, {gr->dk, gr->dv}, s.batch * s.seqlen, G, per, {(int)s.dstate, (int)s.headdim}};
+            if ((e = sum_heads(sums, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         }
         if (gr->dlog_decay) {
             f.s_in = s_in; f.u_in = split ? seg_u : nullptr;
