@@ -15,7 +15,7 @@
  * Shapes use m3_shape: batch b, seqlen L, nheads H query heads, ngroups G key and
  * value heads (H % G == 0; head h reads h / (H/G)), headdim P values per head,
  * dstate N keys per head, io_dtype; rank must be 1, chunk and eps are not used.
- * N and P: 1 to 256, any value; multiples of 8 load fastest. H <= 65536.
+ * N and P: 1 to 256, any value; multiples of 8 load fastest. H <= 65536, b * L * H <= 2^40.
  *   q [b,L,H,N]   k [b,L,G,N]   v [b,L,G,P]   y [b,L,H,P]     io dtype
  *   log_decay [H] fp32: <= 0 (a decay of at most 1); -infinity is a decay of 0,
  *     a state that holds its last token only
@@ -37,8 +37,9 @@
  * stream is a hipStream_t of the current device passed as void*, all arguments
  * are checked on the host before any HIP call, nothing is allocated, freed or
  * synchronised, and every call can be captured into a graph. Outputs may not
- * overlap inputs, but for the step's state. Results do not depend on timing: the
- * same call gives the same bits.
+ * overlap inputs or each other, but for the step's state, and h_final, which may be
+ * h0 itself (a pointer given twice otherwise is M3_ERR_INVALID_ARG). Results do not
+ * depend on timing: the same call gives the same bits.
  */
 #ifndef M3_LINATTN_H
 #define M3_LINATTN_H

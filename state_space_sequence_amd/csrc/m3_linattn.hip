@@ -31,6 +31,8 @@
 // one of 4 rows and gets 4 rows of one column), fp32 element by element.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "m3_internal.h"
 #include "m3_linattn.h"
 
@@ -1085,6 +1087,18 @@ LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
 
 bool al16(const void *p) { return (((uintptr_t)p) & 15u) == 0; }
 
+// whether an output is an input, or another output
+bool clash(std::initializer_list<const void *> out, std::initializer_list<const void *> in) {
+    for (auto o = out.begin(); o != out.end(); ++o) {
+        if (!*o) continue;
+        for (const void *i : in)
+            if (i == *o) return true;
+        for (auto n = out.begin(); n != o; ++n)
+            if (*n == *o) return true;
+    }
+    return false;
+}
+
 m3_status lin_check(const m3_shape *s, uint32_t flags) {
     if (!s) return M3_ERR_INVALID_ARG;
     if (s->batch < 0 || s->seqlen < 0 || s->nheads < 1 || s->ngroups < 1 || s->headdim < 1 || s->dstate < 1 ||
@@ -1095,7 +1109,7 @@ m3_status lin_check(const m3_shape *s, uint32_t flags) {
     if (s->flags & ~flags) return M3_ERR_INVALID_ARG;
     if (s->rank != 1 || s->dstate > kMaxDim || s->headdim > kMaxDim || s->nheads > 65536) return M3_ERR_UNSUPPORTED;
     if (s->batch > (1LL << 31) || s->seqlen > (1LL << 31) || s->batch * s->nheads > kMaxGrid ||
-        (s->seqlen > 0 && s->batch > (1LL << 40) / s->seqlen))
+        (s->seqlen > 0 && s->batch * s->nheads > (1LL << 40) / s->seqlen))
         return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
@@ -1335,6 +1349,9 @@ m3_status m3_linattn_fwd(const m3_shape *shape, const m3_linattn_io *io, void *w
         if (!al16(x)) return M3_ERR_MISALIGNED;
     const size_t need = m3_linattn_workspace_bytes(shape);
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    // (h_final may be h0: a state is read before its end is written)
+    if (clash({io->y, io->h_final}, {io->q, io->k, io->v, workspace}) || (io->y && io->y == io->h0))
+        return M3_ERR_INVALID_ARG;
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = s.io_dtype == M3_BF16;
     const int H = (int)s.nheads, G = (int)s.ngroups;
@@ -1380,6 +1397,9 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         if (!al16(x)) return M3_ERR_MISALIGNED;
     const BwdWs w = bwd_ws(s, p);
     if (w.total && (!workspace || ws_bytes < w.total)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    if (clash({gr->dq, gr->dk, gr->dv, gr->dlog_decay, gr->dh0},
+              {io->q, io->k, io->v, io->log_decay, io->h0, gr->dy, gr->dh_final, workspace}))
+        return M3_ERR_INVALID_ARG;
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = s.io_dtype == M3_BF16;
     const int H = (int)s.nheads, G = (int)s.ngroups, per = H / G;
@@ -1426,9 +1446,10 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         // all three at once where one kernel fits their keys (P of dq and dk, N of dv)
         // or, larger than some need, all workgroups of one launch run at the same time
         const int64_t wgs = p.chains * p.nseg * (2 * tiles(s.dstate) + tiles(s.headdim));
+        const int kp = key_size(s.headdim), kn = key_size(s.dstate);
         Passes first{}, second{};
         first.a[0] = dq; first.a[1] = dk; first.a[2] = dv;
-        first.n = key_size(s.headdim) == key_size(s.dstate) || wgs <= 512 ? 3 : 2;
+        first.n = kp == kn || wgs <= (kp == 256 || kn == 256 ? 256 : 512) ? 3 : 2;
         if ((e = launch_passes<kOut>(first, bf16, hs)) != hipSuccess) return M3_ERR_HIP;
         if (first.n == 2) {
             second.a[0] = dv;
@@ -1463,6 +1484,7 @@ m3_status m3_linattn_step(const m3_shape *shape, const m3_linattn_step_io *io, v
     const void *ptrs[] = {io->q, io->k, io->v, io->log_decay, io->h, io->y};
     for (const void *x : ptrs)
         if (!al16(x)) return M3_ERR_MISALIGNED;
+    if (clash({io->y, io->h}, {io->q, io->k, io->v})) return M3_ERR_INVALID_ARG;
     const StepArgs a = {io, s.batch, (int)s.nheads, (int)(s.nheads / s.ngroups), (int)s.headdim, (int)s.dstate};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const bool bs = (s.flags & M3_FLAG_BF16_STATE) != 0;

@@ -260,3 +260,56 @@ def test_offsets_beyond_32_bits():
     check("y", y[:, -64:], want["y"][:, -64:], size["y"][:, -64:], f)
     check("h", h, want["h"], size["h"], factor(d, True))
     assert not y[:, :1000].any()
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dims", [(16, 70, 16, 4, 48, 72), (8, 40, 32, 32, 130, 64)])
+def test_many_chains_of_unequal_sizes(dims, io):
+    """Keys and values of different tiles on more workgroups than run at once."""
+    from state_space_sequence_amd import m3
+    b, L, H, G, N, P = dims
+    d = draw(11, b, L, H, G, N, P, io, h0=True, lengths=[L - i % 3 for i in range(b)], back=True)
+    want, size = (reference(**d, scale=0.3, magnitude=m) for m in (False, True))
+    args, kw = (d["q"], d["k"], d["v"], d["log_decay"]), dict(scale=0.3, h0=d["h0"], lengths=d["lengths"])
+    got = m3.linattn_bwd(*args, d["dy"], dh_final=d["dh_final"], **kw)
+    torch.cuda.synchronize()
+    for name in ("q", "k", "v", "h0"):
+        check(name, got[name], want[name], size[name], factor(d, name == "h0"))
+
+
+@pytest.mark.parametrize("nsegments", [1, 4])
+def test_state_in_place(nsegments):
+    """h_final may be h0 itself."""
+    from state_space_sequence_amd import m3
+    d = draw(12, 2, 600, 4, 2, 96, 80, torch.bfloat16, h0=True)
+    args = (d["q"], d["k"], d["v"], d["log_decay"])
+    y, h = m3.linattn_fwd(*args, h0=d["h0"], nsegments=nsegments)
+    h2 = d["h0"].clone()
+    y2, same = m3.linattn_fwd(*args, h0=h2, h_final=h2, nsegments=nsegments)
+    torch.cuda.synchronize()
+    assert same is h2 and torch.equal(y, y2) and torch.equal(h, h2)
+
+
+def test_most_heads_and_widest_rows():
+    """65536 heads of 256 keys and values: the first and the last heads' rows, 2^25 and (gradients
+    of shared keys, in fp32) 2^26 bytes apart, hold what a call of these heads alone gives."""
+    from state_space_sequence_amd import m3
+    H, L, D = 65536, 65, 256
+    torch.manual_seed(3)
+    k, v = (torch.randn(1, L, 1, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.zeros(1, L, H, D, device="cuda", dtype=torch.bfloat16)
+    dy = torch.zeros(1, L, H, D, device="cuda", dtype=torch.bfloat16)
+    some = [0, 1, H - 1]
+    q[:, :, some] = torch.randn(1, L, 3, D, device="cuda").to(torch.bfloat16)
+    dy[:, :, some] = torch.randn(1, L, 3, D, device="cuda").to(torch.bfloat16)
+    ld = torch.full((H,), -0.1).cuda()
+    y, _ = m3.linattn_fwd(q, k, v, ld, want_state=False)
+    y2, _ = m3.linattn_fwd(q[:, :, some].contiguous(), k, v, ld[some], want_state=False)
+    assert torch.equal(y[:, :, some], y2) and not y[:, :, 2:-1].any()
+    del y
+    got = m3.linattn_bwd(q, k, v, ld, dy, want_dh0=False, want_dlog_decay=False)
+    want = m3.linattn_bwd(q[:, :, some].contiguous(), k, v, ld[some], dy[:, :, some].contiguous(), want_dh0=False,
+                          want_dlog_decay=False)
+    torch.cuda.synchronize()
+    assert torch.equal(got["q"][:, :, some], want["q"]) and not got["q"][:, :, 2:-1].any()
+    assert torch.equal(got["k"], want["k"]) and torch.equal(got["v"], want["v"])

@@ -112,6 +112,34 @@ def test_workspace(m3):
     assert m3.linattn_workspace_bytes(shape(m3, seqlen=32768)) > 0
 
 
+def test_outputs_that_are_inputs(m3):
+    """A pointer given as an output and an input, or as two outputs, is refused (h_final may be h0)."""
+    s = shape(m3, nsegments=1)
+    for out, other in (("y", "q"), ("y", "v"), ("y", "h0"), ("h_final", "k"), ("y", "h_final")):
+        io = fill(m3.LinattnIO())
+        io.h0, io.h_final = 0x700000, 0x800000
+        setattr(io, out, getattr(io, other))
+        assert fwd(m3, s, io) == -1, (out, other)
+    need = m3.linattn_bwd_workspace_bytes(s)
+    for out, other in (("dq", "q"), ("dv", "v"), ("dq", "dy"), ("dk", "dv"), ("dh0", "dh_final"), ("dh0", "h0")):
+        io, g = fill(m3.LinattnIO()), m3.LinattnGrads()
+        io.h0 = 0x700000
+        for i, name in enumerate(("dy", "dh_final", "dq", "dk", "dv", "dlog_decay", "dh0")):
+            setattr(g, name, 0xa00000 + 0x1000 * i)
+        setattr(g, out, getattr(g if hasattr(g, other) else io, other))
+        assert bwd(m3, s, io, g, 0x200000, need) == -1, (out, other)
+    for out, other in (("y", "q"), ("y", "v"), ("h", "k"), ("y", "h")):
+        io = fill(m3.LinattnStepIO())
+        setattr(io, out, getattr(io, other))
+        assert step(m3, s, io) == -1, (out, other)
+
+
+def test_sizes_whose_tensors_no_memory_holds(m3):
+    s = shape(m3, batch=2, nheads=4096, ngroups=1, seqlen=1 << 31)
+    assert fwd(m3, s, fill(m3.LinattnIO())) == -2
+    assert m3.linattn_bwd_workspace_bytes(s) == 0
+
+
 b, L, H, G, N, P = 2, 10, 4, 2, 32, 16
 
 
