@@ -344,13 +344,15 @@ struct Lane {
         p1 = p0 + a.slice < most ? p0 + a.slice : most;
     }
     // v summed over the threads of this one's group, in a fixed order; every thread of the workgroup takes part
-    __device__ __forceinline__ float sum(const NormArgs &a, float v, float *lds) const {
+    template <typename T>
+    __device__ __forceinline__ T sum(const NormArgs &a, T v, T *lds) const {
         __syncthreads();
-        lds[threadIdx.x] = idle ? 0.f : v;
+        lds[threadIdx.x] = idle ? T{} : v;
         __syncthreads();
         if (po == 0)
             for (int k = 1; k < a.pg; ++k) lds[threadIdx.x] += lds[threadIdx.x + k * a.vb];
         for (int k = kThreads / 2; k > 0; k >>= 1) {
+            if (k >= a.vb) continue;  // (no two vectors are that far apart)
             __syncthreads();
             if (po == 0 && !idle && lv < k && lv + k < run) lds[threadIdx.x] += lds[threadIdx.x + k];
         }
@@ -358,6 +360,8 @@ struct Lane {
         return lds[threadIdx.x % a.vb - (idle ? 0 : lv)];
     }
 };
+
+constexpr int kAhead = 4;  // positions of a thread whose loads are in flight together
 
 // values, mean and squared differences of a group's part of a slice: part [n, G, nslice, pieces, 4]
 template <bool BF16, int V>
@@ -397,7 +401,7 @@ __global__ __launch_bounds__(kThreads) void seq_stats_kernel(const NormArgs a) {
             n = all;
         }
     // the group's part: its mean as a difference to one thread's, so that nothing is lost far from 0
-    const float all = t.sum(a, n, lds);
+    const float all = t.p1 > t.p0 ? (float)((t.p1 - t.p0) * t.run * V) : 0.f;
     __syncthreads();
     lds[threadIdx.x] = mean;
     __syncthreads();
@@ -415,31 +419,45 @@ __device__ __forceinline__ int64_t length_of(const NormArgs &a, int64_t row) {
     return l < 0 ? 0 : (l < a.S ? l : a.S);
 }
 
-__device__ __forceinline__ double wave_sum64(double v) {
+// v summed over the N threads (a wave, or the workgroup) of one (row, group), in a fixed order
+template <int N>
+__device__ __forceinline__ double join_sum(double v) {
     for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    if constexpr (N > 64) {
+        __shared__ double sums[N / 64];
+        __syncthreads();
+        if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll
+        for (int k = 0; k < N / 64; ++k) v += sums[k];
+    }
     return v;
 }
 
-// one wave a (row, group): stats <- mean, 1/std
+// N threads a (row, group): stats <- mean, 1/std.
+template <int N>
 __global__ __launch_bounds__(kThreads) void seq_join_kernel(const NormArgs a) {
-    const int64_t rg = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    const int64_t rg = (int64_t)blockIdx.x * (kThreads / N) + threadIdx.x / N;
     if (rg >= a.n * a.G) return;
-    const int lane = threadIdx.x % 64, total = a.nslice * a.pieces;
+    const int lane = threadIdx.x % N, total = a.nslice * a.pieces;
     const float *part = a.part + 4 * rg * total;
     double n = 0.0, s = 0.0, q = 0.0;
-    for (int i = lane; i < total; i += 64) {
+    for (int i = lane; i < total; i += N) {
         const f32x4 p = *reinterpret_cast<const f32x4 *>(part + 4 * i);
         n += (double)p[0];
         s += (double)p[0] * (double)p[1];
     }
-    n = wave_sum64(n);
-    const double mean = n > 0.0 ? wave_sum64(s) / n : 0.0;
-    for (int i = lane; i < total; i += 64) {
+    n = join_sum<N>(n);
+    s = join_sum<N>(s);
+    const double mean = n > 0.0 ? s / n : 0.0;
+    for (int i = lane; i < total; i += N) {
         const f32x4 p = *reinterpret_cast<const f32x4 *>(part + 4 * i);
         const double d = (double)p[1] - mean;
         q += (double)p[2] + (double)p[0] * d * d;
     }
-    const double var = n > 0.0 ? wave_sum64(q) / n : 0.0;
+    q = join_sum<N>(q);
+    const double var = n > 0.0 ? q / n : 0.0;
     if (lane == 0) {
         a.stats[4 * rg] = (float)mean;
         a.stats[4 * rg + 1] = (float)(1.0 / sqrt(var + (double)a.eps));
@@ -455,20 +473,28 @@ __global__ __launch_bounds__(kThreads) void seq_fwd_kernel(const NormArgs a) {
     float w[V], b[V];
     load_w<V, true>(a.w, t.c, V, 1.f, w);
     load_w<V, true>(a.b, t.c, V, 0.f, b);
-    for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
-        const int64_t at = (t.row * a.S + p) * a.C + t.c;
-        const int live = p < t.len ? V : 0;
-        float x[V], z[V], y[V];
-        load<BF16, V, true>(a.x, at, live, x);
-        if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z);
+    for (int64_t p = t.p0 + t.po; p < t.p1; p += kAhead * t.step) {
+        float x[kAhead][V], z[GATE ? kAhead : 1][V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float u = __builtin_fmaf((x[e] - mean) * r, w[e], b[e]);
-            if constexpr (GATE) y[e] = u * act<BF16>(z[e], a.silu);
-            else y[e] = act<BF16>(u, a.silu);
-            if (!live) y[e] = 0.f;
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
+            const int live = q < t.p1 && q < t.len ? V : 0;
+            load<BF16, V, true>(a.x, at, live, x[k]);
+            if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z[k]);
         }
-        store<BF16, V, true>(a.y, at, V, y);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
+            float y[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float u = __builtin_fmaf((x[k][e] - mean) * r, w[e], b[e]);
+                if constexpr (GATE) y[e] = u * act<BF16>(z[k][e], a.silu);
+                else y[e] = act<BF16>(u, a.silu);
+                if (q >= t.len) y[e] = 0.f;
+            }
+            store<BF16, V, true>(a.y, at, q < t.p1 ? V : 0, y);
+        }
     }
 }
 
@@ -491,7 +517,7 @@ __device__ __forceinline__ void seq_du(const NormArgs &a, float mean, float r, c
 // part of a slice, part [n, G, nslice, pieces, 4]
 template <bool BF16, int V, bool GATE>
 __global__ __launch_bounds__(kThreads) void seq_sums_kernel(const NormArgs a) {
-    __shared__ float lds[kThreads];
+    __shared__ f32x2 lds[kThreads];
     const Lane<V> t(a, false);
     float sa = 0.f, sb = 0.f;
     if (!t.idle) {
@@ -502,17 +528,26 @@ __global__ __launch_bounds__(kThreads) void seq_sums_kernel(const NormArgs a) {
         load_w<V, true>(a.b, t.c, V, 0.f, b);
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
-        for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
-            const int64_t at = (t.row * a.S + p) * a.C + t.c;
-            float x[V], z[V], d[V];
-            load<BF16, V, true>(a.x, at, V, x);
-            load<BF16, V, true>(a.dy, at, V, d);
-            if constexpr (GATE) load<BF16, V, true>(a.z, at, V, z);
-            seq_du<BF16, V, GATE>(a, mean, r, w, b, x, z, d);
+        for (int64_t p = t.p0 + t.po; p < t.p1; p += kAhead * t.step) {
+            float x[kAhead][V], z[kAhead][V], d[kAhead][V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                dw[e] = __builtin_fmaf(d[e], x[e], dw[e]);
-                db[e] += d[e];
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
+                const int live = q < t.p1 ? V : 0;
+                load<BF16, V, true>(a.x, at, live, x[k]);
+                load<BF16, V, true>(a.dy, at, live, d[k]);
+                if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                seq_du<BF16, V, GATE>(a, mean, r, w, b, x[k], z[k], d[k]);
+                if (p + k * t.step < t.p1) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        dw[e] = __builtin_fmaf(d[k][e], x[k][e], dw[e]);
+                        db[e] += d[k][e];
+                    }
+                }
             }
         }
         float *o = a.chan ? a.chan + ((int64_t)blockIdx.x * a.pg + t.po) * 2 * a.C + t.c : nullptr;
@@ -526,27 +561,24 @@ __global__ __launch_bounds__(kThreads) void seq_sums_kernel(const NormArgs a) {
             sb = __builtin_fmaf(w[e], dw[e], sb);
         }
     }
-    sa = t.sum(a, sa, lds);
-    sb = t.sum(a, sb, lds);
-    if (!t.idle && t.po == 0 && t.lv == 0) {
-        a.part[4 * t.entry] = sa;
-        a.part[4 * t.entry + 1] = sb;
-    }
+    const f32x2 sab = t.sum(a, f32x2{sa, sb}, lds);
+    if (!t.idle && t.po == 0 && t.lv == 0) *reinterpret_cast<f32x2 *>(a.part + 4 * t.entry) = sab;
 }
 
-// one wave a (row, group): stats <- means of d and d xh
+// likewise: stats <- means of d and d xh
+template <int N>
 __global__ __launch_bounds__(kThreads) void seq_join_sums_kernel(const NormArgs a) {
-    const int64_t rg = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    const int64_t rg = (int64_t)blockIdx.x * (kThreads / N) + threadIdx.x / N;
     if (rg >= a.n * a.G) return;
-    const int lane = threadIdx.x % 64, total = a.nslice * a.pieces;
+    const int lane = threadIdx.x % N, total = a.nslice * a.pieces;
     const float *part = a.part + 4 * rg * total;
     double sa = 0.0, sb = 0.0;
-    for (int i = lane; i < total; i += 64) {
+    for (int i = lane; i < total; i += N) {
         sa += (double)part[4 * i];
         sb += (double)part[4 * i + 1];
     }
-    sa = wave_sum64(sa);
-    sb = wave_sum64(sb);
+    sa = join_sum<N>(sa);
+    sb = join_sum<N>(sb);
     const double n = (double)length_of(a, rg / a.G) * a.D;
     if (lane == 0) {
         a.stats[4 * rg + 2] = n > 0.0 ? (float)(sa / n) : 0.f;
@@ -563,21 +595,28 @@ __global__ __launch_bounds__(kThreads) void seq_bwd_kernel(const NormArgs a) {
     float w[V], b[V];
     load_w<V, true>(a.w, t.c, V, 1.f, w);
     load_w<V, true>(a.b, t.c, V, 0.f, b);
-    for (int64_t p = t.p0 + t.po; p < t.p1; p += t.step) {
-        const int64_t at = (t.row * a.S + p) * a.C + t.c;
-        const int live = p < t.len ? V : 0;
-        float x[V], z[V], d[V];
-        load<BF16, V, true>(a.x, at, live, x);
-        load<BF16, V, true>(a.dy, at, live, d);
-        if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z);
-        seq_du<BF16, V, GATE>(a, mean, r, w, b, x, z, d);
+    for (int64_t p = t.p0 + t.po; p < t.p1; p += kAhead * t.step) {
+        float x[kAhead][V], z[kAhead][V], d[kAhead][V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            d[e] = live ? r * (d[e] * w[e] - ma - x[e] * mb) : 0.f;
-            if constexpr (GATE) z[e] = live ? z[e] : 0.f;
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
+            const int live = q < t.p1 && q < t.len ? V : 0;
+            load<BF16, V, true>(a.x, at, live, x[k]);
+            load<BF16, V, true>(a.dy, at, live, d[k]);
+            if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z[k]);
         }
-        store<BF16, V, true>(a.dx, at, V, d);
-        if constexpr (GATE) store<BF16, V, true>(a.dz, at, V, z);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
+            seq_du<BF16, V, GATE>(a, mean, r, w, b, x[k], z[k], d[k]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                d[k][e] = q < t.len ? r * (d[k][e] * w[e] - ma - x[k][e] * mb) : 0.f;
+                if constexpr (GATE) z[k][e] = q < t.len ? z[k][e] : 0.f;
+            }
+            store<BF16, V, true>(a.dx, at, q < t.p1 ? V : 0, d[k]);
+            if constexpr (GATE) store<BF16, V, true>(a.dz, at, q < t.p1 ? V : 0, z[k]);
+        }
     }
 }
 
@@ -668,8 +707,9 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
         p.vblocks = (int)(G * p.pieces);
     }
     p.pg = kThreads / p.vb;
-    // slices: eight workgroups a CU, of eight positions a thread at least
-    int64_t n = ceil_div(2048, (s.rows > 0 ? s.rows : 1) * p.vblocks);
+    // Slices: two workgroups a CU, of eight positions a thread at least. More slices are more partial sums (gradients of
+    // b8 L4096 of 4096 channels with a gate: 472 us, with eight a CU 613, with one 507; b1 of 320 channels 41, 40, 50)
+    int64_t n = ceil_div(512, (s.rows > 0 ? s.rows : 1) * p.vblocks);
     const int64_t most = ceil_div(s.positions, 8 * p.pg);
     n = n > most ? most : n;
     n = n < 1 ? 1 : n;
@@ -755,11 +795,15 @@ hipError_t launch_channel_sums(const NormArgs &a, int64_t rows, hipStream_t s) {
 
 template <bool BF16, int V>
 hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
-    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), t(kThreads), j((unsigned)ceil_div(a.n * a.G, kThreads / 64));
+    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), t(kThreads);
+    // (a workgroup a (row, group) where the partial sums are more than a wave takes at once)
+    const bool many = a.nslice * a.pieces > 64 && a.n * a.G <= kMaxGrid;
+    const dim3 j((unsigned)(many ? a.n * a.G : ceil_div(a.n * a.G, kThreads / 64)));
     hipError_t e;
     hipLaunchKernelGGL((seq_stats_kernel<BF16, V>), g, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(seq_join_kernel, j, t, 0, s, a);
+    if (many) hipLaunchKernelGGL(seq_join_kernel<kThreads>, j, t, 0, s, a);
+    else hipLaunchKernelGGL(seq_join_kernel<64>, j, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (!bwd) {
         if (a.z) hipLaunchKernelGGL((seq_fwd_kernel<BF16, V, true>), g, t, 0, s, a);
@@ -769,7 +813,8 @@ hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_
     if (a.z) hipLaunchKernelGGL((seq_sums_kernel<BF16, V, true>), g, t, 0, s, a);
     else hipLaunchKernelGGL((seq_sums_kernel<BF16, V, false>), g, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(seq_join_sums_kernel, j, t, 0, s, a);
+    if (many) hipLaunchKernelGGL(seq_join_sums_kernel<kThreads>, j, t, 0, s, a);
+    else hipLaunchKernelGGL(seq_join_sums_kernel<64>, j, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.z) hipLaunchKernelGGL((seq_bwd_kernel<BF16, V, true>), g, t, 0, s, a);
     else hipLaunchKernelGGL((seq_bwd_kernel<BF16, V, false>), g, t, 0, s, a);
