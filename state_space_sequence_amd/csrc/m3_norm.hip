@@ -30,6 +30,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxGrid = 0xffffff;  // workgroups along x: 2^32 threads
+constexpr int64_t kLastCache = 256 << 20;
 
 struct NormArgs {
     const void *x, *z;
@@ -43,6 +44,7 @@ struct NormArgs {
     int C, G, D;
     float eps;
     bool silu;
+    bool past;  // stores past the caches
     // tokens: rows of a workgroup. sequences: positions of a slice, slices; vectors of a workgroup,
     // positions it takes at a time, workgroups that share a group
     int64_t rows_wg, slice;
@@ -73,8 +75,9 @@ __device__ __forceinline__ void act2(float x, bool silu, float &v, float &s) {
     }
 }
 
-// 16 bytes. Tokens are read once, and past the caches (b8 L4096 of 4096 channels with a gate: 162 us with
-// ordinary loads, 136 with these; gradients 151 and 129); sequences are read again by the next pass.
+// 16 bytes. Tokens are read once, and past the caches; sequences are read again by the next pass. Where the tensors of a call
+// are larger than the last cache the stores go past it too (b8 L4096 of 4096 channels with a gate, one call after
+// another: 155 us, loads alone 162, neither 163; gradients of b4 147, 155, 154).
 template <bool ONCE>
 __device__ __forceinline__ u32x4 load16(const void *p) {
     const u32x4 *q = static_cast<const u32x4 *>(p);
@@ -105,8 +108,9 @@ __device__ __forceinline__ void load(const void *p, int64_t i, int live, float (
     }
 }
 
+// (past: by the caches, where the tensors of the call do not fit them)
 template <bool BF16, int V, bool VEC>
-__device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V]) {
+__device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V], bool past) {
     if constexpr (VEC && V > 1) {
         if (live > 0) {
             u32x4 w;
@@ -116,11 +120,18 @@ __device__ __forceinline__ void store(void *p, int64_t i, int live, const float 
                     const f32x2 v = {x[2 * e], x[2 * e + 1]};
                     w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2));
                 }
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = w;
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(x[e]);
-                *reinterpret_cast<u32x4 *>(static_cast<float *>(p) + i) = w;
+            }
+            u32x4 *to = static_cast<u32x4 *>(BF16 ? static_cast<void *>(static_cast<uint16_t *>(p) + i)
+                                                  : static_cast<void *>(static_cast<float *>(p) + i));
+            if (past) {
+                asm volatile("");  // (two equal stores but for their hint would become one)
+                __builtin_nontemporal_store(w, to);
+                asm volatile("");
+            } else {
+                *to = w;
             }
         }
     } else {
@@ -219,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void token_fwd_kernel(const NormArgs a) {
                 if constexpr (GATE) y[e] = u * act<BF16>(z[k][e], a.silu);
                 else y[e] = act<BF16>(u, a.silu);
             }
-            store<BF16, V, VEC>(a.y, row * a.C + s.c[k], here ? s.live[k] : 0, y);
+            store<BF16, V, VEC>(a.y, row * a.C + s.c[k], here ? s.live[k] : 0, y, a.past);
         }
     }
 }
@@ -284,8 +295,8 @@ __global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
             const int live = here ? s.live[k] : 0;
 #pragma unroll
             for (int e = 0; e < V; ++e) d[k][e] = r * (d[k][e] - sa - x[k][e] * sb);
-            store<BF16, V, VEC>(a.dx, row * a.C + s.c[k], live, d[k]);
-            if constexpr (GATE) store<BF16, V, VEC>(a.dz, row * a.C + s.c[k], live, z[k]);
+            store<BF16, V, VEC>(a.dx, row * a.C + s.c[k], live, d[k], a.past);
+            if constexpr (GATE) store<BF16, V, VEC>(a.dz, row * a.C + s.c[k], live, z[k], a.past);
         }
     }
     if (s.rows && a.chan) {
@@ -493,7 +504,7 @@ __global__ __launch_bounds__(kThreads) void seq_fwd_kernel(const NormArgs a) {
                 else y[e] = act<BF16>(u, a.silu);
                 if (q >= t.len) y[e] = 0.f;
             }
-            store<BF16, V, true>(a.y, at, q < t.p1 ? V : 0, y);
+            store<BF16, V, true>(a.y, at, q < t.p1 ? V : 0, y, a.past);
         }
     }
 }
@@ -614,8 +625,8 @@ __global__ __launch_bounds__(kThreads) void seq_bwd_kernel(const NormArgs a) {
                 d[k][e] = q < t.len ? r * (d[k][e] * w[e] - ma - x[k][e] * mb) : 0.f;
                 if constexpr (GATE) z[k][e] = q < t.len ? z[k][e] : 0.f;
             }
-            store<BF16, V, true>(a.dx, at, q < t.p1 ? V : 0, d[k]);
-            if constexpr (GATE) store<BF16, V, true>(a.dz, at, q < t.p1 ? V : 0, z[k]);
+            store<BF16, V, true>(a.dx, at, q < t.p1 ? V : 0, d[k], a.past);
+            if constexpr (GATE) store<BF16, V, true>(a.dz, at, q < t.p1 ? V : 0, z[k], a.past);
         }
     }
 }
@@ -825,6 +836,9 @@ hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_
 m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, void *workspace, hipStream_t hs) {
     a.n = s.rows; a.S = s.positions; a.C = (int)s.channels; a.G = (int)s.groups; a.D = a.C / a.G;
     a.eps = s.eps; a.silu = s.activation == M3_ACT_SILU;
+    // x, y and the gate, dy, dx and the gate's
+    const int64_t bytes = a.n * a.S * a.C * (s.io_dtype == M3_BF16 ? 2 : 4) * ((bwd ? 3 : 2) + (a.z ? (bwd ? 2 : 1) : 0));
+    a.past = bytes > kLastCache;
     a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = p.nslice; a.vb = p.vb; a.pg = p.pg; a.pieces = p.pieces;
     char *ws = static_cast<char *>(workspace);
     a.part = reinterpret_cast<float *>(ws);

@@ -240,3 +240,19 @@ def test_mixer_layer_of_linear_attention_and_norm():
     near = lambda got, want: float((got.double().cpu() - want).norm() / want.norm()) < 1e-4
     assert near(o, ref["y"][0]) and near(gn["z"], ref["z"][0]) and near(gn["weight"], ref["weight"][0])
     assert all(near(ga[n], back[n]) for n in ("q", "k", "v", "log_decay"))
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+def test_tensors_larger_than_the_caches(io):
+    """Rows of a call whose tensors fit no cache are those of a small call, bit by bit."""
+    from state_space_sequence_amd import m3
+    torch.manual_seed(4)
+    C, G, n = 1024, 8, 50000
+    x, z, dy = (torch.randn(n, C, device="cuda").to(io) for _ in range(3))
+    w, b = torch.randn(C, device="cuda"), torch.randn(C, device="cuda")
+    y = m3.group_norm_fwd(x, G, w, b, z=z)
+    g = m3.group_norm_bwd(x, G, dy, w, b, z=z)
+    for s in (slice(0, 100), slice(31000, 31077), slice(n - 50, n)):
+        assert torch.equal(y[s], m3.group_norm_fwd(x[s], G, w, b, z=z[s]))
+        small = m3.group_norm_bwd(x[s], G, dy[s], w, b, z=z[s])
+        assert torch.equal(g["x"][s], small["x"]) and torch.equal(g["z"][s], small["z"])
