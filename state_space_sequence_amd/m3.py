@@ -578,23 +578,32 @@ def gate_contract(y, z_in, W_Z, W_O, o=None, stream=None):
 
 
 # ------------------------- linear attention with a decay for each head ---
+_HERE = contextlib.nullcontext()
+# the handle of a device's current stream, without an object for it (1 us of a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _owned_by(stream):
     """Context for allocating a call's outputs and workspace: memory of the stream that the
     call runs on, so that what is freed after the call is not handed out before it ran."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _launch(fn, device, stream, *args):
     """fn(*args, stream) on the tensors' device, whichever device is current."""
     index = device.index
-    s = torch.cuda.current_stream(index) if stream is None else stream
-    if s.device_index != index:
-        raise ValueError("stream: on device %d, expected %d (the device of the inputs)" % (s.device_index, index))
+    if stream is None:
+        handle = _raw_stream(index)
+    elif stream.device_index == index:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError("stream: on device %d, expected %d (the device of the inputs)" % (stream.device_index, index))
     if index == torch.cuda.current_device():
-        rc = fn(*args, s.cuda_stream)
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, s.cuda_stream)
+            rc = fn(*args, handle)
     if rc != M3_OK:
         raise M3Error(rc)
 
@@ -673,7 +682,7 @@ def linattn_fwd(q, k, v, log_decay, *, scale=None, h0=None, lengths=None, y=None
     need = lib.m3_linattn_workspace_bytes(ctypes.byref(shape))
     with _owned_by(stream):
         if y is None:
-            y = torch.empty((b, L, H, P), dtype=io, device=q.device)
+            y = q.new_empty((b, L, H, P))
             ptrs.y = y.data_ptr()
         if h_final is None and want_state:
             h_final = torch.empty((b, H, P, N), dtype=f32, device=q.device)
@@ -741,7 +750,7 @@ def linattn_step(q, k, v, log_decay, h, *, scale=None, y=None, stream=None):
     shape = make_shape(b, 1, H, G, P, N, 1, 1, iot, 0.0, M3_FLAG_BF16_STATE if h.dtype is torch.bfloat16 else 0)
     if y is None:
         with _owned_by(stream):
-            y = torch.empty((b, H, P), dtype=io, device=q.device)
+            y = q.new_empty((b, H, P))
         ptrs.y = y.data_ptr()
     _launch(lib.m3_linattn_step, q.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
     return y
@@ -798,7 +807,7 @@ def group_norm_fwd(x, groups, weight=None, bias=None, *, z=None, activation="sil
     need = lib.m3_group_norm_workspace_bytes(ctypes.byref(shape), lengths is not None)
     with _owned_by(stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = x.new_empty(x.shape)
             io.y = y.data_ptr()
         if need and workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
