@@ -248,9 +248,10 @@ def _decode_specs(x, Braw, Craw, dt, A, lam, theta, B_bias, C_bias, B_normw, C_n
 def _dims5(name, t, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a torch.Tensor" % name)
-    if t.dim() != ndim:
-        raise ValueError("%s: expected %d dimensions, got shape %s" % (name, ndim, tuple(t.shape)))
-    return tuple(t.shape)
+    shape = tuple(t.shape)
+    if len(shape) != ndim:
+        raise ValueError("%s: expected %d dimensions, got shape %s" % (name, ndim, shape))
+    return shape
 
 
 def _io_dtype(t):
@@ -609,14 +610,14 @@ def _launch(fn, device, stream, *args):
 
 
 def _arg(name, t, shape, dtype, device):
-    """The pointer of a tensor of exactly this shape and dtype (or one of a tuple of
-    dtypes) on the device of that index; None for None. The checks of _expect and _ptr in
-    one pass: small calls cost as much on the host as on the GPU."""
+    """The pointer of a tensor of exactly this shape and dtype on the device of that index;
+    None for None. The checks of _expect and _ptr in one pass: small calls cost as much on the
+    host as on the GPU."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
-    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+    if t.dtype is not dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
@@ -642,8 +643,10 @@ def _workspace(workspace, device):
 
 
 def _linattn_dims(q, k, v, ndim):
-    """(lead, H, G, N, P) of q [*lead, H, N], k [*lead, G, N], v [*lead, G, P]."""
-    qs, _, vs = _dims5("q", q, ndim), _dims5("k", k, ndim), _dims5("v", v, ndim)
+    """(lead, H, G, N, P) of q [*lead, H, N], k [*lead, G, N] (whose shape is left to _arg),
+    v [*lead, G, P]."""
+    _need("k", k)
+    qs, vs = _dims5("q", q, ndim), _dims5("v", v, ndim)
     return qs[:-2], qs[-2], vs[-2], qs[-1], vs[-1]
 
 
@@ -742,12 +745,13 @@ def linattn_step(q, k, v, log_decay, h, *, scale=None, y=None, stream=None):
     iot, io, dev = _io_dtype(q), q.dtype, q.get_device()
     _need("log_decay", log_decay)
     _need("h", h)
+    half = isinstance(h, torch.Tensor) and h.dtype is torch.bfloat16
     ptrs = LinattnStepIO(_arg("q", q, (b, H, N), io, dev), _arg("k", k, (b, G, N), io, dev),
                          _arg("v", v, (b, G, P), io, dev), _arg("log_decay", log_decay, (H,), torch.float32, dev),
-                         _arg("h", h, (b, H, P, N), (torch.float32, torch.bfloat16), dev),
+                         _arg("h", h, (b, H, P, N), torch.bfloat16 if half else torch.float32, dev),
                          _arg("y", y, (b, H, P), io, dev), N ** -0.5 if scale is None else scale)
     _on_gpu(dev)
-    shape = make_shape(b, 1, H, G, P, N, 1, 1, iot, 0.0, M3_FLAG_BF16_STATE if h.dtype is torch.bfloat16 else 0)
+    shape = make_shape(b, 1, H, G, P, N, 1, 1, iot, 0.0, M3_FLAG_BF16_STATE if half else 0)
     if y is None:
         with _owned_by(stream):
             y = q.new_empty((b, H, P))
