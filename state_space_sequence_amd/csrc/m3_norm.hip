@@ -699,8 +699,10 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
         int64_t passes = ceil_div(s.rows, (int64_t)p.pass * 4096) * p.gy;
         const int64_t most = bwd ? 64 : 16;
         passes = passes < 1 ? 1 : (passes > most ? most : passes);
-        // (a partial sum is 8 bytes a channel: at most 512 of them)
-        if (bwd && ceil_div(s.rows, p.pass * passes) > 512) passes = ceil_div(s.rows, (int64_t)p.pass * 512);
+        // A workgroup's partial sums are 8 bytes a channel: two workgroups a CU (b4 L4096 in 64 groups of 64: 137 us, with four
+        // 146, with one 205)
+        const int64_t wgs = p.gy < 512 ? 512 / p.gy : 1;
+        if (bwd && ceil_div(s.rows, p.pass * passes) > wgs) passes = ceil_div(s.rows, p.pass * wgs);
         if (ceil_div(s.rows, p.pass * passes) > (1 << 20)) passes = ceil_div(s.rows, (int64_t)p.pass << 20);
         p.rows_wg = p.pass * passes;
         p.gx = ceil_div(s.rows, p.rows_wg);
