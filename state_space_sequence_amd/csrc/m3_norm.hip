@@ -4,7 +4,7 @@
 //   du = dy act'(u) | dy act(z);  dz = dy u act'(z);  d = du w
 //   dx = r (d - mean(d) - xh mean(d xh)),  xh = (x - mean) r;  dw = sum du xh;  db = sum du
 // Bound by HBM: x (z, dy) read and y (dx, dz) written once. Tokens, bf16 b8 L4096 of 4096 channels with a gate: 154 us, 5.2 TB/s;
-// gradients of b4: 144 us, 4.7 TB/s. Sequences read x twice, with gradients three times: bf16 b2 L4000 of 2048
+// gradients of b4: 136 us, 4.9 TB/s. Sequences read x twice, with gradients three times: bf16 b2 L4000 of 2048
 // channels 61 us, six launches, of tensors that the last cache holds.
 //
 // Tokens by themselves (one position a row): the lanes of a group (L of them, each with 16 bytes of
