@@ -33,7 +33,7 @@
 // bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 296 us, 230 TFLOP/s of useful products (their splits are as
 // many again), 3.1 TB/s; the bytes alone would take 157 us. The matrix cores are busy 38% of the time at 1.87 GHz; two waves a SIMD
 // (registers: the state, a step's fragments, the next chunk) do not hide each other's LDS reads and barriers. b2 L32768 of 24
-// heads in ten segments: 413 us. Gradients of b8 L2048, 16 heads of 128 x 128: 395 us, of them d log_decay
+// heads in ten segments: 401 us. Gradients of b8 L2048, 16 heads of 128 x 128: 395 us, of them d log_decay
 // about 0.4, bound by the vector instructions of its splits. fp32 runs on the fp32 matrix cores in chunks of 32.
 #include <math.h>
 
@@ -58,8 +58,9 @@ constexpr int kVT = 64;  // value columns of a workgroup
 constexpr int kMaxDim = 256;
 constexpr int64_t kMaxGrid = 0xffffff;  // workgroups along x: 2^32 threads
 
-// kOut: outputs. kState, kStateU: segment states (and their derivatives) only. kDecay: d log_decay
-enum Mode { kOut = 0, kState = 1, kStateU = 2, kDecay = 3 };
+// kOut: outputs. kState, kStateU: segment states (and their derivatives) only. kDecay: d log_decay.
+// kStateOnce: kState of keys and values that no other workgroup reads
+enum Mode { kOut = 0, kState = 1, kStateU = 2, kDecay = 3, kStateOnce = 4 };
 
 // one of a pass's three tensors: [b, L, heads, dim], read at head h / per
 struct Tensor {
@@ -167,16 +168,17 @@ struct Ops<float> {
 // span less, as H <= 65536) without a branch.
 constexpr unsigned kOutside = 0x80000000u;
 
-// 8 elements, packed; `cols` of them exist
-template <typename E, bool VEC>
+// 8 elements, packed; `cols` of them exist. ONCE: past the caches
+template <typename E, bool VEC, bool ONCE = false>
 __device__ __forceinline__ typename Ops<E>::pack load8(const char *p, unsigned bytes, unsigned at, int cols) {
     if constexpr (VEC) {
+        constexpr int AUX = ONCE ? 2 : 0;  // (non-temporal)
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, (int)bytes, 0x00020000);
         if constexpr (sizeof(E) == 2) {
-            return __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+            return __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, AUX);
         } else {
-            const f32x4 a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
-            const f32x4 b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + 16, 0, 0));
+            const f32x4 a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, AUX));
+            const f32x4 b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + 16, 0, AUX));
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     } else {
@@ -340,7 +342,8 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
     typedef Ops<E> O;
     typedef typename O::frag frag;
     constexpr int C = O::C, KT = KD / 16, KS = KD / 32, JS = C / 32, IT = C / 16, ES = sizeof(E);
-    constexpr bool kDec = MODE == kDecay, kSt = MODE == kState || MODE == kStateU, kU = kDec || MODE == kStateU;
+    constexpr bool kDec = MODE == kDecay, kOnce = MODE == kStateOnce,
+                   kSt = MODE == kState || MODE == kStateU || kOnce, kU = kDec || MODE == kStateU;
     constexpr int NA = O::NA, NS = O::NS;
     __shared__ __align__(16) E Qs[kSt ? 8 : C * KD];
     __shared__ __align__(16) E Ks[C * KD];
@@ -476,10 +479,10 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
     };
     const auto down = [&](int nt, int rows, unsigned stride) { return (unsigned)(rv ? nt - rows : rows) * stride; };
     const auto fetch_k = [&](int nt, int u) {
-        kx[u] = load8<E, VEC>(kp, span(nt, kst, kdim), ko + down(nt, KR * u, kst), kdim - kn);
+        kx[u] = load8<E, VEC, kOnce>(kp, span(nt, kst, kdim), ko + down(nt, KR * u, kst), kdim - kn);
     };
     const auto fetch_v = [&](int nt, int u) {
-        vx[u] = load8<E, VEC>(vp, span(nt, vst, a.vd), vo + down(nt, VR * u, vst), a.vd - v0 - vn);
+        vx[u] = load8<E, VEC, kOnce>(vp, span(nt, vst, a.vd), vo + down(nt, VR * u, vst), a.vd - v0 - vn);
     };
     const auto fetch_q = [&](int nt, int u) {
         qx[u] = load8<E, VEC>(qp, span(nt, qst, kdim), qo + down(nt, KR * u, qst), kdim - kn);
@@ -1042,8 +1045,9 @@ hipError_t launch_passes(Passes &p, bool bf16, hipStream_t s) {
         p.ends[i] = (unsigned)end;
     }
     if (end == 0) return hipSuccess;
-    if (bf16) return vec ? launch_dims<uint16_t, MODE, true>(p, s) : launch_dims<uint16_t, MODE, false>(p, s);
-    return vec ? launch_dims<float, MODE, true>(p, s) : launch_dims<float, MODE, false>(p, s);
+    constexpr int kSingle = MODE == kStateOnce ? kState : MODE;  // (loads by elements are all the same)
+    if (bf16) return vec ? launch_dims<uint16_t, MODE, true>(p, s) : launch_dims<uint16_t, kSingle, false>(p, s);
+    return vec ? launch_dims<float, MODE, true>(p, s) : launch_dims<float, kSingle, false>(p, s);
 }
 
 template <int MODE>
@@ -1068,7 +1072,7 @@ int key_size(int64_t d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 // once), and a CU has room for two, or for one with 256 keys. Splitting reads k and v twice, about 1.45 times
 // the work, and two workgroups of a CU run at 0.6 of the speed of one: two segments that fill the
 // second place cost more than they bring (b4 L2048, 256 workgroups: 95 us in one piece, 124 in
-// two), three or more pay (48 workgroups of L32768: 1310 us in one piece, 415 in ten). Segments have two
+// two), three or more pay (48 workgroups of L32768: 1310 us in one piece, 401 in ten). Segments have two
 // chunks at least; below six chunks the two launches more cost as much as they save.
 LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
     LinPlan p{};
@@ -1325,7 +1329,11 @@ m3_status status(hipError_t e) { return e == hipSuccess ? M3_OK : M3_ERR_HIP; }
 // Each segment's own end states in one direction
 hipError_t segment_states(Args a, bool bf16, float *st, float *ut, hipStream_t s) {
     a.s_in = nullptr; a.s_out = st; a.u_out = ut;
-    return ut ? launch_pass<kStateU>(a, bf16, s) : launch_pass<kState>(a, bf16, s);
+    if (ut) return launch_pass<kStateU>(a, bf16, s);
+    // (heads or tiles of values that read the same rows find them in the caches; else these would only hold what the
+    // outputs' pass reads long after: b2 L32768 of 24 heads 401 us, with ordinary loads 414;
+    // b1 L65536 of 16 heads 271 and 284)
+    return a.k.per == 1 && a.v.per == 1 && a.nvt == 1 ? launch_pass<kStateOnce>(a, bf16, s) : launch_pass<kState>(a, bf16, s);
 }
 
 }  // namespace
