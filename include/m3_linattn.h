@@ -15,7 +15,8 @@
  * Shapes use m3_shape: batch b, seqlen L, nheads H query heads, ngroups G key and
  * value heads (H % G == 0; head h reads h / (H/G)), headdim P values per head,
  * dstate N keys per head, io_dtype; rank must be 1, chunk and eps are not used.
- * N and P: 1 to 256, any value; multiples of 8 load fastest. H <= 65536, b * L * H <= 2^40.
+ * N and P: 1 to 256, any value; multiples of 8 load fastest. H <= 65536, b * L * H <= 2^40,
+ * and b * H, times the segments and the tiles of 64 values and keys, below 2^24 (else M3_ERR_UNSUPPORTED).
  *   q [b,L,H,N]   k [b,L,G,N]   v [b,L,G,P]   y [b,L,H,P]     io dtype
  *   log_decay [H] fp32: <= 0 (a decay of at most 1); -infinity is a decay of 0,
  *     a state that holds its last token only

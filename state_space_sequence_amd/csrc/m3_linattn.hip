@@ -30,7 +30,7 @@
 // columns: bf16 through the transposing LDS read (each lane of 16 names 4 consecutive elements of
 // one of 4 rows and gets 4 rows of one column), fp32 element by element.
 //
-// bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 296 us, 230 TFLOP/s of useful products (their splits are as
+// bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 299 us, 230 TFLOP/s of useful products (their splits are as
 // many again), 3.1 TB/s; the bytes alone would take 157 us. The matrix cores are busy 38% of the time at 1.87 GHz; two waves a SIMD
 // (registers: the state, a step's fragments, the next chunk) do not hide each other's LDS reads and barriers. b2 L32768 of 24
 // heads in ten segments: 401 us. Gradients of b8 L2048, 16 heads of 128 x 128: 395 us, of them d log_decay
