@@ -26,8 +26,8 @@
  *     gradients there are written as 0, and the final state is the one after the
  *     last token (h0 for a length of 0)
  * bf16 inputs run on the bf16 matrix cores with what is computed in between
- * (states, weighted values, scores) split into two or three bf16 parts, so that
- * nothing is rounded to fewer than 16 bits before the output is; fp32 inputs run
+ * (states, weighted values, scores) split into three bf16 parts, which hold all
+ * 24 bits of an fp32 value: nothing is rounded to fewer before the output is; fp32 inputs run
  * on the fp32 matrix cores. States and sums are fp32. The masked products of a
  * chunk (64 tokens, 32 in fp32) include zeros times later tokens: an infinity or
  * NaN in a token reaches the outputs of its whole chunk.

@@ -30,10 +30,9 @@
 // columns: bf16 through the transposing LDS read (each lane of 16 names 4 consecutive elements of
 // one of 4 rows and gets 4 rows of one column), fp32 element by element.
 //
-// bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 299 us, 230 TFLOP/s of useful products (their splits are as
-// many again), 3.1 TB/s; the bytes alone would take 157 us. The matrix cores are busy 38% of the time at 1.87 GHz; two waves a SIMD
-// (registers: the state, a step's fragments, the next chunk) do not hide each other's LDS reads and barriers. b2 L32768 of 24
-// heads in ten segments: 401 us. Gradients of b8 L2048, 16 heads of 128 x 128: 395 us, of them d log_decay
+// bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 335 us, 205 TFLOP/s of useful products (76 of a wave's 126
+// products a chunk are those of the further parts of its operands), 2.8 TB/s; the bytes alone would take 157 us. b2 L32768 of 24
+// heads in ten segments: 416 us. Gradients of b8 L2048, 16 heads of 128 x 128: 423 us, of them d log_decay
 // about 0.4, bound by the vector instructions of its splits. fp32 runs on the fp32 matrix cores in chunks of 32.
 #include <math.h>
 
@@ -100,9 +99,10 @@ struct Ops<uint16_t> {
     typedef bf16x8 frag;
     typedef u32x4 pack;  // 8 elements as loaded
     static constexpr int C = 64;   // tokens of a chunk
-    static constexpr int NS = 2;   // parts of a state operand
-    static constexpr int NA = 2;   // parts of a score
-    static constexpr int NW = 3;   // parts of a weighted value, whose sums are stored in fp32
+    // Parts of an operand that is no input (a state, a score, a weighted value): 3 of 8 bits hold all 24 of fp32. With two
+    // parts of a state and of a score, 16 bits, 0.22% of the bf16 outputs land on the other side of a rounding
+    // from the fp32 form's, with three 0.02%, what the order of fp32 sums gives; b8 L4096 takes 335 us instead of 299
+    static constexpr int kParts = 3;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -144,7 +144,7 @@ template <>
 struct Ops<float> {
     typedef f32x8 frag;
     typedef f32x8 pack;
-    static constexpr int C = 32, NS = 1, NA = 1, NW = 1;
+    static constexpr int C = 32, kParts = 1;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
@@ -344,11 +344,11 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
     constexpr int C = O::C, KT = KD / 16, KS = KD / 32, JS = C / 32, IT = C / 16, ES = sizeof(E);
     constexpr bool kDec = MODE == kDecay, kOnce = MODE == kStateOnce,
                    kSt = MODE == kState || MODE == kStateU || kOnce, kU = kDec || MODE == kStateU;
-    constexpr int NA = O::NA, NS = O::NS;
+    constexpr int NP = O::kParts;
     __shared__ __align__(16) E Qs[kSt ? 8 : C * KD];
     __shared__ __align__(16) E Ks[C * KD];
     __shared__ __align__(16) E Vs[C * kVT];
-    __shared__ __align__(16) E As[MODE != kOut ? 8 : NA * C * C];
+    __shared__ __align__(16) E As[MODE != kOut ? 8 : NP * C * C];
     __shared__ __align__(16) E Ds[kDec ? C * kVT : 8];  // dy
     __shared__ __align__(16) float wt[C], wu[kU ? C : 1], wd[kDec ? 2 : 1][kDec ? C : 1];
     __shared__ float pw[C + 1];  // a^n
@@ -634,14 +634,14 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
             // q^T (weighted dy), four key tiles at a time, against the states
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                frag wv[JS][O::NW];
+                frag wv[JS][NP];
 #pragma unroll
                 for (int ks = 0; ks < JS; ++ks) {
                     const frag df = val_frag<E>(Ds, vb, ks);
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = wd[n][32 * ks + 8 * lg + e] * O::value(df, e);
-                    O::template parts<O::NW>(x, wv[ks]);
+                    O::template parts<NP>(x, wv[ks]);
                 }
 #pragma unroll
                 for (int t = 0; t < KT; t += 4) {
@@ -654,7 +654,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
 #pragma unroll
                         for (int d = 0; d < 4; ++d) kf[d] = col_frag<E, KD>(Qs, cb, t + d, ks);
 #pragma unroll
-                        for (int p = O::NW - 1; p >= 0; --p)
+                        for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
                             for (int d = 0; d < 4; ++d) g[d] = O::mfma(kf[d], wv[ks][p], g[d]);
                     }
@@ -687,12 +687,12 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
                 for (int t = 0; t < JW; ++t) kf[b][t] = row_frag<E, KD>(Ks, qb, scol(t), ks);
             };
             // the state's parts of a step, formed during the step before
-            frag sp[2][NS];
+            frag sp[2][NP];
             const auto split = [&](int ks, int b) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = S[2 * ks + (e >> 2)][e & 3];
-                O::template parts<NS>(x, sp[b]);
+                O::template parts<NP>(x, sp[b]);
             };
             if (kAhead) read(0, 0);
             split(0, 0);
@@ -709,7 +709,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
                 __builtin_amdgcn_sched_barrier(0);
                 if (ks + 1 < KS) split(ks + 1, (ks + 1) & 1);
 #pragma unroll
-                for (int n = NS - 1; n >= 0; --n)
+                for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
                     for (int it = 0; it < IT; ++it) acc[it] = O::mfma(sp[ks & 1][n], qf[b][it], acc[it]);
 #pragma unroll
@@ -727,7 +727,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
                     f32x4 x;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) x[r] = sc[t][r] * mask[t][r];
-                    O::template store4<NA>(
+                    O::template store4<NP>(
                         As + (16 * srow(t) + lr) * C + ((jb ^ swap_of<E, C>(lr)) << 3) + 4 * (lg & 1), C * C, x);
                 }
             }
@@ -758,13 +758,13 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
 #pragma unroll
             for (int of_u = kU; of_u >= 0; --of_u) {
                 f32x4 *const X = of_u ? U : S;
-                frag wv[JS][O::NW];
+                frag wv[JS][NP];
                 if (kAhead) read(0);
                 const auto weigh = [&](int ks) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = (of_u ? wu : wt)[32 * ks + 8 * lg + e] * O::value(vf[ks], e);
-                    O::template parts<O::NW>(x, wv[ks]);
+                    O::template parts<NP>(x, wv[ks]);
                 };
                 weigh(0);
 #pragma unroll
@@ -792,7 +792,7 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
                                 X[t + d][r] = of_u ? at * X[t + d][r] + atn * S[t + d][r] : at * X[t + d][r];
                     }
 #pragma unroll
-                    for (int n = O::NW - 1; n >= 0; --n)
+                    for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
                         for (int d = 0; d < TS; ++d)
                             X[t + d] = O::mfma(kf[kAhead ? step & 1 : 0][d], wv[ks][n], X[t + d]);
@@ -809,14 +809,14 @@ __global__ __launch_bounds__(kThreads, KD == 256 ? 1 : 2) void linattn_kernel(co
             // (the blocks of 32 tokens that lie behind a strip hold nothing for it)
 #pragma unroll
             for (int ks = 0; ks < JS; ++ks) {
-                frag af[NA][IT];
+                frag af[NP][IT];
 #pragma unroll
-                for (int n = NA - 1; n >= 0; --n)
+                for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
                     for (int it = 2 * ks; it < IT; ++it) af[n][it] = row_frag<E, C>(As + n * C * C, ab, it, ks);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = NA - 1; n >= 0; --n)
+                for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
                     for (int it = 2 * ks; it < IT; ++it) acc[it] = O::mfma(vf[ks], af[n][it], acc[it]);
             }
