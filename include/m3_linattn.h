@@ -37,9 +37,10 @@
  * and are not kept; calls that may overlap need workspaces of their own), the
  * stream is a hipStream_t of the current device passed as void*, all arguments
  * are checked on the host before any HIP call, nothing is allocated, freed or
- * synchronised, and every call can be captured into a graph. Outputs may not
- * overlap inputs or each other, but for the step's state, and h_final, which may be
- * h0 itself (a pointer given twice otherwise is M3_ERR_INVALID_ARG). Results do not
+ * synchronised, and every call can be captured into a graph. Outputs and
+ * the workspace may not overlap inputs or each other, but for the step's state, and
+ * h_final, which may be h0 itself (a pointer given twice, one of the two for something
+ * that is written, is M3_ERR_INVALID_ARG). Results do not
  * depend on timing: the same call gives the same bits.
  */
 #ifndef M3_LINATTN_H

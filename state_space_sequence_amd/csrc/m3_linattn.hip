@@ -1097,7 +1097,7 @@ LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
 
 bool al16(const void *p) { return (((uintptr_t)p) & 15u) == 0; }
 
-// whether an output is an input, or another output
+// whether one of `out`, which are written, is one of `in` or another of `out`
 bool clash(std::initializer_list<const void *> out, std::initializer_list<const void *> in) {
     for (auto o = out.begin(); o != out.end(); ++o) {
         if (!*o) continue;
@@ -1364,7 +1364,9 @@ m3_status m3_linattn_fwd(const m3_shape *shape, const m3_linattn_io *io, void *w
     const size_t need = m3_linattn_workspace_bytes(shape);
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
     // (h_final may be h0: a state is read before its end is written)
-    if (clash({io->y, io->h_final}, {io->q, io->k, io->v, workspace}) || (io->y && io->y == io->h0))
+    if (clash({io->y, io->h_final}, {io->q, io->k, io->v, io->log_decay, io->lengths, workspace}) ||
+        clash({io->y}, {io->h0}) ||
+        (need && clash({workspace}, {io->q, io->k, io->v, io->log_decay, io->lengths, io->h0})))
         return M3_ERR_INVALID_ARG;
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = s.io_dtype == M3_BF16;
@@ -1411,8 +1413,8 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
         if (!al16(x)) return M3_ERR_MISALIGNED;
     const BwdWs w = bwd_ws(s, p);
     if (w.total && (!workspace || ws_bytes < w.total)) return M3_ERR_WORKSPACE_TOO_SMALL;
-    if (clash({gr->dq, gr->dk, gr->dv, gr->dlog_decay, gr->dh0},
-              {io->q, io->k, io->v, io->log_decay, io->h0, gr->dy, gr->dh_final, workspace}))
+    if (clash({gr->dq, gr->dk, gr->dv, gr->dlog_decay, gr->dh0, w.total ? workspace : nullptr},
+              {io->q, io->k, io->v, io->log_decay, io->h0, io->lengths, gr->dy, gr->dh_final}))
         return M3_ERR_INVALID_ARG;
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = s.io_dtype == M3_BF16;
@@ -1498,7 +1500,7 @@ m3_status m3_linattn_step(const m3_shape *shape, const m3_linattn_step_io *io, v
     const void *ptrs[] = {io->q, io->k, io->v, io->log_decay, io->h, io->y};
     for (const void *x : ptrs)
         if (!al16(x)) return M3_ERR_MISALIGNED;
-    if (clash({io->y, io->h}, {io->q, io->k, io->v})) return M3_ERR_INVALID_ARG;
+    if (clash({io->y, io->h}, {io->q, io->k, io->v, io->log_decay})) return M3_ERR_INVALID_ARG;
     const StepArgs a = {io, s.batch, (int)s.nheads, (int)(s.nheads / s.ngroups), (int)s.headdim, (int)s.dstate};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const bool bs = (s.flags & M3_FLAG_BF16_STATE) != 0;
