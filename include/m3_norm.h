@@ -21,7 +21,9 @@
  * stream is a hipStream_t of the current device passed as void*, all arguments
  * are checked on the host before any HIP call, nothing is allocated, freed or
  * synchronised, and every call can be captured into a graph. The same call gives
- * the same bits. y may be x or z itself, dx may be x or dy, dz may be z; no other overlap.
+ * the same bits. y may be x or z itself, dx may be x or dy, dz may be z; no other overlap
+ * with what is written, the workspace included (a pointer given twice otherwise is
+ * M3_ERR_INVALID_ARG).
  */
 #ifndef M3_NORM_H
 #define M3_NORM_H

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "m3.h"
 
 namespace m3i {
@@ -99,6 +101,18 @@ constexpr int kGenericMaxRows = 64;      // chunk * rank
 constexpr int kGenericMaxNP = 8192;      // N * P
 constexpr int kDecodeMaxP = 256;
 constexpr int kDecodeMaxR = 4;
+
+// whether one of `out`, which are written, is one of `in` or another of `out`
+inline bool clash(std::initializer_list<const void *> out, std::initializer_list<const void *> in) {
+    for (auto o = out.begin(); o != out.end(); ++o) {
+        if (!*o) continue;
+        for (const void *i : in)
+            if (i == *o) return true;
+        for (auto n = out.begin(); n != o; ++n)
+            if (*n == *o) return true;
+    }
+    return false;
+}
 
 // ----------------------------------------------------------------- device ---
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t v) {

@@ -36,8 +36,6 @@
 // about 0.4, bound by the vector instructions of its splits. fp32 runs on the fp32 matrix cores in chunks of 32.
 #include <math.h>
 
-#include <initializer_list>
-
 #include "m3_internal.h"
 #include "m3_linattn.h"
 
@@ -1096,18 +1094,6 @@ LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
 }
 
 bool al16(const void *p) { return (((uintptr_t)p) & 15u) == 0; }
-
-// whether one of `out`, which are written, is one of `in` or another of `out`
-bool clash(std::initializer_list<const void *> out, std::initializer_list<const void *> in) {
-    for (auto o = out.begin(); o != out.end(); ++o) {
-        if (!*o) continue;
-        for (const void *i : in)
-            if (i == *o) return true;
-        for (auto n = out.begin(); n != o; ++n)
-            if (*n == *o) return true;
-    }
-    return false;
-}
 
 m3_status lin_check(const m3_shape *s, uint32_t flags) {
     if (!s) return M3_ERR_INVALID_ARG;

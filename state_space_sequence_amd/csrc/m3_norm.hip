@@ -893,6 +893,10 @@ m3_status m3_group_norm_fwd(const m3_norm_shape *shape, const m3_norm_io *io, vo
         if (!al16(q)) return M3_ERR_MISALIGNED;
     const size_t need = p.total;
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    // (y may be x or z: an element is read before it is written, by the same thread)
+    if (clash({io->y}, {io->weight, io->bias, io->lengths, workspace}) ||
+        (need && clash({workspace}, {io->x, io->z, io->weight, io->bias, io->lengths})))
+        return M3_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = io->x; a.z = io->z; a.w = io->weight; a.b = io->bias; a.lengths = io->lengths; a.y = io->y;
     return run(*shape, p, a, false, workspace, reinterpret_cast<hipStream_t>(stream));
@@ -914,6 +918,13 @@ m3_status m3_group_norm_bwd(const m3_norm_shape *shape, const m3_norm_io *io, co
         if (!al16(q)) return M3_ERR_MISALIGNED;
     const size_t need = p.total;
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    // (likewise dx may be x or dy, and dz may be z)
+    if (clash({gr->dx, gr->dz, gr->dweight, gr->dbias}, {io->weight, io->bias, io->lengths, workspace}) ||
+        clash({gr->dweight, gr->dbias}, {io->x, io->z, gr->dy}) ||
+        (gr->dx != io->x && gr->dx != gr->dy && clash({gr->dx}, {io->z})) ||
+        (gr->dz != io->z && clash({gr->dz}, {io->x, gr->dy})) ||
+        (need && clash({workspace}, {io->x, io->z, io->weight, io->bias, io->lengths, gr->dy})))
+        return M3_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = io->x; a.z = io->z; a.w = io->weight; a.b = io->bias; a.lengths = io->lengths;
     a.dy = gr->dy; a.dx = gr->dx; a.dz = gr->dz; a.dw = gr->dweight; a.db = gr->dbias;

@@ -93,3 +93,42 @@ def test_linattn_step(m3):
                 io, = filled(m3.LinattnStepIO())
                 shared([io], (out, other))
                 assert m3.lib.m3_linattn_step(ctypes.byref(s), ctypes.byref(io), None) == -1, (out, other)
+
+
+def norm(m3, positions):
+    return m3.NormShape(4, positions, 64, 4, m3.M3_BF16, 1, 1e-5, 0)
+
+
+NORM_IN = ("x", "z", "weight", "bias", "lengths")
+NORM_OUT = ("dx", "dz", "dweight", "dbias")
+
+
+@pytest.mark.parametrize("positions", [1, 100])
+def test_group_norm_fwd(m3, positions):
+    s = norm(m3, positions)
+    n = int(m3.lib.m3_group_norm_workspace_bytes(ctypes.byref(s), 1))
+    call = lambda io, ws=WS: m3.lib.m3_group_norm_fwd(ctypes.byref(s), ctypes.byref(io), ws, n, None)
+    for other in ("weight", "bias", "lengths"):
+        io, = filled(m3.NormIO())
+        shared([io], ("y", other))
+        assert call(io) == -1, other
+    for other in NORM_IN + ("y",):
+        io, = filled(m3.NormIO())
+        assert call(io, getattr(io, other)) == -1, other
+
+
+@pytest.mark.parametrize("positions", [1, 100])
+def test_group_norm_bwd(m3, positions):
+    s = norm(m3, positions)
+    n = int(m3.lib.m3_group_norm_bwd_workspace_bytes(ctypes.byref(s), 1))
+    call = lambda io, g, ws=WS: m3.lib.m3_group_norm_bwd(ctypes.byref(s), ctypes.byref(io), ctypes.byref(g), ws, n, None)
+    allowed = {("dx", "x"), ("dx", "dy"), ("dz", "z")}
+    for out in NORM_OUT:
+        for other in NORM_IN + ("dy",) + NORM_OUT:
+            if other != out and (out, other) not in allowed:
+                io, g = both = filled(m3.NormIO(), m3.NormGrads())
+                shared(both, (out, other))
+                assert call(io, g) == -1, (out, other)
+    for other in NORM_IN + ("dy",) + NORM_OUT:
+        io, g = filled(m3.NormIO(), m3.NormGrads())
+        assert call(io, g, getattr(g if hasattr(g, other) else io, other)) == -1, other
