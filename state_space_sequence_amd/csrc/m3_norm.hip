@@ -33,6 +33,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;
 constexpr int64_t kMaxGrid = 0xffffff;  // workgroups along x: 2^32 threads
 constexpr int64_t kLastCache = 256 << 20;
+// Terms that a thread adds up in fp32, one after another: their error is below 2^-16 of the sum of their sizes
+// (2^-17 where they are equal). What is beyond is added in fp64
+constexpr int64_t kChain = 256;
 
 struct NormArgs {
     const void *x, *z;
@@ -152,6 +155,34 @@ __device__ __forceinline__ void load_w(const float *p, int64_t i, int live, floa
     for (int e = 0; e < V; ++e) x[e] = p && (VEC ? live > 0 : e < live) ? p[i + e] : none;
 }
 
+// u and v summed over the `rows` threads of a workgroup that hold the same channels, `stride` threads apart (this
+// one is number `row`; `rows` or more: none of them), in LDS and in a fixed order. The first of them gets the
+// sums; every thread of the workgroup takes part
+template <int N>
+__device__ __forceinline__ void join_rows(float (&u)[N], float (&v)[N], int row, int rows, int stride,
+                                          float (*lds)[kThreads]) {
+    if (rows == 1) return;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        lds[e][threadIdx.x] = u[e];
+        lds[N + e][threadIdx.x] = v[e];
+    }
+    for (int k = kThreads / 2; k > 0; k >>= 1) {
+        if (k >= rows) continue;
+        __syncthreads();
+        if (row < k && row + k < rows) {
+#pragma unroll
+            for (int e = 0; e < 2 * N; ++e) lds[e][threadIdx.x] += lds[e][threadIdx.x + k * stride];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        u[e] = lds[e][threadIdx.x];
+        v[e] = lds[N + e][threadIdx.x];
+    }
+}
+
 // ------------------------------------------------------------------ tokens ---
 // Slots of L lanes, one group each: slots of a pass cover groups blockIdx.y * slots .. or, with
 // fewer groups than slots, several rows. CH pieces of L * V channels a group.
@@ -237,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void token_fwd_kernel(const NormArgs a) {
     }
 }
 
-// chan: [gridDim.x * rows of a pass][2][C]
+// chan: [gridDim.x][2][C]
 template <bool BF16, int L, int CH, bool VEC, bool GATE>
 __global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
     constexpr int V = BF16 ? 8 : 4;
@@ -301,16 +332,20 @@ __global__ __launch_bounds__(kThreads) void token_bwd_kernel(const NormArgs a) {
             if constexpr (GATE) store<BF16, V, VEC>(a.dz, row * a.C + s.c[k], live, z[k], a.past);
         }
     }
-    if (s.rows && a.chan) {
-        float *p = a.chan + ((int64_t)blockIdx.x * s.rows + s.row0) * 2 * a.C;
+    if (a.chan) {
+        __shared__ float lds[2 * V][kThreads];
+        float *p = a.chan + (int64_t)blockIdx.x * 2 * a.C;
+        const int rows = end - first < step ? (int)(end - first) : step;  // (the others have no sums)
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
+        for (int k = 0; k < CH; ++k) {
+            join_rows<V>(dw[k], db[k], s.rows ? s.row0 : rows, rows, a.G * L, lds);
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (VEC ? s.live[k] > 0 : e < s.live[k]) {
+                if (s.row0 == 0 && (VEC ? s.live[k] > 0 : e < s.live[k])) {
                     p[s.c[k] + e] = dw[k][e];
                     p[a.C + s.c[k] + e] = db[k][e];
                 }
+        }
     }
 }
 
@@ -703,10 +738,11 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
         // 146, with one 205)
         const int64_t wgs = p.gy < 512 ? 512 / p.gy : 1;
         if (bwd && ceil_div(s.rows, p.pass * passes) > wgs) passes = ceil_div(s.rows, p.pass * wgs);
-        if (ceil_div(s.rows, p.pass * passes) > (1 << 20)) passes = ceil_div(s.rows, (int64_t)p.pass << 20);
+        if (bwd && passes > kChain) passes = kChain;
+        if (!bwd && ceil_div(s.rows, p.pass * passes) > (1 << 20)) passes = ceil_div(s.rows, (int64_t)p.pass << 20);
         p.rows_wg = p.pass * passes;
         p.gx = ceil_div(s.rows, p.rows_wg);
-        if (bwd) p.total = p.chan_bytes = up((size_t)(p.gx * p.pass) * 2 * C * 4);
+        if (bwd) p.total = p.chan_bytes = up((size_t)p.gx * 2 * C * 4);
         return p;
     }
     p.V = D % V == 0 ? V : 1;
@@ -854,7 +890,7 @@ m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, 
         if (bwd) e = launch_channel_sums(a, 0, hs);  // zeros
     } else if (p.token) {
         e = bf16 ? launch_tokens<true>(a, p, bwd, hs) : launch_tokens<false>(a, p, bwd, hs);
-        if (bwd && e == hipSuccess) e = launch_channel_sums(a, p.gx * p.pass, hs);
+        if (bwd && e == hipSuccess) e = launch_channel_sums(a, p.gx, hs);
     } else if (bf16) {
         e = p.V > 1 ? launch_seq<true, 8>(a, p, bwd, hs) : launch_seq<true, 1>(a, p, bwd, hs);
     } else {
