@@ -709,7 +709,8 @@ struct NormPlan {
     int64_t rows_wg, gx;  // tokens: rows of a workgroup, workgroups along the rows
     int gy, pass;         // tokens: workgroups along the groups, rows of a pass
     int64_t slice;        // sequences
-    int nslice, vb, pg, pieces, vblocks, V;
+    int64_t nslice;
+    int vb, pg, pieces, vblocks, V;
     size_t part_bytes, chan_bytes, stats_bytes, total;
 };
 
@@ -765,8 +766,9 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
     n = n > most ? most : n;
     n = n < 1 ? 1 : n;
     p.slice = ceil_div(ceil_div(s.positions, n), p.pg) * p.pg;
+    if (p.slice > kChain * p.pg) p.slice = kChain * p.pg;
     if (p.slice < 1) p.slice = 1;
-    p.nslice = s.positions > 0 ? (int)ceil_div(s.positions, p.slice) : 1;
+    p.nslice = s.positions > 0 ? ceil_div(s.positions, p.slice) : 1;
     p.part_bytes = up((size_t)s.rows * G * p.nslice * p.pieces * 16);
     if (bwd) p.chan_bytes = up((size_t)s.rows * p.nslice * p.pg * 8 * C);
     p.stats_bytes = up((size_t)s.rows * G * 16);
@@ -879,7 +881,7 @@ m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, 
     // x, y and the gate, dy, dx and the gate's
     const int64_t bytes = a.n * a.S * a.C * (s.io_dtype == M3_BF16 ? 2 : 4) * ((bwd ? 3 : 2) + (a.z ? (bwd ? 2 : 1) : 0));
     a.past = bytes > kLastCache;
-    a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = p.nslice; a.vb = p.vb; a.pg = p.pg; a.pieces = p.pieces;
+    a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = (int)p.nslice; a.vb = p.vb; a.pg = p.pg; a.pieces = p.pieces;
     char *ws = static_cast<char *>(workspace);
     a.part = reinterpret_cast<float *>(ws);
     a.stats = reinterpret_cast<float *>(ws + p.part_bytes);

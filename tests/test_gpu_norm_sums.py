@@ -33,3 +33,21 @@ def test_tokens_of_many_rows():
     d = float(torch.tensor(0.1))
     near("bias", g["bias"], torch.full((2 * G,), rows * d, dtype=torch.float64, device="cuda"))
     near("weight", g["weight"], rows * d / (1 + EPS) ** 0.5 * x[0].double())
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_many_long_sequences(ragged):
+    """512 rows of 4096 positions of 43 groups of three channels: 1, -1 and 0, dy 0.1."""
+    from state_space_sequence_amd import m3
+    rows, S, G = 512, 4096, 43
+    x = torch.tensor([1.0, -1.0, 0.0], device="cuda").repeat(G).expand(rows, S, 3 * G).contiguous()
+    dy = torch.full_like(x, 0.1)
+    w = torch.ones(3 * G, device="cuda")
+    lengths = torch.arange(S, S - rows, -1, dtype=torch.int32, device="cuda") if ragged else None
+    g = m3.group_norm_bwd(x, G, dy, w, w, activation="none", eps=EPS, over="sequence", lengths=lengths)
+    torch.cuda.synchronize()
+    n = int(lengths.sum()) if ragged else rows * S
+    d = float(torch.tensor(0.1))
+    near("bias", g["bias"], torch.full((3 * G,), n * d, dtype=torch.float64, device="cuda"))
+    live = x[0, 0] != 0
+    near("weight", g["weight"][live], (n * d / (2.0 / 3 + EPS) ** 0.5 * x[0, 0].double())[live])
