@@ -13,7 +13,8 @@
  *     positions). What lies behind them is not read into any result, and the
  *     outputs and gradients there are written as 0.
  *   weight, bias [channels] fp32 or NULL (ones, zeros). x, z, y: io dtype. Statistics and
- * sums are fp32 (the sums over rows fp64); each output is rounded once.
+ * sums are fp32 for at most 256 rows or positions, one after another, and fp64 beyond; each
+ * output is rounded once.
  *
  * Conventions as in m3.h: dense row-major tensors, 16-byte aligned pointers, the
  * caller owns every buffer and the workspace (contents need not be initialised

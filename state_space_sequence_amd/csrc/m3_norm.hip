@@ -53,7 +53,7 @@ struct NormArgs {
     // tokens: rows of a workgroup. sequences: positions of a slice, slices; vectors of a workgroup,
     // positions it takes at a time, workgroups that share a group
     int64_t rows_wg, slice;
-    int nslice, vb, pg, pieces;
+    int nslice, vb, pg, pieces, sweep;  // (sweep: slices of a workgroup that sums gradients)
     float *part, *chan;  // partial sums: of groups, of channels (tokens and sequences)
     float *stats;        // [n, G, 4]: mean, 1/std, mean of d, mean of d xh
 };
@@ -358,15 +358,18 @@ struct Lane {
     int64_t len;
     int c, po, step;
     int lv, run;   // this thread's vector in its group's part here, and the vectors of that part
+    int g, piece;
     int64_t entry; // where the part's partial sums go
     bool idle;
-    __device__ __forceinline__ Lane(const NormArgs &a, bool whole) {
-        const int dv = a.D / V, cv = a.C / V, slice = (int)(blockIdx.x % (unsigned)a.nslice);
-        row = blockIdx.x / (unsigned)a.nslice;
+    __device__ __forceinline__ Lane(const NormArgs &a, bool whole) : Lane(a) { take(a, blockIdx.x, whole); }
+    // (without a slice yet)
+    __device__ __forceinline__ explicit Lane(const NormArgs &a) {
+        const int dv = a.D / V, cv = a.C / V;
         const int lane = (int)threadIdx.x % a.vb;
         po = (int)threadIdx.x / a.vb;
         step = a.pg;
-        int v, g, piece = 0;
+        int v;
+        piece = 0;
         if (a.pieces == 1) {
             v = (int)blockIdx.y * a.vb + lane;
             g = v / dv;
@@ -381,6 +384,11 @@ struct Lane {
         }
         idle = v >= cv || po >= a.pg || lv >= run;
         c = v * V;
+    }
+    // slice `id` of all rows' slices
+    __device__ __forceinline__ void take(const NormArgs &a, unsigned id, bool whole) {
+        const int slice = (int)(id % (unsigned)a.nslice);
+        row = id / (unsigned)a.nslice;
         entry = ((row * a.G + g) * a.nslice + slice) * a.pieces + piece;
         len = a.S;
         if (a.lengths) {
@@ -561,56 +569,72 @@ __device__ __forceinline__ void seq_du(const NormArgs &a, float mean, float r, c
     }
 }
 
-// Sums of du xh and du of every channel, chan [n, nslice, pg][2][C], and of d and d xh of a group's
-// part of a slice, part [n, G, nslice, pieces, 4]
+// Sums of du xh and du of every channel, chan [gridDim.x][2][C], and of d and d xh of a group's part of a slice,
+// part [n, G, nslice, pieces, 4]. A workgroup takes `sweep` slices, one after another
 template <bool BF16, int V, bool GATE>
 __global__ __launch_bounds__(kThreads) void seq_sums_kernel(const NormArgs a) {
     __shared__ f32x2 lds[kThreads];
-    const Lane<V> t(a, false);
-    float sa = 0.f, sb = 0.f;
-    if (!t.idle) {
-        const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
-        const float mean = st[0], r = st[1];
-        float w[V], b[V], dw[V], db[V];
-        load_w<V, true>(a.w, t.c, V, 1.f, w);
-        load_w<V, true>(a.b, t.c, V, 0.f, b);
+    __shared__ float rows[2 * V][kThreads];
+    Lane<V> t(a);
+    float w[V], b[V], dw[V], db[V];
+    load_w<V, true>(a.w, t.c, t.idle ? 0 : V, 1.f, w);
+    load_w<V, true>(a.b, t.c, t.idle ? 0 : V, 0.f, b);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
-        for (int64_t p = t.p0 + t.po; p < t.p1; p += kAhead * t.step) {
-            float x[kAhead][V], z[kAhead][V], d[kAhead][V];
+    for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+    const unsigned total = (unsigned)(a.n * a.nslice), first = blockIdx.x * (unsigned)a.sweep;
+    for (unsigned id = first; id < total && id < first + (unsigned)a.sweep; ++id) {
+        t.take(a, id, false);
+        float sw[V], sb[V];  // of this slice
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
-                const int live = q < t.p1 ? V : 0;
-                load<BF16, V, true>(a.x, at, live, x[k]);
-                load<BF16, V, true>(a.dy, at, live, d[k]);
-                if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z[k]);
-            }
+        for (int e = 0; e < V; ++e) sw[e] = sb[e] = 0.f;
+        if (!t.idle) {
+            const float *st = a.stats + 4 * (t.row * a.G + t.c / a.D);
+            const float mean = st[0], r = st[1];
+            for (int64_t p = t.p0 + t.po; p < t.p1; p += kAhead * t.step) {
+                float x[kAhead][V], z[kAhead][V], d[kAhead][V];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                seq_du<BF16, V, GATE>(a, mean, r, w, b, x[k], z[k], d[k]);
-                if (p + k * t.step < t.p1) {
+                for (int k = 0; k < kAhead; ++k) {
+                    const int64_t q = p + k * t.step, at = (t.row * a.S + q) * a.C + t.c;
+                    const int live = q < t.p1 ? V : 0;
+                    load<BF16, V, true>(a.x, at, live, x[k]);
+                    load<BF16, V, true>(a.dy, at, live, d[k]);
+                    if constexpr (GATE) load<BF16, V, true>(a.z, at, live, z[k]);
+                }
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        dw[e] = __builtin_fmaf(d[k][e], x[k][e], dw[e]);
-                        db[e] += d[k][e];
+                for (int k = 0; k < kAhead; ++k) {
+                    seq_du<BF16, V, GATE>(a, mean, r, w, b, x[k], z[k], d[k]);
+                    if (p + k * t.step < t.p1) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            sw[e] = __builtin_fmaf(d[k][e], x[k][e], sw[e]);
+                            sb[e] += d[k][e];
+                        }
                     }
                 }
             }
         }
-        float *o = a.chan ? a.chan + ((int64_t)blockIdx.x * a.pg + t.po) * 2 * a.C + t.c : nullptr;
+        f32x2 s = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            if (o) {
+            s[0] = __builtin_fmaf(w[e], sb[e], s[0]);
+            s[1] = __builtin_fmaf(w[e], sw[e], s[1]);
+            dw[e] += sw[e];
+            db[e] += sb[e];
+        }
+        s = t.sum(a, s, lds);
+        if (!t.idle && t.po == 0 && t.lv == 0) *reinterpret_cast<f32x2 *>(a.part + 4 * t.entry) = s;
+    }
+    if (a.chan) {
+        join_rows<V>(dw, db, t.po, a.pg, a.vb, rows);
+        if (!t.idle && t.po == 0) {
+            float *o = a.chan + (int64_t)blockIdx.x * 2 * a.C + t.c;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
                 o[e] = dw[e];
                 o[a.C + e] = db[e];
             }
-            sa = __builtin_fmaf(w[e], db[e], sa);
-            sb = __builtin_fmaf(w[e], dw[e], sb);
         }
     }
-    const f32x2 sab = t.sum(a, f32x2{sa, sb}, lds);
-    if (!t.idle && t.po == 0 && t.lv == 0) *reinterpret_cast<f32x2 *>(a.part + 4 * t.entry) = sab;
 }
 
 // likewise: stats <- means of d and d xh
@@ -711,6 +735,7 @@ struct NormPlan {
     int64_t slice;        // sequences
     int64_t nslice;
     int vb, pg, pieces, vblocks, V;
+    int64_t sweep, sweeps;  // slices of a workgroup of the gradients' sums, and how many such workgroups (times vblocks)
     size_t part_bytes, chan_bytes, stats_bytes, total;
 };
 
@@ -769,8 +794,17 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
     if (p.slice > kChain * p.pg) p.slice = kChain * p.pg;
     if (p.slice < 1) p.slice = 1;
     p.nslice = s.positions > 0 ? ceil_div(s.positions, p.slice) : 1;
-    p.part_bytes = up((size_t)s.rows * G * p.nslice * p.pieces * 16);
-    if (bwd) p.chan_bytes = up((size_t)s.rows * p.nslice * p.pg * 8 * C);
+    // A workgroup that sums gradients takes several short slices, so that about a thousand workgroups (what the CUs have at
+    // once) hold all, as long as a thread's additions stay a chain: the partial sums are at most 32 MB, or a sixteenth of x
+    // (a workgroup a slice and a partial sum a thread: 100000 rows of 4 positions of 64 channels 44 ms and 1.6 GB, now 1.2 ms
+    // and 4 MB; one group of 4096 channels for each of 32768 tokens 1657 us and 1.1 GB, now 765 and 18 MB)
+    const int64_t slices = s.rows * p.nslice, chain = ceil_div(p.slice, p.pg);
+    p.sweep = slices * p.vblocks / 1024;
+    if (p.sweep > kChain / chain) p.sweep = kChain / chain;
+    if (p.sweep < 1) p.sweep = 1;
+    p.sweeps = ceil_div(slices, p.sweep);
+    p.part_bytes = up((size_t)slices * G * p.pieces * 16);
+    if (bwd) p.chan_bytes = up((size_t)p.sweeps * 8 * C);
     p.stats_bytes = up((size_t)s.rows * G * 16);
     p.total = p.part_bytes + p.chan_bytes + p.stats_bytes;
     return p;
@@ -848,7 +882,7 @@ hipError_t launch_channel_sums(const NormArgs &a, int64_t rows, hipStream_t s) {
 
 template <bool BF16, int V>
 hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_t s) {
-    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), t(kThreads);
+    const dim3 g((unsigned)(a.n * a.nslice), (unsigned)p.vblocks), gs((unsigned)p.sweeps, (unsigned)p.vblocks), t(kThreads);
     // (a workgroup a (row, group) where the partial sums are more than a wave takes at once)
     const bool many = a.nslice * a.pieces > 64 && a.n * a.G <= kMaxGrid;
     const dim3 j((unsigned)(many ? a.n * a.G : ceil_div(a.n * a.G, kThreads / 64)));
@@ -863,8 +897,8 @@ hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_
         else hipLaunchKernelGGL((seq_fwd_kernel<BF16, V, false>), g, t, 0, s, a);
         return hipGetLastError();
     }
-    if (a.z) hipLaunchKernelGGL((seq_sums_kernel<BF16, V, true>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((seq_sums_kernel<BF16, V, false>), g, t, 0, s, a);
+    if (a.z) hipLaunchKernelGGL((seq_sums_kernel<BF16, V, true>), gs, t, 0, s, a);
+    else hipLaunchKernelGGL((seq_sums_kernel<BF16, V, false>), gs, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (many) hipLaunchKernelGGL(seq_join_sums_kernel<kThreads>, j, t, 0, s, a);
     else hipLaunchKernelGGL(seq_join_sums_kernel<64>, j, t, 0, s, a);
@@ -872,7 +906,7 @@ hipError_t launch_seq(const NormArgs &a, const NormPlan &p, bool bwd, hipStream_
     if (a.z) hipLaunchKernelGGL((seq_bwd_kernel<BF16, V, true>), g, t, 0, s, a);
     else hipLaunchKernelGGL((seq_bwd_kernel<BF16, V, false>), g, t, 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    return launch_channel_sums(a, a.n * a.nslice * a.pg, s);
+    return launch_channel_sums(a, p.sweeps, s);
 }
 
 m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, void *workspace, hipStream_t hs) {
@@ -882,6 +916,7 @@ m3_status run(const m3_norm_shape &s, const NormPlan &p, NormArgs &a, bool bwd, 
     const int64_t bytes = a.n * a.S * a.C * (s.io_dtype == M3_BF16 ? 2 : 4) * ((bwd ? 3 : 2) + (a.z ? (bwd ? 2 : 1) : 0));
     a.past = bytes > kLastCache;
     a.rows_wg = p.rows_wg; a.slice = p.slice; a.nslice = (int)p.nslice; a.vb = p.vb; a.pg = p.pg; a.pieces = p.pieces;
+    a.sweep = (int)p.sweep;
     char *ws = static_cast<char *>(workspace);
     a.part = reinterpret_cast<float *>(ws);
     a.stats = reinterpret_cast<float *>(ws + p.part_bytes);
