@@ -1477,10 +1477,13 @@ m3_status m3_linattn_bwd(const m3_shape *shape, const m3_linattn_io *io, const m
 }
 
 m3_status m3_linattn_step(const m3_shape *shape, const m3_linattn_step_io *io, void *stream) {
-    const m3_status st = lin_check(shape, M3_FLAG_BF16_STATE);
+    if (!shape) return M3_ERR_INVALID_ARG;
+    m3_shape s = *shape;
+    s.seqlen = 1;
+    s.nsegments = 0;  // (neither is used)
+    const m3_status st = lin_check(&s, M3_FLAG_BF16_STATE);
     if (st != M3_OK) return st;
     if (!io || !isfinite(io->scale)) return M3_ERR_INVALID_ARG;
-    const m3_shape &s = *shape;
     if (s.batch == 0) return M3_OK;
     if (!io->q || !io->k || !io->v || !io->log_decay || !io->h || !io->y) return M3_ERR_INVALID_ARG;
     const void *ptrs[] = {io->q, io->k, io->v, io->log_decay, io->h, io->y};
