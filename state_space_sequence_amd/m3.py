@@ -647,6 +647,8 @@ def _linattn_dims(q, k, v, ndim):
     v [*lead, G, P]."""
     _need("k", k)
     qs, vs = _dims5("q", q, ndim), _dims5("v", v, ndim)
+    if qs[-1] == 0:
+        raise ValueError("q: no keys, got shape %s" % (qs,))
     return qs[:-2], qs[-2], vs[-2], qs[-1], vs[-1]
 
 

@@ -1,10 +1,12 @@
-"""Edges of the linear attention calls on the host (no GPU needed): what a step does not use."""
+"""Edges of the linear attention calls on the host (no GPU needed): what a step does not use, and
+sizes that the binding leaves to the library to refuse."""
 from __future__ import annotations
 
 import ctypes
 import os
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LIB = os.path.join(ROOT, "state_space_sequence_amd", "libm3.so")
@@ -31,3 +33,16 @@ def test_a_step_does_not_use_the_length(m3, seqlen, nsegments):
     assert step() == -1  # no tensors
     s.dstate = 257
     assert step() == -2
+
+
+def test_no_keys(m3):
+    """Tensors without a key dimension are refused like other sizes, not by the default scale's division."""
+    b, L, H, G, P = 2, 10, 4, 2, 16
+    q, k, v = torch.zeros(b, L, H, 0), torch.zeros(b, L, G, 0), torch.zeros(b, L, G, P)
+    ld, dy = torch.zeros(H), torch.zeros(b, L, H, P)
+    with pytest.raises(ValueError, match="q"):
+        m3.linattn_fwd(q, k, v, ld)
+    with pytest.raises(ValueError, match="q"):
+        m3.linattn_bwd(q, k, v, ld, dy)
+    with pytest.raises(ValueError, match="q"):
+        m3.linattn_step(q[:, 0], k[:, 0], v[:, 0], ld, torch.zeros(b, H, P, 0))
