@@ -1,5 +1,5 @@
 """Edges of the linear attention calls on the host (no GPU needed): what a step does not use, and
-sizes that the binding leaves to the library to refuse."""
+tensors without keys."""
 from __future__ import annotations
 
 import ctypes
