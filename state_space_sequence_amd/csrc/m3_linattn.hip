@@ -30,9 +30,11 @@
 // columns: bf16 through the transposing LDS read (each lane of 16 names 4 consecutive elements of
 // one of 4 rows and gets 4 rows of one column), fp32 element by element.
 //
-// bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 335 us, 205 TFLOP/s of useful products (76 of a wave's 126
-// products a chunk are those of the further parts of its operands), 2.8 TB/s; the bytes alone would take 157 us. b2 L32768 of 24
-// heads in ten segments: 416 us. Gradients of b8 L2048, 16 heads of 128 x 128: 423 us, of them d log_decay
+// bf16, b8 L4096 of 64 query heads on 8, 128 keys, 64 values: 333 us, 206 TFLOP/s of useful products (76 of a wave's 126
+// products a chunk are those of the further parts of its operands), 2.8 TB/s; the bytes alone would take 157 us. No unit is
+// full: vector issue takes 51% of the cycles, the LDS 50%, the matrix cores 41%, at 1.87 GHz; two waves a SIMD (registers:
+// the state, a step's fragments, the next chunk) wait for each other. b2 L32768 of 24
+// heads in ten segments: 414 us. Gradients of b8 L2048, 16 heads of 128 x 128: 417 us, of them d log_decay
 // about 0.4, bound by the vector instructions of its splits. fp32 runs on the fp32 matrix cores in chunks of 32.
 #include <math.h>
 
@@ -99,7 +101,7 @@ struct Ops<uint16_t> {
     static constexpr int C = 64;   // tokens of a chunk
     // Parts of an operand that is no input (a state, a score, a weighted value): 3 of 8 bits hold all 24 of fp32. With two
     // parts of a state and of a score, 16 bits, 0.22% of the bf16 outputs land on the other side of a rounding
-    // from the fp32 form's, with three 0.02%, what the order of fp32 sums gives; b8 L4096 takes 335 us instead of 299
+    // from the fp32 form's, with three 0.02%, what the order of fp32 sums gives; b8 L4096 takes 333 us instead of 297
     static constexpr int kParts = 3;
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -1069,8 +1071,8 @@ int key_size(int64_t d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 // Segments. A pass has a workgroup a chain and tile of values (the backward runs three passes at
 // once), and a CU has room for two, or for one with 256 keys. Splitting reads k and v twice, about 1.45 times
 // the work, and two workgroups of a CU run at 0.6 of the speed of one: two segments that fill the
-// second place cost more than they bring (b4 L2048, 256 workgroups: 95 us in one piece, 124 in
-// two), three or more pay (48 workgroups of L32768: 1310 us in one piece, 401 in ten). Segments have two
+// second place cost more than they bring (b4 L2048, 256 workgroups: 110 us in one piece, 138 in
+// two), three or more pay (48 workgroups of L32768: 1487 us in one piece, 414 in ten). Segments have two
 // chunks at least; below six chunks the two launches more cost as much as they save.
 LinPlan make_lin_plan(const m3_shape &s, bool bwd) {
     LinPlan p{};
@@ -1317,8 +1319,8 @@ hipError_t segment_states(Args a, bool bf16, float *st, float *ut, hipStream_t s
     a.s_in = nullptr; a.s_out = st; a.u_out = ut;
     if (ut) return launch_pass<kStateU>(a, bf16, s);
     // (heads or tiles of values that read the same rows find them in the caches; else these would only hold what the
-    // outputs' pass reads long after: b2 L32768 of 24 heads 401 us, with ordinary loads 414;
-    // b1 L65536 of 16 heads 271 and 284)
+    // outputs' pass reads long after: b2 L32768 of 24 heads 413 us, with ordinary loads 425;
+    // b1 L65536 of 16 heads 275 and 287)
     return a.k.per == 1 && a.v.per == 1 && a.nvt == 1 ? launch_pass<kStateOnce>(a, bf16, s) : launch_pass<kState>(a, bf16, s);
 }
 

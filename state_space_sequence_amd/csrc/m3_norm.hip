@@ -10,10 +10,10 @@
 // Tokens by themselves (one position a row): the lanes of a group (L of them, each with 16 bytes of
 // its channels) hold it in registers, so one pass is enough: the variance is taken of
 // the differences to the mean, and the sums go across lanes by DPP moves. A lane keeps
-// its channels from row to row: weights, and the sums for dw and db, stay in registers.
+// its channels from row to row: weights, and the sums for dw and db, stay in registers, and a workgroup's are joined in LDS.
 //
-// Sequences: partial sums of a slice of the positions (a thread keeps its channels), joined in a
-// fixed order by one workgroup a group, then one elementwise pass. Slices' means and
+// Sequences: partial sums of a slice of the positions (a thread keeps its channels; the sums for dw and db from one
+// short slice to the next), joined in a fixed order by one workgroup a group, then one elementwise pass. Slices' means and
 // squared differences are joined, not raw squares, which would lose the variance of
 // values far from 0. The backward needs the sums of du and du xh of every channel
 // only: the group's means of d and d xh are their products with w.
@@ -785,7 +785,7 @@ NormPlan make_plan(const m3_norm_shape &s, bool lengths, bool bwd) {
     }
     p.pg = kThreads / p.vb;
     // Slices: two workgroups a CU, of eight positions a thread at least. More slices are more partial sums (gradients of
-    // b8 L4096 of 4096 channels with a gate: 472 us, with eight a CU 613, with one 507; b1 of 320 channels 41, 40, 50)
+    // b8 L4096 of 4096 channels with a gate: 455 us, with eight a CU 560, with one 503; b1 of 320 channels 40, 37, 50)
     int64_t n = ceil_div(512, (s.rows > 0 ? s.rows : 1) * p.vblocks);
     const int64_t most = ceil_div(s.positions, 8 * p.pg);
     n = n > most ? most : n;
