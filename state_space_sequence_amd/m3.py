@@ -82,6 +82,26 @@ class NormGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "dx", "dz", "dweight", "dbias")]
 
 
+class RecShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("nsegments", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RecIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "x", "decay_gate", "input_gate", "log_decay", "h0", "lengths", "y", "h_final", "states")]
+
+
+class RecGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "dy", "dh_final", "dx", "ddecay_gate", "dinput_gate", "dlog_decay", "dh0")]
+
+
+class RecStepIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "decay_gate", "input_gate", "log_decay", "h", "y")]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("nsegments", ctypes.c_int32),
                 ("workgroups", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
@@ -153,6 +173,18 @@ def _load():
         f = getattr(lib, name)
         f.restype = ctypes.c_size_t
         f.argtypes = [ctypes.POINTER(NormShape), ctypes.c_int]
+    lib.m3_recurrence_fwd.restype = ctypes.c_int
+    lib.m3_recurrence_fwd.argtypes = [ctypes.POINTER(RecShape), ctypes.POINTER(RecIO), ctypes.c_void_p, ctypes.c_size_t,
+                                      ctypes.c_void_p]
+    lib.m3_recurrence_workspace_bytes.restype = ctypes.c_size_t
+    lib.m3_recurrence_workspace_bytes.argtypes = [ctypes.POINTER(RecShape)]
+    lib.m3_recurrence_bwd.restype = ctypes.c_int
+    lib.m3_recurrence_bwd.argtypes = [ctypes.POINTER(RecShape), ctypes.POINTER(RecIO), ctypes.POINTER(RecGrads),
+                                      ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.m3_recurrence_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.m3_recurrence_bwd_workspace_bytes.argtypes = [ctypes.POINTER(RecShape), ctypes.c_int]
+    lib.m3_recurrence_step.restype = ctypes.c_int
+    lib.m3_recurrence_step.argtypes = [ctypes.POINTER(RecShape), ctypes.POINTER(RecStepIO), ctypes.c_void_p]
     return lib
 
 
@@ -857,6 +889,137 @@ def group_norm_bwd(x, groups, dy, weight=None, bias=None, *, z=None, activation=
     _on_gpu(dev)
     _launch(lib.m3_group_norm_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs), ws, wsb)
     return grads
+
+
+# ----------------------------------- gated linear recurrence, one state a channel ---
+M3_REC_KEEP = 64  # tokens between two kept states
+M3_REC_UNSCALED = 1
+
+
+def recurrence_shape(x, nsegments=0, scaled=True) -> RecShape:
+    """The shape of x [b,L,C]."""
+    b, L, C = x.shape
+    return RecShape(b, L, C, _io_dtype(x), 0 if scaled else M3_REC_UNSCALED, nsegments, 0)
+
+
+def recurrence_workspace_bytes(shape: RecShape) -> int:
+    return int(lib.m3_recurrence_workspace_bytes(ctypes.byref(shape)))
+
+
+def recurrence_bwd_workspace_bytes(shape: RecShape, states=False) -> int:
+    return int(lib.m3_recurrence_bwd_workspace_bytes(ctypes.byref(shape), bool(states)))
+
+
+def _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegments, scaled):
+    """The shape and the inputs of a recurrence over x [b,L,C], checked."""
+    b, L, C = _dims5("x", x, 3)
+    iot, io, f32, dev, s = _io_dtype(x), x.dtype, torch.float32, x.get_device(), x.shape
+    if C == 0:
+        raise ValueError("x: no channels, got shape %s" % (tuple(s),))
+    _need("decay_gate", decay_gate)
+    _need("log_decay", log_decay)
+    ptrs = RecIO(_arg("x", x, s, io, dev), _arg("decay_gate", decay_gate, s, io, dev),
+                 _arg("input_gate", input_gate, s, io, dev), _arg("log_decay", log_decay, (C,), f32, dev),
+                 _arg("h0", h0, (b, C), f32, dev), _arg("lengths", lengths, (b,), torch.int32, dev), None, None,
+                 _arg("states", states, (b, -(-L // M3_REC_KEEP), C), f32, dev))
+    return RecShape(b, L, C, iot, 0 if scaled else M3_REC_UNSCALED, nsegments, 0), ptrs
+
+
+def recurrence_fwd(x, decay_gate, log_decay, *, input_gate=None, h0=None, lengths=None, scaled=True, y=None,
+                   h_final=None, want_state=True, states=None, want_states=False, workspace=None, nsegments=0,
+                   stream=None):
+    """Gated linear recurrence over a prompt, one state a channel (m3_recurrence_fwd):
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t with a_t = exp(log_decay *
+    sigmoid(decay_gate_t)), y_t = h_t. x and the gates [b,L,C] (fp32 or bf16; no input gate: 1),
+    log_decay [C] fp32 <= 0, h0 [b,C] fp32, lengths [b] int32: row i has lengths[i] tokens, y is 0
+    behind them and the state is the one after them. scaled=False: without sqrt(1 - a^2). Returns
+    (y, h_final [b,C] fp32 or None), and with want_states (or states) a third, the states that
+    recurrence_bwd takes: [b, ceil(L/64), C] fp32."""
+    shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegments, scaled)
+    b, L, C = x.shape
+    f32, dev = torch.float32, x.get_device()
+    ptrs.y, ptrs.h_final = _arg("y", y, x.shape, x.dtype, dev), _arg("h_final", h_final, (b, C), f32, dev)
+    ws, wsb = _workspace(workspace, dev)
+    _on_gpu(dev)
+    need = lib.m3_recurrence_workspace_bytes(ctypes.byref(shape))
+    with _owned_by(stream):
+        if y is None:
+            y = x.new_empty(x.shape)
+            ptrs.y = y.data_ptr()
+        if h_final is None and want_state:
+            h_final = torch.empty((b, C), dtype=f32, device=x.device)
+            ptrs.h_final = h_final.data_ptr()
+        if states is None and want_states:
+            states = torch.empty((b, -(-L // M3_REC_KEEP), C), dtype=f32, device=x.device)
+            ptrs.states = states.data_ptr()
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws, wsb = workspace.data_ptr(), need
+    _launch(lib.m3_recurrence_fwd, x.device, stream, ctypes.byref(shape), ctypes.byref(ptrs), ws, wsb)
+    return (y, h_final) if states is None else (y, h_final, states)
+
+
+def recurrence_bwd(x, decay_gate, log_decay, dy, *, input_gate=None, h0=None, lengths=None, scaled=True, dh_final=None,
+                   states=None, want_dh0=True, want_dlog_decay=True, workspace=None, grads=None, nsegments=0,
+                   stream=None):
+    """Gradients of <dy, y> + <dh_final, h_final> of recurrence_fwd (m3_recurrence_bwd). states: what the
+    forward call kept (h0 is then not read); without them the recurrence runs over the sequence once
+    more. Returns a dict: x, decay_gate and, with an input gate, input_gate in the dtype of x;
+    log_decay [C] and h0 [b,C] in fp32 where wanted. grads: such a dict to write into (x and the
+    gates required)."""
+    shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegments, scaled)
+    _need("dy", dy)
+    b, _, C = x.shape
+    io, s, f32, dev = x.dtype, x.shape, torch.float32, x.get_device()
+    gs = RecGrads(_arg("dy", dy, s, io, dev), _arg("dh_final", dh_final, (b, C), f32, dev))
+    ws, wsb = _workspace(workspace, dev)
+    need = lib.m3_recurrence_bwd_workspace_bytes(ctypes.byref(shape), states is not None)
+    required = ("x", "decay_gate") if input_gate is None else ("x", "decay_gate", "input_gate")
+    with _owned_by(stream):
+        if grads is None:
+            grads = {name: torch.empty(s, dtype=io, device=x.device) for name in required}
+            if want_dlog_decay:
+                grads["log_decay"] = torch.empty((C,), dtype=f32, device=x.device)
+            if want_dh0:
+                grads["h0"] = torch.empty((b, C), dtype=f32, device=x.device)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws, wsb = workspace.data_ptr(), need
+    want = {"log_decay": ((C,), f32), "h0": ((b, C), f32)}
+    for name in required:
+        want[name] = (s, io)
+    for name, t in grads.items():
+        if name not in want:
+            raise ValueError("grads: unknown entry %r" % name)
+        setattr(gs, "d" + name, _arg("grads[%r]" % name, t, *want[name], dev))
+    for name in required:
+        _need("grads[%r]" % name, grads.get(name))
+    _on_gpu(dev)
+    _launch(lib.m3_recurrence_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(ptrs), ctypes.byref(gs), ws, wsb)
+    return grads
+
+
+def recurrence_step(x, decay_gate, log_decay, h, *, input_gate=None, scaled=True, y=None, stream=None):
+    """One token of recurrence_fwd (m3_recurrence_step): x and the gates [b,C], the state h [b,C] fp32
+    updated in place. Returns y [b,C]."""
+    b, C = _dims5("x", x, 2)
+    iot, io, f32, dev, s = _io_dtype(x), x.dtype, torch.float32, x.get_device(), x.shape
+    if C == 0:
+        raise ValueError("x: no channels, got shape %s" % (tuple(s),))
+    _need("decay_gate", decay_gate)
+    _need("log_decay", log_decay)
+    _need("h", h)
+    ptrs = RecStepIO(_arg("x", x, s, io, dev), _arg("decay_gate", decay_gate, s, io, dev),
+                     _arg("input_gate", input_gate, s, io, dev), _arg("log_decay", log_decay, (C,), f32, dev),
+                     _arg("h", h, s, f32, dev), _arg("y", y, s, io, dev))
+    _on_gpu(dev)
+    shape = RecShape(b, 1, C, iot, 0 if scaled else M3_REC_UNSCALED, 0, 0)
+    if y is None:
+        with _owned_by(stream):
+            y = x.new_empty(s)
+        ptrs.y = y.data_ptr()
+    _launch(lib.m3_recurrence_step, x.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
+    return y
 
 
 # ------------------------------------------------------ calibration probes ---
