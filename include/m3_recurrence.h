@@ -10,8 +10,8 @@
  *   y_t = h_t
  *
  * With M3_REC_UNSCALED the factor sqrt(1 - a_t^2) is 1. m3_recurrence_fwd evaluates
- * a prompt (tokens in chunks, chunks joined by their decay and end state),
- * m3_recurrence_bwd gives the gradients, m3_recurrence_step advances one token.
+ * a prompt (in tiles of 128 tokens, each joined to those before it by their decays
+ * and end states), m3_recurrence_bwd gives the gradients, m3_recurrence_step advances one token.
  *
  *   x, decay_gate, input_gate, y [b,L,C]   io dtype
  *   log_decay [C] fp32: finite and <= 0
@@ -24,9 +24,9 @@
  *     index is a multiple of M3_REC_KEEP (behind a row's length: the last one). The
  *     forward writes it where it is given; the backward then need not run the
  *     recurrence over the sequence again first.
- * C: 1 to 2^20; even C load fastest in bf16. b * L <= 2^40, and b times C / 64 times
- * the segments below 2^23 (else M3_ERR_UNSUPPORTED). States, gates and sums are fp32,
- * sums over tokens and rows fp64 beyond 8 terms; each output is rounded once. 1 - a_t
+ * C: 1 to 2^20; even C load fastest in bf16. b * L <= 2^40, and b times the tiles of 64
+ * channels times those of 64 tokens below 2^24 (else M3_ERR_UNSUPPORTED). States, gates and sums are fp32,
+ * sums over tokens and rows fp64 beyond 16 terms (joined from fp32 sums of 64); each output is rounded once. 1 - a_t
  * is formed without cancellation, so slow decays keep their input. Where
  * 1 - a_t^2 is 0 (a log_decay of 0), an input has no effect and no gradient.
  *
@@ -59,8 +59,6 @@ typedef struct {
     int64_t channels;  /* >= 1, up to 2^20 */
     int32_t io_dtype;  /* m3_dtype of x, gates, y and their gradients */
     uint32_t flags;    /* 0 or M3_REC_UNSCALED */
-    int32_t nsegments; /* 0 picks the split of the sequence, 1 none, k > 1 about k segments */
-    int32_t reserved;  /* 0 */
 } m3_rec_shape;
 
 typedef struct {
@@ -105,7 +103,7 @@ m3_status m3_recurrence_bwd(const m3_rec_shape *shape, const m3_rec_io *io, cons
 /* Likewise of m3_recurrence_bwd; states: whether the call passes them. */
 size_t m3_recurrence_bwd_workspace_bytes(const m3_rec_shape *shape, int states);
 
-/* One token: the state is updated in place, y written. seqlen and nsegments are not used. */
+/* One token: the state is updated in place, y written. seqlen is not used. */
 m3_status m3_recurrence_step(const m3_rec_shape *shape, const m3_rec_step_io *io, void *stream);
 
 #ifdef __cplusplus

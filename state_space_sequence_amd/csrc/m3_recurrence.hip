@@ -5,13 +5,25 @@
 //   G_t = a_t (dy_t + G_{t+1}) is the gradient of h_{t-1}; with E_t = dy_t + G_{t+1}, that of h_t:
 //   dx = E m g, di = E m x g (1-g), d(ld s) = E (a h_{t-1} - g x a^2 / m), dr = d(ld s) ld s (1-s), dld = sum d(ld s) s
 //
-// A step is the map h -> A h + B, and maps in a row are one map again: (A2 A1, A2 B1 + B2). A workgroup of kW
-// waves owns 64 lanes of channels (one of fp32, two of bf16: 4 bytes each) of a row and walks a segment of its tokens in chunks of
-// kW x kT: a wave forms the gates of its kT tokens and their joint map, the maps meet in LDS, and each wave runs its tokens
-// from the state that the maps before it give. The next chunk is loaded meanwhile. Backwards the same
-// in both directions at once: states forwards from the kept one, G backwards from the chunk behind.
-// With few channels the sequence is split: the map of each segment first, then all segments, from the maps before them.
+// A step is the map h -> A h + B, and maps in a row are one map again: (A2 A1, A2 B1 + B2). A workgroup of eight waves has a
+// column of 64 lanes of channels (4 bytes each) of a row and takes its tokens tile by tile: a wave forms the gates of its
+// run of 16 tokens (8 with gradients), all in registers, and their joint map; the maps of the runs meet in LDS, and each wave runs
+// its tokens from the state that the maps before it give. One pass over the data. Backwards the same in both
+// directions at once: states forwards from the kept one at the tile's start, G backwards.
+//
+// With few columns several workgroups share one, and the state that a tile starts from comes through memory (CHAIN). A
+// tile publishes its map as soon as it has it, and the state behind it later; one that needs its start looks at the
+// kWindow tiles before it for the nearest known state and the maps from there. The state behind a tile is
+// A h + B of its joint map wherever it is formed, so the bits do not depend on who was first. A word is written and read
+// by one atomic access and is there whole or not at all, without fences or flags. A wait ends: the tiles of a column are
+// taken in order from a counter, a workgroup does what it took in that order, and a tile needs nothing from later ones.
+//
+// Bound by HBM and, nearly as much, by vector issue: 34 instructions an element, 5 of them exponentials, reciprocals and roots, 53 ns
+// an element of a wave on a SIMD, so 110 us of the prompt's 206. bf16, with an input gate: prompt b8 L4096 of 4096
+// channels 206 us (5.2 TB/s), long b2 L32768 of 2560 in a chain 309 (4.3 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
 #include <math.h>
+
+#include <type_traits>
 
 #include "m3_internal.h"
 #include "m3_recurrence.h"
@@ -19,10 +31,20 @@
 namespace m3i {
 namespace {
 
-constexpr int kT = 8, kW = 8, kChunk = kT * kW, kThreads = 64 * kW;
-static_assert(kChunk == M3_REC_KEEP, "a chunk starts at a kept state");
-constexpr int64_t kMaxGrid = 0x7fffff;  // workgroups of one launch: 2^32 threads
-constexpr unsigned kOutside = 0x80000000u;  // a byte offset behind every buffer (chunks are at most 2^28 bytes)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kW = 8, kThreads = 64 * kW;        // runs of a tile, one a wave
+constexpr int kFwd = 16, kBwd = 8;               // tokens of a run
+constexpr int kWindow = 8;                       // tiles before it that a tile looks at
+constexpr int kSlots = 256;                      // workgroups that run at a time: one a CU
+constexpr int64_t kMaxGrid = 0x7fffff;           // workgroups of one launch: 2^32 threads
+constexpr unsigned kOutside = 0x80000000u;       // a byte offset behind every buffer (tiles are at most 2^29 bytes)
+constexpr uint64_t kEmpty = ~0ull;               // (a word of 64 bits; of 32: its half)
+constexpr int kPast = 2;                         // buffer accesses past the caches
+static_assert(kW * kBwd == M3_REC_KEEP && M3_REC_KEEP % kFwd == 0, "kept states are at the start of runs and of tiles");
 
 struct RecArgs {
     const void *x, *r, *i;
@@ -30,80 +52,69 @@ struct RecArgs {
     const int *lengths;
     void *y;
     float *hf, *states;
-    float *part;  // [b][nseg][2][C]: maps of the segments
-    float *start; // [b][C]: with segments, a copy of the state (the gradient) that they start from: the last one's end may
-                  // be written over it while the others still begin
     const void *dy;
     const float *dhf;
     void *dx, *dr, *di;
-    float *dld, *dh0;
-    double *dpart;  // [b][nseg][C]: sums of dld
+    float *dh0;
+    float *dpart;     // [b][ntile][C]: sums of dld
+    uint64_t *maps;   // [b][ntile][C]: maps of the tiles, in the order of the chain
+    unsigned *ends;   // [b][ntile][C]: the states behind them
+    unsigned *begins; // [b][C]: what the chain starts from
+    unsigned *taken;  // [b][cols]: tiles taken so far
     int64_t L;
-    int C, cols, nseg, nkeep;  // workgroups across the channels, segments, kept states of a row
-    int64_t seg;               // tokens of a segment, whole chunks
-};
-
-// what a workgroup works on
-struct Place {
-    int lane, wave, seg, c;
-    int64_t row, s0, s1, len;  // tokens of the segment; valid tokens of the row
-    bool in;                   // this lane has channels
-    template <int V>
-    static __device__ __forceinline__ Place make(const RecArgs &a) {
-        Place p;
-        p.lane = threadIdx.x & 63;
-        p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int col = blockIdx.x % a.cols, rest = blockIdx.x / a.cols;
-        p.seg = rest % a.nseg;
-        p.row = rest / a.nseg;
-        p.c = (col * 64 + p.lane) * V;
-        p.in = p.c < a.C;
-        p.len = a.L;
-        if (a.lengths) {
-            const int64_t n = a.lengths[p.row];
-            p.len = n < 0 ? 0 : (n < a.L ? n : a.L);
-        }
-        p.s0 = p.seg * a.seg;
-        p.s1 = p.s0 + a.seg < a.L ? p.s0 + a.seg : a.L;
-        return p;
-    }
+    int C, cols, ntile, nkeep;  // tiles across the channels and along the tokens, kept states of a row
+    unsigned columns;           // batch * cols
+    int turns;                  // tiles that a workgroup takes at most, one after another
 };
 
 // V channels of one token of a lane, as they lie in memory, by buffer accesses: what lies
 // behind the buffer reads as 0 and is not written
 template <bool BF16, int V>
 struct Io {
-    static constexpr int B = BF16 ? 2 * V : 4;  // bytes of a lane and token
-    static_assert(BF16 ? V <= 2 : V == 1, "four bytes at most");
+    static constexpr int B = (BF16 ? 2 : 4) * V, W = (B + 3) / 4;  // bytes and words of a lane and token
+    static_assert(B == 2 || B == 4 || B == 8, "an access of two to eight bytes");
+    struct raw { unsigned w[W]; };
     using rsrc_t = decltype(__builtin_amdgcn_make_buffer_rsrc(static_cast<void *>(nullptr), 0, 0, 0));
-    // tokens t0 .. t0 + rows - 1 of a row
-    static __device__ __forceinline__ rsrc_t rows(const RecArgs &a, const void *p, int64_t row, int64_t t0, int64_t n) {
+    // tokens t0 .. t0 + n - 1 of a row
+    static __device__ __forceinline__ rsrc_t rows(const RecArgs &a, const void *p, int64_t row, int64_t t0, int n) {
         constexpr int E = BF16 ? 2 : 4;
         const char *at = static_cast<const char *>(p) + (row * a.L + t0) * a.C * E;
-        n = n < 0 ? 0 : (n < kChunk ? n : kChunk);
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, (int)n * a.C * E, 0x00020000);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, n * a.C * E, 0x00020000);
     }
-    static __device__ __forceinline__ unsigned load(rsrc_t r, unsigned at) {
-        if constexpr (B == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
-        else return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
-    }
-    static __device__ __forceinline__ void unpack(unsigned w, float (&v)[V]) {
-        if constexpr (!BF16) {
-            v[0] = __uint_as_float(w);
+    static __device__ __forceinline__ raw load(rsrc_t r, unsigned at) {
+        raw o;
+        if constexpr (B == 8) {
+            const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, kPast);
+            o.w[0] = w[0];
+            o.w[W - 1] = w[1];
+        } else if constexpr (B == 4) {
+            o.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kPast);
         } else {
-            v[0] = __uint_as_float(w << 16);
-            if constexpr (V > 1) v[V - 1] = __uint_as_float(w & 0xffff0000u);
+            o.w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, kPast);
+        }
+        return o;
+    }
+    // (the words stay packed until here: unpacked ahead, as the compiler would, two paths' values spill)
+    static __device__ __forceinline__ void unpack(raw o, float (&v)[V]) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) asm volatile("" : "+v"(o.w[e]));
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if constexpr (!BF16) v[e] = __uint_as_float(o.w[e]);
+            else v[e] = __uint_as_float(e % 2 ? o.w[e / 2] & 0xffff0000u : o.w[e / 2] << 16);
         }
     }
     static __device__ __forceinline__ void store(rsrc_t r, unsigned at, const float (&v)[V]) {
-        if constexpr (!BF16) {
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, at, 0, 0);
-        } else if constexpr (V == 1) {
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[0]), r, at, 0, 0);
-        } else {
-            const unsigned lo = __builtin_bit_cast(uint16_t, (__bf16)v[0]), hi = __builtin_bit_cast(uint16_t, (__bf16)v[V - 1]);
-            __builtin_amdgcn_raw_buffer_store_b32(lo | hi << 16, r, at, 0, 0);
+        unsigned w[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            if constexpr (!BF16) w[e] = __float_as_uint(v[e]);
+            else if constexpr (V == 1) w[e] = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+            else w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{v[2 * e], v[2 * e + 1]}), bf16x2));
         }
+        if constexpr (B == 8) __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[W - 1]}), r, at, 0, kPast);
+        else if constexpr (B == 4) __builtin_amdgcn_raw_buffer_store_b32(w[0], r, at, 0, kPast);
+        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w[0], r, at, 0, 0);
     }
 };
 
@@ -139,395 +150,546 @@ __device__ __forceinline__ void decay(float l, float &a, float &p) {
     p = __builtin_fmaf(-z, e, 1.f - z);
 }
 
-// log_decay in powers of 2 (of the lanes without channels: 0, a state that stays)
-template <int V>
-__device__ __forceinline__ void load_decay(const RecArgs &a, const Place &p, float (&ld2)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) ld2[v] = p.in ? a.ld[p.c + v] * 1.4426950408889634f : 0.f;
+// The same for kMild <= l <= 0, where one polynomial of degree 6 gives p (3.2e-9 relative; fitted here) without a division
+// of the range: 8 operations in place of 13. A channel's l is between 0 and its log_decay in powers of 2
+constexpr float kMild = -1.5f;
+__device__ __forceinline__ void mild_decay(float l, float &a, float &p) {
+    float q = __builtin_fmaf(l, -0x1.458340p-17f, -0x1.2c9900p-13f);
+    q = __builtin_fmaf(q, l, -0x1.5ab9a6p-10f);
+    q = __builtin_fmaf(q, l, -0x1.3afb90p-7f);
+    q = __builtin_fmaf(q, l, -0x1.c6ad90p-5f);
+    q = __builtin_fmaf(q, l, -0x1.ebfbcep-3f);
+    q = __builtin_fmaf(q, l, -0x1.62e430p-1f);
+    p = l * q;
+    a = 1.f - p;
 }
 
 // the step's map h -> a h + b of one channel
-template <bool BF16, bool GATE, bool UNIT>
+template <bool BF16, bool GATE, bool UNIT, bool MILD>
 __device__ __forceinline__ void step_map(float x, float r, float i, float ld2, float &a, float &b) {
     float p;
-    decay(ld2 * sigmoid<BF16>(r), a, p);
+    const float l = ld2 * sigmoid<BF16>(r);
+    if constexpr (MILD) mild_decay(l, a, p);
+    else decay(l, a, p);
     b = GATE ? x * sigmoid<BF16>(i) : x;
     if constexpr (!UNIT) b *= __builtin_amdgcn_sqrtf(p * (2.f - p));  // 1 - a^2 = p (2 - p)
 }
 
-// ------------------------------------------------------------------ forward ---
-// y, kept states and the final state of a segment, from the state that the maps before it give
-template <bool BF16, int V, bool GATE, bool UNIT>
-__global__ __launch_bounds__(kThreads) void fwd_kernel(const RecArgs a) {
-    using IO = Io<BF16, V>;
-    __shared__ float lds[2][kW][2 * V][64];
-    const Place p = Place::make<V>(a);
-    const unsigned bytes = (unsigned)a.C * (BF16 ? 2 : 4), own = (p.in ? p.c * (BF16 ? 2 : 4) : kOutside) + p.wave * kT * bytes;
-    float ld2[V], h[V];
-    load_decay<V>(a, p, ld2);
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.f;
-    const float *h0 = a.nseg > 1 && a.h0 ? a.start : a.h0;
-    if (p.in && h0)
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = h0[p.row * a.C + p.c + v];
-    if (p.in) {
-        const float *m = a.part + p.row * a.nseg * 2 * a.C + p.c;
-        for (int k = 0; k < p.seg; ++k, m += 2 * (int64_t)a.C)
-#pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(m[v], h[v], m[a.C + v]);
+// -------------------------------------------------------------------- tiles ---
+// The column of a workgroup, 64 lanes of V channels of a row, and the tiles of it that it takes
+template <bool BF16, int V, int T, bool CHAIN>
+struct Column {
+    static constexpr int kTile = kW * T;
+    int row, lane, wave;
+    int c;       // this lane's first channel
+    bool in;     // (it has channels)
+    unsigned at, bytes, own;  // the column's number; bytes of a token; this lane's first offset in a tile
+    int64_t len;
+    __device__ __forceinline__ explicit Column(const RecArgs &a) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        at = blockIdx.x % a.columns;
+        row = at / a.cols;
+        c = ((int)(at % a.cols) * 64 + lane) * V;
+        in = c < a.C;
+        bytes = (unsigned)a.C * (BF16 ? 2 : 4);
+        own = (in ? c * (BF16 ? 2 : 4) : kOutside) + wave * T * bytes;
+        len = a.L;
+        if (a.lengths) {
+            const int64_t n = a.lengths[row];
+            len = n < 0 ? 0 : (n < a.L ? n : a.L);
+        }
     }
-    const int64_t end = p.s1 < p.len ? p.s1 : p.len;
-    unsigned rx[kT], rr[kT], ri[GATE ? kT : 1];
-    auto fetch = [&](int64_t t0) {
-        const auto bx = IO::rows(a, a.x, p.row, t0, end - t0), br = IO::rows(a, a.r, p.row, t0, end - t0);
-        const auto bi = IO::rows(a, GATE ? a.i : a.r, p.row, t0, end - t0);
+    // `own`, which the compiler takes for a new value each time: it would keep the offsets of all tokens in registers
+    __device__ __forceinline__ unsigned start() const {
+        unsigned o = own;
+        asm volatile("" : "+v"(o));
+        return o;
+    }
+    // the column's next tile, for the workgroup's turn-th (one thread)
+    __device__ __forceinline__ int take(const RecArgs &a, int turn) const {
+        if constexpr (!CHAIN) return turn;
+        if (turn >= a.turns) return a.ntile;
+        return (int)__hip_atomic_fetch_add(a.taken + at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // tokens of the tile that starts at t0, of the first n of the row
+    static __device__ __forceinline__ int count(int64_t t0, int64_t n) {
+        n -= t0;
+        return n < 0 ? 0 : (n < kTile ? (int)n : kTile);
+    }
+};
+
+// Words that other workgroups wait for. (A NaN of all ones would look like an empty one)
+__device__ __forceinline__ unsigned word(float x) {
+    const unsigned u = __float_as_uint(x);
+    return u == (unsigned)kEmpty ? 0x7fc00000u : u;
+}
+template <class T>
+__device__ __forceinline__ void put(T *p, T w) {
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get(const T *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void give_map(const RecArgs &a, int row, int k, int c, float A, float B) {
+    put(a.maps + ((int64_t)row * a.ntile + k) * a.C + c, (uint64_t)__float_as_uint(B) << 32 | word(A));
+}
+__device__ __forceinline__ void give_end(const RecArgs &a, int row, int k, int c, float h) {
+    put(a.ends + ((int64_t)row * a.ntile + k) * a.C + c, word(h));
+}
+
+// What tile k starts from, for one channel a lane: the nearest state before it that is known, and the maps from there
+__device__ __forceinline__ float chain(const RecArgs &a, int row, int k, int c, bool in) {
+    const uint64_t *map = a.maps + ((int64_t)row * a.ntile + k - 1) * a.C + c;
+    const unsigned *end = a.ends + ((int64_t)row * a.ntile + k - 1) * a.C + c, *begin = a.begins + (int64_t)row * a.C + c;
+    while (true) {
+        uint64_t m[kWindow - 1];
+        unsigned e[kWindow];
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            rx[t] = IO::load(bx, own + t * bytes);
-            rr[t] = IO::load(br, own + t * bytes);
-            if constexpr (GATE) ri[t] = IO::load(bi, own + t * bytes);
+        for (int j = 0; j < kWindow; ++j) {
+            e[j] = (unsigned)kEmpty;
+            if (in && j <= k) e[j] = get(j < k ? end - (int64_t)j * a.C : begin);
         }
+#pragma unroll
+        for (int j = 0; j < kWindow - 1; ++j) {
+            m[j] = kEmpty;
+            if (in && j < k) m[j] = get(map - (int64_t)j * a.C);
+        }
+        bool known = false;
+        float h = 0.f;
+#pragma unroll
+        for (int j = kWindow - 1; j >= 0; --j) {
+            if (j < kWindow - 1) {
+                known = known && m[j] != kEmpty;
+                h = __builtin_fmaf(__uint_as_float((unsigned)m[j]), h, __uint_as_float((unsigned)(m[j] >> 32)));
+            }
+            const bool here = e[j] != (unsigned)kEmpty;
+            known = known || here;
+            h = here ? __uint_as_float(e[j]) : h;
+        }
+        if (__all(known || !in)) return h;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// Two chains before they start: all words empty, no tile taken, what they start from
+struct ChainStart {
+    u32x4 *words;         // maps and ends, to a whole number of 16 bytes
+    int64_t nwords;
+    unsigned *begins, *taken;
+    const float *from;
+    int64_t nbegins, ntaken;
+};
+__global__ __launch_bounds__(256) void chain_start_kernel(const ChainStart one, const ChainStart two) {
+    const int64_t step = (int64_t)gridDim.x * 256, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    constexpr unsigned none = (unsigned)kEmpty;
+    for (const ChainStart &s : {one, two}) {
+        for (int64_t i = at; i < s.nwords; i += step) s.words[i] = u32x4{none, none, none, none};
+        for (int64_t i = at; i < s.nbegins; i += step) s.begins[i] = s.from ? word(s.from[i]) : 0u;
+        for (int64_t i = at; i < s.ntaken; i += step) s.taken[i] = 0;
+    }
+}
+
+// ------------------------------------------------------------------ forward ---
+template <bool BF16, int V, bool GATE, bool UNIT, bool CHAIN>
+__global__ __launch_bounds__(kThreads, 2) void fwd_kernel(const RecArgs a) {
+    constexpr int T = kFwd;
+    using IO = Io<BF16, V>;
+    using At = Column<BF16, V, T, CHAIN>;
+    __shared__ float both[2][2][kW][64 * V], first[64 * V];
+    __shared__ int taken[4];
+    const At p(a);
+    int k = 0, next = 1;
+    if constexpr (CHAIN) {
+        if (threadIdx.x == 0) {
+            taken[0] = p.take(a, 0);
+            taken[1] = p.take(a, 1);
+        }
+        __syncthreads();
+        k = __builtin_amdgcn_readfirstlane(taken[0]);
+        next = __builtin_amdgcn_readfirstlane(taken[1]);
+    }
+    typename IO::raw rx[T], rr[T], ri[GATE ? T : 1];
+    // the loads of a tile, token by token (none behind the last tile)
+    struct Source {
+        typename IO::rsrc_t x, r, i;
+        unsigned at;
     };
-    if (p.s0 < end) fetch(p.s0);
-    int side = 0;
-    for (int64_t t0 = p.s0; t0 < p.s1; t0 += kChunk, side ^= 1) {
-        const int n = end - t0 < kChunk ? (int)(end - t0) : kChunk;  // valid tokens (none or fewer behind the length)
-        const auto by = IO::rows(a, a.y, p.row, t0, a.y ? p.s1 - t0 : 0);
-        if (n <= 0) {
-            const float zero[V] = {};
+    auto source = [&](int tile) {
+        const int64_t t0 = tile < a.ntile ? (int64_t)tile * At::kTile : 0;
+        const int n = tile < a.ntile ? p.count(t0, p.len) : 0;
+        return Source{IO::rows(a, a.x, p.row, t0, n), IO::rows(a, a.r, p.row, t0, n), IO::rows(a, GATE ? a.i : a.r, p.row, t0, n),
+                      p.start()};
+    };
+    auto fetch = [&](Source &f, int t) {
+        rr[t] = IO::load(f.r, f.at);
+        if constexpr (GATE) ri[t] = IO::load(f.i, f.at);
+        rx[t] = IO::load(f.x, f.at);
+        f.at += p.bytes;
+    };
+    auto fetch_all = [&](int tile) {
+        if (tile >= a.ntile) return;
+        Source f = source(tile);
 #pragma unroll
-            for (int t = 0; t < kT; ++t) IO::store(by, own + t * bytes, zero);
-            if (a.states && p.in && p.wave == 0)
+        for (int t = 0; t < T; ++t) fetch(f, t);
+    };
+    fetch_all(k);
+    float ld2[V], h[V];
+    bool mild = true;
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.states[(p.row * a.nkeep + t0 / kChunk) * a.C + p.c + v] = h[v];
-            continue;
-        }
-        float sa[kT][V], sb[kT][V], A[V], B[V];
+    for (int v = 0; v < V; ++v) {
+        ld2[v] = p.in ? a.ld[p.c + v] * 1.4426950408889634f : 0.f;
+        h[v] = !CHAIN && p.in && a.h0 ? a.h0[(int64_t)p.row * a.C + p.c + v] : 0.f;
+        mild = mild && ld2[v] >= kMild;
+    }
+    mild = __all(mild);
+    int last = CHAIN ? -2 : -1;  // the tile behind which h is
+    auto tile = [&](int turn, float(*maps)[kW][64 * V]) {
+        int later = 0;
+        if (CHAIN && threadIdx.x == 0) later = p.take(a, turn + 2);
+        const int64_t t0 = (int64_t)k * At::kTile;
+        const int n = p.count(t0, p.len);
+        const bool whole = n == At::kTile;
+        float sa[T][V], sb[T][V], A[V], B[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             A[v] = 1.f;
             B[v] = 0.f;
         }
+        // The next tile is loaded behind the gates, and between them in a chain, where a workgroup waits for others: long
+        // b2 L32768 of 2560 channels 340 us with the first, 300 with the second; prompt b8 L4096 of 4096, no chain, 206 and 214
+        Source f{};
+        if constexpr (CHAIN) f = source(next);
+        auto gates = [&](auto easy) {
+            constexpr bool MILD = decltype(easy)::value;
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            float x[V], r[V], i[V] = {};
-            IO::unpack(rx[t], x);
-            IO::unpack(rr[t], r);
-            if constexpr (GATE) IO::unpack(ri[t], i);
-            const bool valid = p.wave * kT + t < n;  // (what is not: x is 0, and with a decay of 1 the state stays)
+            for (int t = 0; t < T; ++t) {
+                float x[V], r[V], i[V] = {};
+                IO::unpack(rx[t], x);
+                IO::unpack(rr[t], r);
+                if constexpr (GATE) IO::unpack(ri[t], i);
+                if constexpr (CHAIN) fetch(f, t);
+                // (what is behind the length: x is 0, and with a decay of 1 the state stays)
+                const bool valid = MILD || p.wave * T + t < n;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                step_map<BF16, GATE, UNIT>(x[v], r[v], i[v], valid ? ld2[v] : 0.f, sa[t][v], sb[t][v]);
-                B[v] = __builtin_fmaf(sa[t][v], B[v], sb[t][v]);
-                A[v] *= sa[t][v];
+                for (int v = 0; v < V; ++v) {
+                    step_map<BF16, GATE, UNIT, MILD>(x[v], r[v], i[v], valid ? ld2[v] : 0.f, sa[t][v], sb[t][v]);
+                    B[v] = __builtin_fmaf(sa[t][v], B[v], sb[t][v]);
+                    A[v] *= sa[t][v];
+                }
             }
-        }
-        if (t0 + kChunk < end) fetch(t0 + kChunk);
+        };
+        if (whole && mild) gates(std::true_type{});
+        else gates(std::false_type{});
+        if constexpr (!CHAIN) fetch_all(next);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            lds[side][p.wave][v][p.lane] = A[v];
-            lds[side][p.wave][V + v][p.lane] = B[v];
+            maps[0][p.wave][p.lane * V + v] = A[v];
+            maps[1][p.wave][p.lane * V + v] = B[v];
         }
-        __syncthreads();  // (two sides: the next chunk's maps are written while these are read)
-        if (a.states && p.in && p.wave == 0)
-#pragma unroll
-            for (int v = 0; v < V; ++v) a.states[(p.row * a.nkeep + t0 / kChunk) * a.C + p.c + v] = h[v];
-        float hw[V];
-#pragma unroll
-        for (int k = 0; k < kW; ++k)
+        if (CHAIN && threadIdx.x == 0) taken[2 + (turn & 1)] = later;
+        __syncthreads();  // (two sides of maps: the next tile's are written while these are read)
+        if constexpr (CHAIN) {
+            later = __builtin_amdgcn_readfirstlane(taken[2 + (turn & 1)]);
+            // (the state behind the tile is always that of its joint map, whoever forms it: the same bits)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (k == p.wave) hw[v] = h[v];
-                h[v] = __builtin_fmaf(lds[side][k][v][p.lane], h[v], lds[side][k][V + v][p.lane]);
-            }
-        if (a.y) {
+                A[v] = 1.f;
+                B[v] = 0.f;
 #pragma unroll
-            for (int t = 0; t < kT; ++t) {
+                for (int j = 0; j < kW; ++j) {
+                    A[v] *= maps[0][j][p.lane * V + v];
+                    B[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], B[v], maps[1][j][p.lane * V + v]);
+                }
+                if (p.wave == 0 && p.in && k + 1 < a.ntile) give_map(a, p.row, k, p.c + v, A[v], B[v]);
+            }
+            if (k != last + 1) {
+                if (p.wave < V) {  // (a channel a lane)
+                    const int c = p.c + (p.wave * 64 + p.lane) - p.lane * V;
+                    first[p.wave * 64 + p.lane] = chain(a, p.row, k, c, c < a.C);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = first[p.lane * V + v];
+            }
+        }
+        float hw[V];
+        if constexpr (CHAIN) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) hw[v] = h[v];
+            for (int j = 0; j < p.wave; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    hw[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], hw[v], maps[1][j][p.lane * V + v]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h[v] = __builtin_fmaf(A[v], h[v], B[v]);
+                if (p.wave == 0 && p.in && k + 1 < a.ntile) give_end(a, p.row, k, p.c + v, h[v]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kW; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (j == p.wave) hw[v] = h[v];
+                    h[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], h[v], maps[1][j][p.lane * V + v]);
+                }
+        }
+        if (a.hf && p.in && p.wave == 0 && k == a.ntile - 1)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.hf[(int64_t)p.row * a.C + p.c + v] = h[v];
+        const int64_t at = t0 + p.wave * T;
+        if (a.states && p.in && at % M3_REC_KEEP == 0 && at < a.L)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.states[((int64_t)p.row * a.nkeep + at / M3_REC_KEEP) * a.C + p.c + v] = hw[v];
+        if (a.y) {
+            const auto by = IO::rows(a, a.y, p.row, t0, p.count(t0, a.L));
+            unsigned to = p.start();
+#pragma unroll
+            for (int t = 0; t < T; ++t, to += p.bytes) {
                 float y[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     hw[v] = __builtin_fmaf(sa[t][v], hw[v], sb[t][v]);
-                    y[v] = p.wave * kT + t < n ? hw[v] : 0.f;
+                    y[v] = whole || p.wave * T + t < n ? hw[v] : 0.f;
                 }
-                IO::store(by, own + t * bytes, y);
+                IO::store(by, to, y);
             }
         }
-    }
-    if (a.hf && p.in && p.wave == 0 && p.seg == a.nseg - 1)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.hf[p.row * a.C + p.c + v] = h[v];
-}
-
-// The map of every segment: of the states (BACK: of their gradients, the last token first). A wave takes a run
-// of the segment's tokens by itself; the runs are joined at the end.
-template <bool BF16, int V, bool GATE, bool UNIT, bool BACK>
-__global__ __launch_bounds__(kThreads) void map_kernel(const RecArgs a) {
-    using IO = Io<BF16, V>;
-    __shared__ float lds[kW][2 * V][64];
-    const Place p = Place::make<V>(a);
-    const unsigned bytes = (unsigned)a.C * (BF16 ? 2 : 4), own = p.in ? p.c * (BF16 ? 2 : 4) : kOutside;
-    float ld2[V], A[V], B[V];
-    load_decay<V>(a, p, ld2);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = 1.f;
-        B[v] = 0.f;
-    }
-    const int64_t end = p.s1 < p.len ? p.s1 : p.len, run = a.seg / kW;  // (a multiple of kT)
-    const int64_t r0 = p.s0 + p.wave * run, r1 = r0 + run < end ? r0 + run : end;
-    unsigned rx[kT], rr[kT], ri[GATE ? kT : 1];  // (BACK: rx is dy)
-    auto fetch = [&](int64_t t0) {
-        const auto bx = IO::rows(a, BACK ? a.dy : a.x, p.row, t0, r1 - t0), br = IO::rows(a, a.r, p.row, t0, r1 - t0);
-        const auto bi = IO::rows(a, GATE ? a.i : a.r, p.row, t0, r1 - t0);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            rx[t] = IO::load(bx, own + t * bytes);
-            rr[t] = IO::load(br, own + t * bytes);
-            if constexpr (GATE && !BACK) ri[t] = IO::load(bi, own + t * bytes);
-        }
+        last = k;
+        k = next;
+        next = CHAIN ? later : k + 1;
     };
-    const int64_t steps = r0 < r1 ? (r1 - r0 + kT - 1) / kT : 0;
-    auto start = [&](int64_t k) { return r0 + (BACK ? steps - 1 - k : k) * kT; };
-    if (steps) fetch(start(0));
-    for (int64_t k = 0; k < steps; ++k) {
-        const int64_t t0 = start(k);
-        const int n = r1 - t0 < kT ? (int)(r1 - t0) : kT;
-        float sa[kT][V], sb[kT][V];
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            float x[V], r[V], i[V] = {};
-            IO::unpack(rx[t], x);
-            IO::unpack(rr[t], r);
-            if constexpr (GATE && !BACK) IO::unpack(ri[t], i);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                step_map<BF16, GATE && !BACK, UNIT || BACK>(x[v], r[v], i[v], t < n ? ld2[v] : 0.f, sa[t][v], sb[t][v]);
-                A[v] *= sa[t][v];
-            }
-        }
-        if (k + 1 < steps) fetch(start(k + 1));
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if constexpr (BACK) B[v] = sa[kT - 1 - t][v] * (B[v] + sb[kT - 1 - t][v]);
-                else B[v] = __builtin_fmaf(sa[t][v], B[v], sb[t][v]);
-            }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        lds[p.wave][v][p.lane] = A[v];
-        lds[p.wave][V + v][p.lane] = B[v];
-    }
-    __syncthreads();
-    const float *from = BACK ? a.dhf : a.h0;
-    if (p.seg == 0 && p.wave == 1 && p.in && from)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.start[p.row * a.C + p.c + v] = from[p.row * a.C + p.c + v];
-    if (p.wave == 0 && p.in) {
-        float *to = a.part + (p.row * a.nseg + p.seg) * 2 * a.C + p.c;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float m = 1.f, b = 0.f;
-#pragma unroll
-            for (int k = 0; k < kW; ++k) {
-                const int w = BACK ? kW - 1 - k : k;
-                b = __builtin_fmaf(lds[w][v][p.lane], b, lds[w][V + v][p.lane]);
-                m *= lds[w][v][p.lane];
-            }
-            to[v] = m;
-            to[a.C + v] = b;
-        }
-    }
+    for (int turn = 0; k < a.ntile; ++turn) tile(turn, both[turn & 1]);
 }
 
 // ---------------------------------------------------------------- gradients ---
-// Chunks of a segment, the last first; the states come from the kept ones
-template <bool BF16, int V, bool GATE, bool UNIT>
-__global__ __launch_bounds__(kThreads) void bwd_kernel(const RecArgs a) {
+// The chain runs from the last tile to the first: place k is tile ntile - 1 - k
+template <bool BF16, int V, bool GATE, bool UNIT, bool CHAIN>
+__global__ __launch_bounds__(kThreads, 2) void bwd_kernel(const RecArgs a) {
+    constexpr int T = kBwd;
     using IO = Io<BF16, V>;
-    __shared__ float lds[2][kW][3 * V][64];
-    const Place p = Place::make<V>(a);
-    const unsigned bytes = (unsigned)a.C * (BF16 ? 2 : 4), own = (p.in ? p.c * (BF16 ? 2 : 4) : kOutside) + p.wave * kT * bytes;
-    float ld2[V], ld[V], G[V];
-    double sum[V];
-    load_decay<V>(a, p, ld2);
+    using At = Column<BF16, V, T, CHAIN>;
+    __shared__ float both[2][3][kW][64 * V], first[64 * V];
+    __shared__ int taken[4];
+    const At p(a);
+    int k = 0, next = 1;
+    if constexpr (CHAIN) {
+        if (threadIdx.x == 0) {
+            taken[0] = p.take(a, 0);
+            taken[1] = p.take(a, 1);
+        }
+        __syncthreads();
+        k = __builtin_amdgcn_readfirstlane(taken[0]);
+        next = __builtin_amdgcn_readfirstlane(taken[1]);
+    }
+    typename IO::raw rx[T], rr[T], ri[GATE ? T : 1], rd[T];
+    float kept[V] = {};
+    auto fetch = [&](int place) {
+        if (place >= a.ntile) return;
+        const int64_t t0 = (int64_t)(a.ntile - 1 - place) * At::kTile;
+        const int n = p.count(t0, p.len);
+        const auto bx = IO::rows(a, a.x, p.row, t0, n), br = IO::rows(a, a.r, p.row, t0, n);
+        const auto bi = IO::rows(a, GATE ? a.i : a.r, p.row, t0, n), bd = IO::rows(a, a.dy, p.row, t0, n);
+        unsigned at = p.start();
+#pragma unroll
+        for (int t = 0; t < T; ++t, at += p.bytes) {
+            rr[t] = IO::load(br, at);
+            if constexpr (GATE) ri[t] = IO::load(bi, at);
+            rx[t] = IO::load(bx, at);
+            rd[t] = IO::load(bd, at);
+        }
+        if (p.in && a.nkeep)
+#pragma unroll
+            for (int v = 0; v < V; ++v) kept[v] = a.states[((int64_t)p.row * a.nkeep + a.ntile - 1 - place) * a.C + p.c + v];
+    };
+    fetch(k);
+    float ld[V], ld2[V], G[V];
+    bool mild = true;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         ld[v] = p.in ? a.ld[p.c + v] : 0.f;
-        G[v] = 0.f;
-        sum[v] = 0.;
+        ld2[v] = ld[v] * 1.4426950408889634f;
+        G[v] = !CHAIN && p.in && a.dhf ? a.dhf[(int64_t)p.row * a.C + p.c + v] : 0.f;
+        mild = mild && ld2[v] >= kMild;
     }
-    const float *last = a.nseg > 1 && a.dhf ? a.start : a.dhf;
-    if (p.in && last)
-#pragma unroll
-        for (int v = 0; v < V; ++v) G[v] = last[p.row * a.C + p.c + v];
-    if (p.in) {
-        for (int k = a.nseg - 1; k > p.seg; --k) {
-            const float *m = a.part + (p.row * a.nseg + k) * 2 * a.C + p.c;
-#pragma unroll
-            for (int v = 0; v < V; ++v) G[v] = __builtin_fmaf(m[v], G[v], m[a.C + v]);
-        }
-    }
-    const int64_t end = p.s1 < p.len ? p.s1 : p.len;
-    unsigned rx[kT], rr[kT], ri[GATE ? kT : 1], rd[kT];
-    float hs[V] = {};
-    auto fetch = [&](int64_t t0) {
-        const auto bx = IO::rows(a, a.x, p.row, t0, end - t0), br = IO::rows(a, a.r, p.row, t0, end - t0);
-        const auto bi = IO::rows(a, GATE ? a.i : a.r, p.row, t0, end - t0), bd = IO::rows(a, a.dy, p.row, t0, end - t0);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            rx[t] = IO::load(bx, own + t * bytes);
-            rr[t] = IO::load(br, own + t * bytes);
-            if constexpr (GATE) ri[t] = IO::load(bi, own + t * bytes);
-            rd[t] = IO::load(bd, own + t * bytes);
-        }
-        if (p.in)
-#pragma unroll
-            for (int v = 0; v < V; ++v) hs[v] = a.states[(p.row * a.nkeep + t0 / kChunk) * a.C + p.c + v];
-    };
-    const int64_t nchunk = (p.s1 - p.s0 + kChunk - 1) / kChunk, live = end > p.s0 ? (end - p.s0 + kChunk - 1) / kChunk : 0;
-    for (int64_t k = nchunk - 1; k >= live; --k) {
-        const int64_t t0 = p.s0 + k * kChunk;
-        const float zero[V] = {};
-        const auto b1 = IO::rows(a, a.dx, p.row, t0, p.s1 - t0), b2 = IO::rows(a, a.dr, p.row, t0, p.s1 - t0);
-        const auto b3 = IO::rows(a, GATE ? a.di : a.dr, p.row, t0, p.s1 - t0);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            IO::store(b1, own + t * bytes, zero);
-            IO::store(b2, own + t * bytes, zero);
-            if constexpr (GATE) IO::store(b3, own + t * bytes, zero);
-        }
-    }
-    if (live > 0) fetch(p.s0 + (live - 1) * kChunk);
-    int side = 0;
-    for (int64_t k = live - 1; k >= 0; --k, side ^= 1) {
-        const int64_t t0 = p.s0 + k * kChunk;
-        const int n = end - t0 < kChunk ? (int)(end - t0) : kChunk;
-        // of a step: a, b; E's factors in dx, in di, in d(ld s) and from there in dr; s
-        float sa[kT][V], sb[kT][V], fx[kT][V], fi[GATE ? kT : 1][V], fl[kT][V], fr[kT][V], ss[kT][V], dy[kT][V];
+    mild = __all(mild);
+    int last = CHAIN ? -2 : -1;
+    auto tile = [&](int turn, float(*maps)[kW][64 * V]) {
+        int later = 0;
+        if (CHAIN && threadIdx.x == 0) later = p.take(a, turn + 2);
+        const int64_t t0 = (int64_t)(a.ntile - 1 - k) * At::kTile;
+        const int n = p.count(t0, p.len);
+        const bool whole = n == At::kTile;
+        // of a step: a, b; E's factors in dx, in di, in d(ld s) and from there in dr; s; dy
+        float sa[T][V], sb[T][V], fx[T][V], fi[GATE ? T : 1][V], fl[T][V], fr[T][V], ss[T][V], dy[T][V];
         float A[V], B[V], D[V], h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            h[v] = kept[v];
             A[v] = 1.f;
             B[v] = D[v] = 0.f;
-            h[v] = hs[v];
         }
+        auto gates = [&](auto easy) {
+            constexpr bool MILD = decltype(easy)::value;
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            float x[V], r[V], i[V] = {};
-            IO::unpack(rx[t], x);
-            IO::unpack(rr[t], r);
-            if constexpr (GATE) IO::unpack(ri[t], i);
-            IO::unpack(rd[t], dy[t]);
-            const bool valid = p.wave * kT + t < n;
+            for (int t = 0; t < T; ++t) {
+                float x[V], r[V], i[V] = {};
+                IO::unpack(rx[t], x);
+                IO::unpack(rr[t], r);
+                if constexpr (GATE) IO::unpack(ri[t], i);
+                IO::unpack(rd[t], dy[t]);
+                const bool valid = MILD || p.wave * T + t < n;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float q, s1, g = 1.f, g1 = 0.f;
-                const float s = sigmoid<BF16>(r[v], s1);
-                decay(valid ? ld2[v] * s : 0.f, sa[t][v], q);
-                q *= 2.f - q;
-                if constexpr (GATE) g = sigmoid<BF16>(i[v], g1);
-                float m = 1.f, inv = 0.f;
-                if constexpr (!UNIT) {
-                    // (below the smallest normal number the root counts as 0, and its slope too)
-                    inv = q < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q);
-                    m = q * inv;
+                for (int v = 0; v < V; ++v) {
+                    float q, s1, g = 1.f, g1 = 0.f;
+                    const float s = sigmoid<BF16>(r[v], s1), l = valid ? ld2[v] * s : 0.f;
+                    if constexpr (MILD) mild_decay(l, sa[t][v], q);
+                    else decay(l, sa[t][v], q);
+                    q *= 2.f - q;
+                    if constexpr (GATE) g = sigmoid<BF16>(i[v], g1);
+                    float m = 1.f, inv = 0.f;
+                    if constexpr (!UNIT) {
+                        // (below the smallest normal number the root counts as 0, and its slope too)
+                        inv = q < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q);
+                        m = q * inv;
+                    }
+                    const float b = g * x[v];
+                    sb[t][v] = m * b;
+                    fx[t][v] = m * g;
+                    if constexpr (GATE) fi[t][v] = m * b * g1;
+                    fl[t][v] = b * sa[t][v] * sa[t][v] * inv;
+                    fr[t][v] = ld[v] * (s * s1);
+                    ss[t][v] = s;
+                    B[v] = __builtin_fmaf(sa[t][v], B[v], sb[t][v]);
+                    A[v] *= sa[t][v];
                 }
-                const float u = g * x[v];
-                sb[t][v] = m * u;
-                fx[t][v] = m * g;
-                if constexpr (GATE) fi[t][v] = m * u * g1;
-                fl[t][v] = u * sa[t][v] * sa[t][v] * inv;
-                fr[t][v] = ld[v] * (s * s1);
-                ss[t][v] = valid ? s : 0.f;
-                B[v] = __builtin_fmaf(sa[t][v], B[v], sb[t][v]);
-                A[v] *= sa[t][v];
             }
-        }
-        if (k > 0) fetch(t0 - kChunk);
+        };
+        if (whole && mild) gates(std::true_type{});
+        else gates(std::false_type{});
+        fetch(next);
 #pragma unroll
-        for (int t = kT - 1; t >= 0; --t)
+        for (int t = T - 1; t >= 0; --t)
 #pragma unroll
             for (int v = 0; v < V; ++v) D[v] = sa[t][v] * (dy[t][v] + D[v]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            lds[side][p.wave][v][p.lane] = A[v];
-            lds[side][p.wave][V + v][p.lane] = B[v];
-            lds[side][p.wave][2 * V + v][p.lane] = D[v];
+            maps[0][p.wave][p.lane * V + v] = A[v];
+            maps[1][p.wave][p.lane * V + v] = B[v];
+            maps[2][p.wave][p.lane * V + v] = D[v];
         }
+        if (CHAIN && threadIdx.x == 0) taken[2 + (turn & 1)] = later;
         __syncthreads();
-        float hw[V], Gw[V];
+        // the state that this run starts from, and those before its tokens
+        for (int j = 0; j < p.wave; ++j)
 #pragma unroll
-        for (int w = 0; w < kW; ++w)
+            for (int v = 0; v < V; ++v)
+                h[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], h[v], maps[1][j][p.lane * V + v]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (w == p.wave) hw[v] = h[v];
-                h[v] = __builtin_fmaf(lds[side][w][v][p.lane], h[v], lds[side][w][V + v][p.lane]);
-            }
-#pragma unroll
-        for (int w = kW - 1; w >= 0; --w)
+        for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (w == p.wave) Gw[v] = G[v];
-                G[v] = __builtin_fmaf(lds[side][w][v][p.lane], G[v], lds[side][w][2 * V + v][p.lane]);
+                const float left = sa[t][v] * h[v];
+                fl[t][v] = left - fl[t][v];
+                h[v] = left + sb[t][v];
             }
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
+        if constexpr (CHAIN) {
+            later = __builtin_amdgcn_readfirstlane(taken[2 + (turn & 1)]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float kept = sa[t][v] * hw[v];
-                fl[t][v] = kept - fl[t][v];
-                hw[v] = kept + sb[t][v];
+                A[v] = 1.f;
+                D[v] = 0.f;
+#pragma unroll
+                for (int j = kW - 1; j >= 0; --j) {
+                    A[v] *= maps[0][j][p.lane * V + v];
+                    D[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], D[v], maps[2][j][p.lane * V + v]);
+                }
+                if (p.wave == 0 && p.in && k + 1 < a.ntile) give_map(a, p.row, k, p.c + v, A[v], D[v]);
             }
-        const auto b1 = IO::rows(a, a.dx, p.row, t0, p.s1 - t0), b2 = IO::rows(a, a.dr, p.row, t0, p.s1 - t0);
-        const auto b3 = IO::rows(a, GATE ? a.di : a.dr, p.row, t0, p.s1 - t0);
+            if (k != last + 1) {
+                if (p.wave < V) {  // (a channel a lane)
+                    const int c = p.c + (p.wave * 64 + p.lane) - p.lane * V;
+                    first[p.wave * 64 + p.lane] = chain(a, p.row, k, c, c < a.C);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int v = 0; v < V; ++v) G[v] = first[p.lane * V + v];
+            }
+        }
+        float Gw[V];
+        if constexpr (CHAIN) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) Gw[v] = G[v];
+            for (int j = kW - 1; j > p.wave; --j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    Gw[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], Gw[v], maps[2][j][p.lane * V + v]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                G[v] = __builtin_fmaf(A[v], G[v], D[v]);
+                if (p.wave == 0 && p.in && k + 1 < a.ntile) give_end(a, p.row, k, p.c + v, G[v]);
+            }
+        } else {
+#pragma unroll
+            for (int j = kW - 1; j >= 0; --j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (j == p.wave) Gw[v] = G[v];
+                    G[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], G[v], maps[2][j][p.lane * V + v]);
+                }
+        }
+        if (a.dh0 && p.in && p.wave == 0 && k == a.ntile - 1)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.dh0[(int64_t)p.row * a.C + p.c + v] = G[v];
+        const int rows = p.count(t0, a.L);
+        const auto b1 = IO::rows(a, a.dx, p.row, t0, rows), b2 = IO::rows(a, a.dr, p.row, t0, rows);
+        const auto b3 = IO::rows(a, GATE ? a.di : a.dr, p.row, t0, rows);
         float dl[V] = {};
+        unsigned to = p.start() + (T - 1) * p.bytes;
 #pragma unroll
-        for (int t = kT - 1; t >= 0; --t) {
+        for (int t = T - 1; t >= 0; --t, to -= p.bytes) {
             float ox[V], orr[V], oi[V];
-            const bool valid = p.wave * kT + t < n;
+            const bool valid = whole || p.wave * T + t < n;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float E = valid ? dy[t][v] + Gw[v] : 0.f, d = E * fl[t][v];
-                ox[v] = E * fx[t][v];
+                // (behind the length: no gradient, and a decay of 1 passes G on)
+                const float E = dy[t][v] + Gw[v], F = valid ? E : 0.f, d = F * fl[t][v];
+                ox[v] = F * fx[t][v];
                 orr[v] = d * fr[t][v];
-                if constexpr (GATE) oi[v] = E * fi[t][v];
+                if constexpr (GATE) oi[v] = F * fi[t][v];
                 dl[v] = __builtin_fmaf(d, ss[t][v], dl[v]);
-                Gw[v] = valid ? sa[t][v] * E : Gw[v];
+                Gw[v] = sa[t][v] * E;
             }
-            IO::store(b1, own + t * bytes, ox);
-            IO::store(b2, own + t * bytes, orr);
-            if constexpr (GATE) IO::store(b3, own + t * bytes, oi);
+            IO::store(b1, to, ox);
+            IO::store(b2, to, orr);
+            if constexpr (GATE) IO::store(b3, to, oi);
         }
+        if (a.dpart) {
+            __syncthreads();  // (the maps are read no more)
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum[v] += dl[v];
-    }
-    if (a.dh0 && p.in && p.wave == 0 && p.seg == 0)
+            for (int v = 0; v < V; ++v) maps[1][p.wave][p.lane * V + v] = dl[v];
+            __syncthreads();
+            if (p.wave == 0 && p.in)
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.dh0[p.row * a.C + p.c + v] = G[v];
-    if (a.dpart) {
-        double(*join)[V][64] = reinterpret_cast<double(*)[V][64]>(&lds[0][0][0][0]);
-        static_assert(sizeof(double) * kW * V * 64 <= sizeof(lds), "the sums fit");
-        __syncthreads();
+                for (int v = 0; v < V; ++v) {
+                    double d = 0.;
 #pragma unroll
-        for (int v = 0; v < V; ++v) join[p.wave][v][p.lane] = sum[v];
-        __syncthreads();
-        if (p.wave == 0 && p.in)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                double d = 0.;
-#pragma unroll
-                for (int w = 0; w < kW; ++w) d += join[w][v][p.lane];
-                a.dpart[(p.row * a.nseg + p.seg) * a.C + p.c + v] = d;
-            }
-    }
+                    for (int j = 0; j < kW; ++j) d += maps[1][j][p.lane * V + v];
+                    a.dpart[((int64_t)p.row * a.ntile + k) * a.C + p.c + v] = (float)d;
+                }
+        }
+        last = k;
+        k = next;
+        next = CHAIN ? later : k + 1;
+    };
+    for (int turn = 0; k < a.ntile; ++turn) tile(turn, both[turn & 1]);
 }
 
-// dld[c]: the sums of all rows and segments, in a fixed order
-constexpr int kRuns = 4;
-__global__ __launch_bounds__(64 * kRuns) void decay_sums_kernel(const double *part, int64_t rows, int C, float *dld) {
+// dld[c]: the sums of all tiles, in a fixed order
+constexpr int kRuns = 16;
+__global__ __launch_bounds__(64 * kRuns) void decay_sums_kernel(const float *part, int64_t rows, int C, float *dld) {
     __shared__ double lds[kRuns][64];
     const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
     double d = 0.;
@@ -535,7 +697,10 @@ __global__ __launch_bounds__(64 * kRuns) void decay_sums_kernel(const double *pa
         for (int64_t r = run; r < rows; r += kRuns) d += part[r * C + c];
     lds[run][lane] = d;
     __syncthreads();
-    if (run == 0 && c < C) dld[c] = (float)(lds[0][lane] + lds[1][lane] + lds[2][lane] + lds[3][lane]);
+    if (run == 0 && c < C) {
+        for (int k = 1; k < kRuns; ++k) d += lds[k][lane];
+        dld[c] = (float)d;
+    }
 }
 
 // ------------------------------------------------------------- single token ---
@@ -547,7 +712,7 @@ __global__ __launch_bounds__(256) void step_kernel(const void *x, const void *r,
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float a, b;
-            step_map<BF16, GATE, UNIT>(ld_io<BF16>(x, at + v), ld_io<BF16>(r, at + v), GATE ? ld_io<BF16>(i, at + v) : 0.f,
+            step_map<BF16, GATE, UNIT, false>(ld_io<BF16>(x, at + v), ld_io<BF16>(r, at + v), GATE ? ld_io<BF16>(i, at + v) : 0.f,
                                        ld[c + v] * 1.4426950408889634f, a, b);
             const float s = __builtin_fmaf(a, h[at + v], b);
             h[at + v] = s;
@@ -562,15 +727,22 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-struct RecPlan {
+// one direction: channels a lane, tiles along and across, columns of all rows, workgroups a column (chained where
+// there is more than one), bytes of the chain's words, of all of the chain
+struct RecWay {
     int V;
-    int64_t cols, nseg, seg, nkeep, groups;  // groups: workgroups of a launch
-    size_t states, part, dpart;              // bytes
+    int64_t ntile, cols, columns, each;
+    size_t words, chain;
+};
+struct RecPlan {
+    int64_t nkeep;  // kept states of a row
+    RecWay fwd, bwd;
+    size_t states, dpart;  // bytes
 };
 
 m3_status rec_check(const m3_rec_shape *s) {
     if (!s) return M3_ERR_INVALID_ARG;
-    if (s->batch < 0 || s->seqlen < 0 || s->channels < 1 || s->nsegments < 0 || s->reserved) return M3_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->seqlen < 0 || s->channels < 1) return M3_ERR_INVALID_ARG;
     if (s->io_dtype != M3_F32 && s->io_dtype != M3_BF16) return M3_ERR_INVALID_ARG;
     if (s->flags & ~(uint32_t)M3_REC_UNSCALED) return M3_ERR_INVALID_ARG;
     if (s->channels > (1 << 20) || s->batch > (1LL << 31) || s->seqlen > (1LL << 40) ||
@@ -579,63 +751,81 @@ m3_status rec_check(const m3_rec_shape *s) {
     return M3_OK;
 }
 
+m3_status way(const m3_rec_shape &s, int tile, RecWay *w) {
+    *w = {};
+    w->V = s.io_dtype == M3_BF16 && s.channels % 2 == 0 ? 2 : 1;
+    w->ntile = s.seqlen ? ceil_div(s.seqlen, tile) : 1;
+    w->cols = ceil_div(s.channels, 64 * w->V);
+    w->columns = s.batch * w->cols;
+    if (w->columns > kMaxGrid || w->columns * w->ntile > kMaxGrid) return M3_ERR_UNSUPPORTED;
+    // enough workgroups a column that all of them fill the card once or a few times
+    w->each = 1;
+    double best = 0.;
+    for (int64_t rounds = 1; rounds <= 4 && w->columns > 0; ++rounds) {
+        const int64_t n = rounds * kSlots / w->columns, each = n < 1 ? 1 : (n < w->ntile ? n : w->ntile);
+        const double full = (double)(w->columns * each) / (double)(ceil_div(w->columns * each, kSlots) * kSlots);
+        if (full > best * 1.1) {
+            best = full;
+            w->each = each;
+        }
+    }
+    w->words = w->each == 1 ? 0 : up((size_t)(s.batch * s.channels * w->ntile) * (sizeof(uint64_t) + sizeof(unsigned)));
+    w->chain = w->each == 1 ? 0 : w->words + up((size_t)(s.batch * s.channels + w->columns) * sizeof(unsigned));
+    return M3_OK;
+}
+
 m3_status rec_plan(const m3_rec_shape *s, RecPlan *p) {
     const m3_status st = rec_check(s);
     if (st != M3_OK) return st;
-    p->V = s->io_dtype == M3_BF16 && s->channels % 2 == 0 ? 2 : 1;
-    p->cols = ceil_div(s->channels, 64 * p->V);
-    p->nkeep = ceil_div(s->seqlen, kChunk);
-    const int64_t wide = s->batch * p->cols;
-    int64_t k = s->nsegments;
-    if (k == 0) k = wide >= 192 || wide == 0 ? 1 : ceil_div(512, wide) < 64 ? ceil_div(512, wide) : 64;
-    // whole chunks, four at least where the split is picked here
-    int64_t chunks = ceil_div(p->nkeep, k);
-    if (s->nsegments == 0 && chunks < 4) chunks = 4;
-    if (chunks < 1) chunks = 1;
-    p->seg = chunks * kChunk;
-    p->nseg = p->nkeep ? ceil_div(p->nkeep, chunks) : 1;
-    if (wide > kMaxGrid || wide * p->nseg > kMaxGrid) return M3_ERR_UNSUPPORTED;
-    p->groups = wide * p->nseg;
+    if (s->batch > kMaxGrid || way(*s, kW * kFwd, &p->fwd) != M3_OK || way(*s, kW * kBwd, &p->bwd) != M3_OK)
+        return M3_ERR_UNSUPPORTED;
+    p->nkeep = ceil_div(s->seqlen, M3_REC_KEEP);
     p->states = up((size_t)(s->batch * p->nkeep * s->channels) * sizeof(float));
-    p->part = p->nseg > 1 ? up((size_t)(s->batch * (2 * p->nseg + 1) * s->channels) * sizeof(float)) : 0;
-    p->dpart = up((size_t)(s->batch * p->nseg * s->channels) * sizeof(double));
+    p->dpart = up((size_t)(s->batch * p->bwd.ntile * s->channels) * sizeof(float));
     return M3_OK;
 }
 
 RecArgs rec_args(const m3_rec_shape &s, const m3_rec_io &io, const RecPlan &p) {
     RecArgs a{};
     a.x = io.x; a.r = io.decay_gate; a.i = io.input_gate; a.ld = io.log_decay; a.h0 = io.h0; a.lengths = io.lengths;
-    a.L = s.seqlen; a.C = (int)s.channels; a.cols = (int)p.cols; a.nseg = (int)p.nseg; a.nkeep = (int)p.nkeep;
-    a.seg = p.seg;
+    a.L = s.seqlen; a.C = (int)s.channels; a.nkeep = (int)p.nkeep;
     return a;
 }
 
-void set_part(RecArgs &a, void *at, int64_t batch) {
-    a.part = static_cast<float *>(at);
-    a.start = a.part + batch * a.nseg * 2 * a.C;
+// one direction's part of the arguments, and its chain in the workspace at `ws`, which starts from `from`
+ChainStart set_way(RecArgs &a, const RecWay &w, int64_t batch, void *ws, const float *from) {
+    a.ntile = (int)w.ntile;
+    a.cols = (int)w.cols;
+    a.columns = (unsigned)w.columns;
+    a.turns = (int)ceil_div(w.ntile, w.each);
+    if (w.each == 1) return {};
+    const int64_t n = batch * w.ntile * a.C;
+    a.maps = static_cast<uint64_t *>(ws);
+    a.ends = reinterpret_cast<unsigned *>(a.maps + n);
+    a.begins = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + w.words);
+    a.taken = a.begins + batch * a.C;
+    return {static_cast<u32x4 *>(ws), (int64_t)(w.words / 16), a.begins, a.taken, from, batch * a.C, w.columns};
 }
-
-template <bool BF16, int V, bool GATE, bool UNIT>
-hipError_t launch_fwd(const RecArgs &a, const RecPlan &p, hipStream_t s) {
-    const dim3 g((unsigned)p.groups), t(kThreads);
-    if (p.nseg > 1) {
-        hipLaunchKernelGGL((map_kernel<BF16, V, GATE, UNIT, false>), g, t, 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((fwd_kernel<BF16, V, GATE, UNIT>), g, t, 0, s, a);
+hipError_t start(const ChainStart &one, const ChainStart &two, hipStream_t s) {
+    const int64_t n = one.nwords + two.nwords, g = ceil_div(n, 256 * 2);
+    if (n == 0) return hipSuccess;
+    hipLaunchKernelGGL(chain_start_kernel, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s, one, two);
     return hipGetLastError();
 }
 
 template <bool BF16, int V, bool GATE, bool UNIT>
-hipError_t launch_bwd(const RecArgs &a, const RecPlan &p, hipStream_t s) {
-    const dim3 g((unsigned)p.groups), t(kThreads);
-    if (p.nseg > 1) {
-        hipLaunchKernelGGL((map_kernel<BF16, V, GATE, UNIT, true>), g, t, 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((bwd_kernel<BF16, V, GATE, UNIT>), g, t, 0, s, a);
+hipError_t launch_fwd(const RecArgs &a, const RecWay &w, hipStream_t s) {
+    const dim3 g((unsigned)(w.columns * w.each)), t(kThreads);
+    if (w.each > 1) hipLaunchKernelGGL((fwd_kernel<BF16, V, GATE, UNIT, true>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((fwd_kernel<BF16, V, GATE, UNIT, false>), g, t, 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool BF16, int V, bool GATE, bool UNIT>
+hipError_t launch_bwd(const RecArgs &a, const RecWay &w, hipStream_t s) {
+    const dim3 g((unsigned)(w.columns * w.each)), t(kThreads);
+    if (w.each > 1) hipLaunchKernelGGL((bwd_kernel<BF16, V, GATE, UNIT, true>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((bwd_kernel<BF16, V, GATE, UNIT, false>), g, t, 0, s, a);
     return hipGetLastError();
 }
 
@@ -648,18 +838,21 @@ hipError_t launch_step(const m3_rec_shape &s, const m3_rec_step_io &io, hipStrea
 }
 
 // f<BF16, V, GATE, UNIT>(...) of the shape at hand
-#define M3_REC_PICK(f, shape, V, gate, ...)                                                        \
-    [&]() -> hipError_t {                                                                          \
-        const bool unit = ((shape).flags & M3_REC_UNSCALED) != 0;                                  \
-        if ((shape).io_dtype != M3_BF16)                                                           \
-            return gate ? (unit ? f<false, 1, true, true>(__VA_ARGS__) : f<false, 1, true, false>(__VA_ARGS__))    \
-                        : (unit ? f<false, 1, false, true>(__VA_ARGS__) : f<false, 1, false, false>(__VA_ARGS__)); \
-        if (V == 1)                                                                                \
-            return gate ? (unit ? f<true, 1, true, true>(__VA_ARGS__) : f<true, 1, true, false>(__VA_ARGS__))      \
-                        : (unit ? f<true, 1, false, true>(__VA_ARGS__) : f<true, 1, false, false>(__VA_ARGS__));   \
-        return gate ? (unit ? f<true, 2, true, true>(__VA_ARGS__) : f<true, 2, true, false>(__VA_ARGS__))          \
-                    : (unit ? f<true, 2, false, true>(__VA_ARGS__) : f<true, 2, false, false>(__VA_ARGS__));       \
-    }()
+#define M3_REC_PICK_V(f, BF, V, gate, unit, ...)                                            \
+    (gate ? (unit ? f<BF, V, true, true>(__VA_ARGS__) : f<BF, V, true, false>(__VA_ARGS__)) \
+          : (unit ? f<BF, V, false, true>(__VA_ARGS__) : f<BF, V, false, false>(__VA_ARGS__)))
+#define M3_REC_PICK(f, s, gate, ...)                                                                             \
+    ((s)->io_dtype != M3_BF16                                                                                    \
+         ? M3_REC_PICK_V(f, false, 1, gate, ((s)->flags & M3_REC_UNSCALED) != 0, __VA_ARGS__)                    \
+         : ((s)->channels % 2 == 0 ? M3_REC_PICK_V(f, true, 2, gate, ((s)->flags & M3_REC_UNSCALED) != 0, __VA_ARGS__) \
+                                   : M3_REC_PICK_V(f, true, 1, gate, ((s)->flags & M3_REC_UNSCALED) != 0, __VA_ARGS__)))
+
+hipError_t launch_fwd_any(const m3_rec_shape *s, bool gate, const RecArgs &a, const RecWay &w, hipStream_t hs) {
+    return M3_REC_PICK(launch_fwd, s, gate, a, w, hs);
+}
+hipError_t launch_bwd_any(const m3_rec_shape *s, bool gate, const RecArgs &a, const RecWay &w, hipStream_t hs) {
+    return M3_REC_PICK(launch_bwd, s, gate, a, w, hs);
+}
 
 }  // namespace
 }  // namespace m3i
@@ -670,12 +863,12 @@ extern "C" {
 
 size_t m3_recurrence_workspace_bytes(const m3_rec_shape *shape) {
     RecPlan p;
-    return rec_plan(shape, &p) == M3_OK ? p.part : 0;
+    return rec_plan(shape, &p) == M3_OK ? p.fwd.chain : 0;
 }
 
 size_t m3_recurrence_bwd_workspace_bytes(const m3_rec_shape *shape, int states) {
     RecPlan p;
-    return rec_plan(shape, &p) == M3_OK ? (states ? 0 : p.states) + p.part + p.dpart : 0;
+    return rec_plan(shape, &p) == M3_OK ? (states ? 0 : p.states + p.fwd.chain) + p.bwd.chain + p.dpart : 0;
 }
 
 m3_status m3_recurrence_fwd(const m3_rec_shape *shape, const m3_rec_io *io, void *workspace, size_t ws_bytes, void *stream) {
@@ -689,16 +882,17 @@ m3_status m3_recurrence_fwd(const m3_rec_shape *shape, const m3_rec_io *io, void
                           io->states, workspace};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;
-    if (p.part && (!workspace || ws_bytes < p.part)) return M3_ERR_WORKSPACE_TOO_SMALL;
-    void *ws = p.part ? workspace : nullptr;
+    if (p.fwd.chain && (!workspace || ws_bytes < p.fwd.chain)) return M3_ERR_WORKSPACE_TOO_SMALL;
+    void *ws = p.fwd.chain ? workspace : nullptr;
     if (clash({io->y, io->states, ws}, {io->x, io->decay_gate, io->input_gate, io->log_decay, io->h0, io->lengths, io->h_final}) ||
         clash({io->h_final}, {io->x, io->decay_gate, io->input_gate, io->log_decay, io->lengths}))
         return M3_ERR_INVALID_ARG;
-    if (p.groups == 0) return M3_OK;
+    if (shape->batch == 0) return M3_OK;
+    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     RecArgs a = rec_args(*shape, *io, p);
     a.y = io->y; a.hf = io->h_final; a.states = io->states;
-    set_part(a, workspace, shape->batch);
-    const hipError_t e = M3_REC_PICK(launch_fwd, *shape, p.V, a.i != nullptr, a, p, reinterpret_cast<hipStream_t>(stream));
+    hipError_t e = start(set_way(a, p.fwd, shape->batch, workspace, a.h0), {}, hs);
+    if (e == hipSuccess) e = launch_fwd_any(shape, a.i != nullptr, a, p.fwd, hs);
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
 
@@ -716,7 +910,8 @@ m3_status m3_recurrence_bwd(const m3_rec_shape *shape, const m3_rec_io *io, cons
                           gr->dh_final, gr->dx, gr->ddecay_gate, gr->dinput_gate, gr->dlog_decay, gr->dh0, workspace};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;
-    const size_t own_states = io->states ? 0 : p.states, need = own_states + p.part + p.dpart;
+    // the states, where they are formed here, and their chain; the gradients' chain; partial sums
+    const size_t own_states = io->states ? 0 : p.states + p.fwd.chain, need = own_states + p.bwd.chain + p.dpart;
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
     void *ws = need ? workspace : nullptr;
     if (clash({gr->dx, gr->ddecay_gate, gr->dinput_gate, gr->dlog_decay, ws},
@@ -729,18 +924,19 @@ m3_status m3_recurrence_bwd(const m3_rec_shape *shape, const m3_rec_io *io, cons
     RecArgs a = rec_args(*shape, *io, p);
     hipError_t e = hipSuccess;
     a.states = io->states ? io->states : reinterpret_cast<float *>(at);
-    set_part(a, at + own_states, shape->batch);
-    if (p.groups > 0) {
-        if (!io->states && shape->seqlen > 0)
-            e = M3_REC_PICK(launch_fwd, *shape, p.V, a.i != nullptr, a, p, hs);
-        a.dy = gr->dy; a.dhf = gr->dh_final; a.dx = gr->dx; a.dr = gr->ddecay_gate; a.di = gr->dinput_gate;
-        a.dld = gr->dlog_decay; a.dh0 = gr->dh0;
-        a.dpart = gr->dlog_decay ? reinterpret_cast<double *>(at + own_states + p.part) : nullptr;
-        if (e == hipSuccess) e = M3_REC_PICK(launch_bwd, *shape, p.V, a.i != nullptr, a, p, hs);
+    a.dpart = gr->dlog_decay ? reinterpret_cast<float *>(at + own_states + p.bwd.chain) : nullptr;
+    if (shape->batch > 0) {
+        const bool first = !io->states && shape->seqlen > 0;
+        RecArgs f = a;
+        const ChainStart back = set_way(a, p.bwd, shape->batch, at + own_states, gr->dh_final);
+        e = start(first ? set_way(f, p.fwd, shape->batch, at + p.states, a.h0) : ChainStart{}, back, hs);
+        if (e == hipSuccess && first) e = launch_fwd_any(shape, a.i != nullptr, f, p.fwd, hs);
+        a.dy = gr->dy; a.dhf = gr->dh_final; a.dx = gr->dx; a.dr = gr->ddecay_gate; a.di = gr->dinput_gate; a.dh0 = gr->dh0;
+        if (e == hipSuccess) e = launch_bwd_any(shape, a.i != nullptr, a, p.bwd, hs);
     }
     if (e == hipSuccess && gr->dlog_decay) {
         hipLaunchKernelGGL(decay_sums_kernel, dim3((unsigned)ceil_div(shape->channels, 64)), dim3(64 * kRuns), 0, hs, a.dpart,
-                           shape->batch * p.nseg, (int)shape->channels, gr->dlog_decay);
+                           shape->batch * p.bwd.ntile, (int)shape->channels, gr->dlog_decay);
         e = hipGetLastError();
     }
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
@@ -756,9 +952,8 @@ m3_status m3_recurrence_step(const m3_rec_shape *shape, const m3_rec_step_io *io
         if (!al16(q)) return M3_ERR_MISALIGNED;
     if (clash({io->h, io->y}, {io->x, io->decay_gate, io->input_gate, io->log_decay})) return M3_ERR_INVALID_ARG;
     if (shape->batch == 0) return M3_OK;
-    const int V = shape->io_dtype == M3_BF16 && shape->channels % 2 == 0 ? 2 : 1;
     const hipError_t e =
-        M3_REC_PICK(launch_step, *shape, V, io->input_gate != nullptr, *shape, *io, reinterpret_cast<hipStream_t>(stream));
+        M3_REC_PICK(launch_step, shape, io->input_gate != nullptr, *shape, *io, reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
 

@@ -84,8 +84,7 @@ class NormGrads(ctypes.Structure):
 
 class RecShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
-                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("nsegments", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class RecIO(ctypes.Structure):
@@ -896,10 +895,10 @@ M3_REC_KEEP = 64  # tokens between two kept states
 M3_REC_UNSCALED = 1
 
 
-def recurrence_shape(x, nsegments=0, scaled=True) -> RecShape:
+def recurrence_shape(x, scaled=True) -> RecShape:
     """The shape of x [b,L,C]."""
     b, L, C = x.shape
-    return RecShape(b, L, C, _io_dtype(x), 0 if scaled else M3_REC_UNSCALED, nsegments, 0)
+    return RecShape(b, L, C, _io_dtype(x), 0 if scaled else M3_REC_UNSCALED)
 
 
 def recurrence_workspace_bytes(shape: RecShape) -> int:
@@ -910,7 +909,7 @@ def recurrence_bwd_workspace_bytes(shape: RecShape, states=False) -> int:
     return int(lib.m3_recurrence_bwd_workspace_bytes(ctypes.byref(shape), bool(states)))
 
 
-def _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegments, scaled):
+def _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, scaled):
     """The shape and the inputs of a recurrence over x [b,L,C], checked."""
     b, L, C = _dims5("x", x, 3)
     iot, io, f32, dev, s = _io_dtype(x), x.dtype, torch.float32, x.get_device(), x.shape
@@ -922,12 +921,11 @@ def _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegmen
                  _arg("input_gate", input_gate, s, io, dev), _arg("log_decay", log_decay, (C,), f32, dev),
                  _arg("h0", h0, (b, C), f32, dev), _arg("lengths", lengths, (b,), torch.int32, dev), None, None,
                  _arg("states", states, (b, -(-L // M3_REC_KEEP), C), f32, dev))
-    return RecShape(b, L, C, iot, 0 if scaled else M3_REC_UNSCALED, nsegments, 0), ptrs
+    return RecShape(b, L, C, iot, 0 if scaled else M3_REC_UNSCALED), ptrs
 
 
 def recurrence_fwd(x, decay_gate, log_decay, *, input_gate=None, h0=None, lengths=None, scaled=True, y=None,
-                   h_final=None, want_state=True, states=None, want_states=False, workspace=None, nsegments=0,
-                   stream=None):
+                   h_final=None, want_state=True, states=None, want_states=False, workspace=None, stream=None):
     """Gated linear recurrence over a prompt, one state a channel (m3_recurrence_fwd):
     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t with a_t = exp(log_decay *
     sigmoid(decay_gate_t)), y_t = h_t. x and the gates [b,L,C] (fp32 or bf16; no input gate: 1),
@@ -935,7 +933,7 @@ def recurrence_fwd(x, decay_gate, log_decay, *, input_gate=None, h0=None, length
     behind them and the state is the one after them. scaled=False: without sqrt(1 - a^2). Returns
     (y, h_final [b,C] fp32 or None), and with want_states (or states) a third, the states that
     recurrence_bwd takes: [b, ceil(L/64), C] fp32."""
-    shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegments, scaled)
+    shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, scaled)
     b, L, C = x.shape
     f32, dev = torch.float32, x.get_device()
     ptrs.y, ptrs.h_final = _arg("y", y, x.shape, x.dtype, dev), _arg("h_final", h_final, (b, C), f32, dev)
@@ -960,14 +958,13 @@ def recurrence_fwd(x, decay_gate, log_decay, *, input_gate=None, h0=None, length
 
 
 def recurrence_bwd(x, decay_gate, log_decay, dy, *, input_gate=None, h0=None, lengths=None, scaled=True, dh_final=None,
-                   states=None, want_dh0=True, want_dlog_decay=True, workspace=None, grads=None, nsegments=0,
-                   stream=None):
+                   states=None, want_dh0=True, want_dlog_decay=True, workspace=None, grads=None, stream=None):
     """Gradients of <dy, y> + <dh_final, h_final> of recurrence_fwd (m3_recurrence_bwd). states: what the
     forward call kept (h0 is then not read); without them the recurrence runs over the sequence once
     more. Returns a dict: x, decay_gate and, with an input gate, input_gate in the dtype of x;
     log_decay [C] and h0 [b,C] in fp32 where wanted. grads: such a dict to write into (x and the
     gates required)."""
-    shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, nsegments, scaled)
+    shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, scaled)
     _need("dy", dy)
     b, _, C = x.shape
     io, s, f32, dev = x.dtype, x.shape, torch.float32, x.get_device()
@@ -1013,7 +1010,7 @@ def recurrence_step(x, decay_gate, log_decay, h, *, input_gate=None, scaled=True
                      _arg("input_gate", input_gate, s, io, dev), _arg("log_decay", log_decay, (C,), f32, dev),
                      _arg("h", h, s, f32, dev), _arg("y", y, s, io, dev))
     _on_gpu(dev)
-    shape = RecShape(b, 1, C, iot, 0 if scaled else M3_REC_UNSCALED, 0, 0)
+    shape = RecShape(b, 1, C, iot, 0 if scaled else M3_REC_UNSCALED)
     if y is None:
         with _owned_by(stream):
             y = x.new_empty(s)

@@ -97,9 +97,9 @@ def draw(seed, b, L, C, io, gate=True, h0=True):
                 dy=r(b, L, C).to(io).cuda(), dh=r(b, C).cuda())
 
 
-def run(d, lengths=None, scaled=True, kept=False, nsegments=0):
+def run(d, lengths=None, scaled=True, kept=False):
     from state_space_sequence_amd import m3
-    kw = dict(input_gate=d["i"], h0=d["h0"], lengths=lengths, scaled=scaled, nsegments=nsegments)
+    kw = dict(input_gate=d["i"], h0=d["h0"], lengths=lengths, scaled=scaled)
     y, h, states = m3.recurrence_fwd(d["x"], d["r"], d["ld"], want_states=True, **kw)
     if kept:
         kw["states"] = states
@@ -129,25 +129,38 @@ def test_forward_and_backward(b, L, C, gate, scaled, h0, io):
 
 
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("L,nseg", [(640, 2), (700, 3), (1500, 24), (1025, 4), (100, 9), (2000, 0)])
-def test_segments(L, nseg, io):
-    print("recurrence segments", L, nseg, io, flush=True)
+@pytest.mark.parametrize("L", [640, 700, 1024, 1025, 1100, 2177, 3300])
+def test_long_chains(L, io):
+    """Many tiles: within a group, at a group's end, over several groups."""
+    print("recurrence long", L, io, flush=True)
     d = draw(L, 2, L, 66, io)
     lengths = torch.tensor([L, L // 3], dtype=torch.int32).cuda()
-    compare(d, run(d, lengths, nsegments=nseg), lengths)
+    compare(d, run(d, lengths), lengths)
+
+
+@pytest.mark.parametrize("io,b,L,C", [(torch.bfloat16, 2, 130, 16384), (torch.float32, 3, 70, 8000), (torch.bfloat16, 1, 9000, 34),
+                                      (torch.float32, 1, 5000, 65), (torch.bfloat16, 5, 300, 7682)])
+def test_columns_from_one_to_more_than_the_card_holds(io, b, L, C):
+    """Many columns, a workgroup each or a few; one or two columns, whose tiles are all taken at once."""
+    print("recurrence columns", io, b, L, C, flush=True)
+    d = draw(L, b, L, C, io)
+    got = run(d)
+    compare(d, got)
+    for _ in range(5):  # whoever is first, the same bits
+        again = run(d)
+        assert all(torch.equal(got[n], again[n]) for n in got)
 
 
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("nseg", [1, 2])
-def test_lengths(nseg, io):
+def test_lengths(io):
     """Rows of no, one and all tokens; what lies behind the lengths reaches nothing; lengths are clamped."""
     d = draw(4, 5, 150, 40, io)
     lengths = torch.tensor([150, 0, 1, 64, 97], dtype=torch.int32).cuda()
-    got = run(d, lengths, nsegments=nseg)
+    got = run(d, lengths)
     compare(d, got, lengths)
     for n in ("x", "r", "i", "dy"):
         d[n][1], d[n][2, 1:], d[n][3, 64:], d[n][4, 97:] = float("nan"), float("inf"), float("nan"), float("-inf")
-    again = run(d, torch.tensor([1 << 30, -5, 1, 64, 97], dtype=torch.int32).cuda(), nsegments=nseg)
+    again = run(d, torch.tensor([1 << 30, -5, 1, 64, 97], dtype=torch.int32).cuda())
     assert all(torch.equal(got[n], again[n]) for n in got)
     assert torch.equal(got["h"][1], d["h0"][1]) and torch.equal(got["dh0"][1], d["dh"][1])
     assert not got["y"][2, 1:].any() and not got["decay_gate"][4, 97:].any()
@@ -215,12 +228,12 @@ def test_prompt_continued_by_steps_is_the_prompt():
     check("h", state, ref["h"])
 
 
-@pytest.mark.parametrize("nseg", [1, 5])
-def test_state_in_place(nseg):
-    """h_final may be h0 itself, dh0 dh_final: segments that start later still see the first."""
+@pytest.mark.parametrize("L", [60, 1600])
+def test_state_in_place(L):
+    """h_final may be h0 itself, dh0 dh_final: tiles that start later still see the first."""
     from state_space_sequence_amd import m3
-    d = draw(3, 4, 1600, 700, torch.bfloat16)
-    kw = dict(input_gate=d["i"], nsegments=nseg)
+    d = draw(3, 4, L, 700, torch.bfloat16)
+    kw = dict(input_gate=d["i"])
     y, h = m3.recurrence_fwd(d["x"], d["r"], d["ld"], h0=d["h0"], **kw)
     g = m3.recurrence_bwd(d["x"], d["r"], d["ld"], d["dy"], h0=d["h0"], dh_final=d["dh"], **kw)
     for _ in range(3):
@@ -268,11 +281,11 @@ def test_empty_calls():
     assert m3.recurrence_step(n[:, 0], n[:, 0], ld, n[:, 0]).shape == (0, 6)
 
 
-@pytest.mark.parametrize("nseg", [1, 3])
-def test_captured_and_on_another_stream(nseg):
+@pytest.mark.parametrize("L", [50, 300])
+def test_captured_and_on_another_stream(L):
     from state_space_sequence_amd import m3
-    d = draw(7, 2, 300, 64, torch.bfloat16)
-    kw = dict(input_gate=d["i"], h0=d["h0"], nsegments=nseg)
+    d = draw(7, 2, L, 64, torch.bfloat16)
+    kw = dict(input_gate=d["i"], h0=d["h0"])
     state = torch.zeros(2, 64, device="cuda")
 
     def call(stream=None):

@@ -25,7 +25,7 @@ def m3():
 
 
 def shape(m3, **kw):
-    d = dict(batch=2, seqlen=1000, channels=64, io_dtype=m3.M3_BF16, flags=0, nsegments=3, reserved=0)
+    d = dict(batch=2, seqlen=1000, channels=64, io_dtype=m3.M3_BF16, flags=0)
     d.update(kw)
     return m3.RecShape(*(d[n] for n, _ in m3.RecShape._fields_))
 
@@ -44,9 +44,9 @@ def step(m3, s, io):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=-1), -1), (dict(seqlen=-1), -1), (dict(channels=0), -1), (dict(io_dtype=2), -1), (dict(flags=2), -1),
-    (dict(nsegments=-1), -1), (dict(reserved=1), -1), (dict(channels=(1 << 20) + 1), -2), (dict(batch=1 << 32), -2),
+    (dict(channels=(1 << 20) + 1), -2), (dict(batch=1 << 32), -2),
     (dict(seqlen=1 << 41), -2), (dict(batch=1 << 20, seqlen=1 << 21), -2), (dict(batch=1 << 24), -2),
-    (dict(batch=1 << 13, channels=1 << 17, seqlen=1 << 10), -2), (dict(seqlen=1 << 30, nsegments=1 << 24, batch=1), -2)])
+    (dict(batch=1 << 13, channels=1 << 17, seqlen=1 << 10), -2), (dict(seqlen=1 << 30, batch=1), -2)])
 def test_refused_shapes(m3, kw, code):
     s = shape(m3, **kw)
     assert fwd(m3, s, *filled(m3.RecIO())) == code
@@ -91,7 +91,7 @@ def test_required_aligned_and_workspace(m3):
     assert bwd(m3, s, io, g, (BIG[0], with_states - 1)) == -4
     io.states = None
     assert bwd(m3, s, io, g, (BIG[0], without - 1)) == -4
-    assert m3.recurrence_workspace_bytes(shape(m3, nsegments=1)) == 0
+    assert m3.recurrence_workspace_bytes(shape(m3, seqlen=128)) == 0
     for f, a in ((fwd, (None,)), (bwd, (None, g)), (bwd, (io, None)), (step, (None,))):
         assert f(m3, s, *a) == -1
     assert m3.lib.m3_recurrence_fwd(None, ctypes.byref(io), *BIG, None) == -1
@@ -101,17 +101,20 @@ def test_required_aligned_and_workspace(m3):
 def test_workspace_is_bounded(m3):
     """The kept states, the segments' maps and the sums: a small part of the tensors."""
     for b, L, C in ((1, 1 << 20, 64), (8, 4096, 4096), (1, 1, 1 << 20), (64, 100, 1000), (1, 65536, 8)):
-        s = shape(m3, batch=b, seqlen=L, channels=C, nsegments=0)
-        assert m3.recurrence_workspace_bytes(s) <= 12 * b * C * 64 + 1024
-        assert m3.recurrence_bwd_workspace_bytes(s) <= 4 * b * C * (L // 64 + 1) + 24 * b * C * 64 + 2048
+        s = shape(m3, batch=b, seqlen=L, channels=C)
+        # maps and states of tiles of 128 tokens (64 with gradients), and what the chain starts from
+        fwd = 12 * b * C * (L // 128 + 1) + 8 * b * C + 1024
+        assert m3.recurrence_workspace_bytes(s) <= fwd
+        # and kept states and sums of 64 tokens
+        assert m3.recurrence_bwd_workspace_bytes(s) <= fwd + (4 + 12 + 4) * b * C * (L // 64 + 1) + 8 * b * C + 2048
 
 
 IN = ("x", "decay_gate", "input_gate", "log_decay", "h0", "lengths")
 
 
-@pytest.mark.parametrize("nsegments", [1, 3])
-def test_a_pointer_given_twice(m3, nsegments):
-    s = shape(m3, nsegments=nsegments)
+@pytest.mark.parametrize("seqlen", [60, 1000])
+def test_a_pointer_given_twice(m3, seqlen):
+    s = shape(m3, seqlen=seqlen)
     for out in ("y", "h_final", "states"):
         for other in IN + ("y", "h_final", "states"):
             if other == out or (out, other) == ("h_final", "h0"):
