@@ -35,7 +35,8 @@
 extern "C" {
 #endif
 
-typedef enum { M3_ACT_NONE = 0, M3_ACT_SILU = 1 } m3_act;
+/* (the sigmoid is for the gate of m3_block_norm.h alone) */
+typedef enum { M3_ACT_NONE = 0, M3_ACT_SILU = 1, M3_ACT_SIGMOID = 2 } m3_act;
 
 typedef struct {
     int64_t rows;       /* >= 0 */

@@ -82,6 +82,22 @@ class NormGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "dx", "dz", "dweight", "dbias")]
 
 
+class BlockNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class BlockNormIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "x", "z", "residual", "post_weight", "pre_weight", "scale", "residual_out", "y")]
+
+
+class BlockNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "dy", "dresidual_out", "dx", "dz", "dresidual", "dpost_weight", "dpre_weight", "dscale")]
+
+
 class RecShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
                 ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
@@ -172,6 +188,13 @@ def _load():
         f = getattr(lib, name)
         f.restype = ctypes.c_size_t
         f.argtypes = [ctypes.POINTER(NormShape), ctypes.c_int]
+    lib.m3_block_norm_fwd.restype = ctypes.c_int
+    lib.m3_block_norm_fwd.argtypes = [ctypes.POINTER(BlockNormShape), ctypes.POINTER(BlockNormIO), ctypes.c_void_p]
+    lib.m3_block_norm_bwd.restype = ctypes.c_int
+    lib.m3_block_norm_bwd.argtypes = [ctypes.POINTER(BlockNormShape), ctypes.POINTER(BlockNormIO),
+                                      ctypes.POINTER(BlockNormGrads), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.m3_block_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.m3_block_norm_bwd_workspace_bytes.argtypes = [ctypes.POINTER(BlockNormShape)]
     lib.m3_recurrence_fwd.restype = ctypes.c_int
     lib.m3_recurrence_fwd.argtypes = [ctypes.POINTER(RecShape), ctypes.POINTER(RecIO), ctypes.c_void_p, ctypes.c_size_t,
                                       ctypes.c_void_p]
@@ -887,6 +910,128 @@ def group_norm_bwd(x, groups, dy, weight=None, bias=None, *, z=None, activation=
         _need("grads['z']", grads.get("z"))
     _on_gpu(dev)
     _launch(lib.m3_group_norm_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs), ws, wsb)
+    return grads
+
+
+# ------------------------- the norms around a block, its gate, scale and residual ---
+M3_BLOCK_ACT = {"none": 0, "silu": 1, "sigmoid": 2}
+M3_BLOCK_POST_NORM = 1
+M3_BLOCK_PRE_NORM = 2
+
+
+def _block_norm_call(x, z, activation, scale, post_norm, post_weight, pre_norm, pre_weight, residual_scale, eps,
+                     residual_dtype):
+    """The shape and the inputs of a block norm of x [..., C] but the residual streams, checked."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: expected a torch.Tensor")
+    iot = _io_dtype(x)
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x: expected [..., channels], got shape %s" % (tuple(x.shape),))
+    if activation not in M3_BLOCK_ACT:
+        raise ValueError("activation must be 'none', 'silu' or 'sigmoid'")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight: only with post_norm")
+    if pre_weight is not None and not pre_norm:
+        raise ValueError("pre_weight: only with pre_norm")
+    if residual_dtype is not torch.float32 and residual_dtype is not x.dtype:
+        raise TypeError("the residual stream must be float32 or of the dtype of x, got %s" % residual_dtype)
+    C, s, f32, dev = x.shape[-1], x.shape, torch.float32, x.get_device()
+    rows = 1
+    for n in s[:-1]:
+        rows *= int(n)
+    io = BlockNormIO(_arg("x", x, s, x.dtype, dev), _arg("z", z, s, x.dtype, dev), None,
+                     _arg("post_weight", post_weight, (C,), f32, dev), _arg("pre_weight", pre_weight, (C,), f32, dev),
+                     _arg("scale", scale, (C,), f32, dev))
+    flags = (M3_BLOCK_POST_NORM if post_norm else 0) | (M3_BLOCK_PRE_NORM if pre_norm else 0)
+    rt = M3_F32 if residual_dtype is torch.float32 else M3_BF16
+    return BlockNormShape(rows, C, iot, rt, M3_BLOCK_ACT[activation], eps, residual_scale, flags), io
+
+
+def block_norm_fwd(x, residual=None, *, z=None, activation="silu", scale=None, post_norm=False, post_weight=None,
+                   pre_norm=True, pre_weight=None, residual_scale=1.0, eps=1e-5, residual_dtype=None, y=None,
+                   residual_out=None, stream=None):
+    """What stands between two blocks, in one pass (m3_block_norm_fwd): with x [..., C] a block's output and
+    residual the stream around it (fp32 or of the dtype of x; None: 0),
+    v = rms_norm(x) * post_weight (post_norm; else v = x), R = residual_scale * residual + scale * act(z) * v,
+    y = rms_norm(R) * pre_weight (pre_norm). z: a gate like x or None, activation 'none', 'silu' or
+    'sigmoid'; scale, post_weight, pre_weight [C] fp32 or None (ones). residual_dtype: of R without a residual
+    (else as residual; x's by default). Returns (y or None, R)."""
+    given = residual if residual is not None else residual_out
+    if residual_dtype is None:
+        residual_dtype = given.dtype if isinstance(given, torch.Tensor) else getattr(x, "dtype", None)
+    shape, io = _block_norm_call(x, z, activation, scale, post_norm, post_weight, pre_norm, pre_weight,
+                                 residual_scale, eps, residual_dtype)
+    dev = x.get_device()
+    io.residual = _arg("residual", residual, x.shape, residual_dtype, dev)
+    io.residual_out = _arg("residual_out", residual_out, x.shape, residual_dtype, dev)
+    io.y = _arg("y", y, x.shape, x.dtype, dev)
+    if y is not None and not pre_norm:
+        raise ValueError("y: only with pre_norm")
+    _on_gpu(dev)
+    with _owned_by(stream):
+        if residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual_dtype, device=x.device)
+            io.residual_out = residual_out.data_ptr()
+        if y is None and pre_norm:
+            y = x.new_empty(x.shape)
+            io.y = y.data_ptr()
+    _launch(lib.m3_block_norm_fwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io))
+    return y, residual_out
+
+
+def block_norm_bwd(x, residual_out, dy, dresidual_out=None, *, z=None, activation="silu", scale=None, post_norm=False,
+                   post_weight=None, pre_norm=True, pre_weight=None, residual_scale=1.0, eps=1e-5, want_dresidual=True,
+                   grads=None, workspace=None, stream=None):
+    """Gradients of <dy, y> + <dresidual_out, R> of block_norm_fwd (m3_block_norm_bwd), from x, z and the stored
+    stream residual_out = R (dy is None without pre_norm; dresidual_out may be None with it). Returns a dict:
+    x, and z with a gate, in the dtype of x; residual in that of the stream, where wanted; post_weight,
+    pre_weight, scale [C] in fp32 where they were given. grads: such a dict to write into (x, and z with a
+    gate, required)."""
+    if not isinstance(residual_out, torch.Tensor):
+        raise TypeError("residual_out: expected a torch.Tensor")
+    rt = residual_out.dtype
+    shape, io = _block_norm_call(x, z, activation, scale, post_norm, post_weight, pre_norm, pre_weight,
+                                 residual_scale, eps, rt)
+    if pre_norm:
+        _need("dy", dy)
+    else:
+        _need("dresidual_out", dresidual_out)
+        if dy is not None:
+            raise ValueError("dy: only with pre_norm")
+    C, s, f32, dev = x.shape[-1], x.shape, torch.float32, x.get_device()
+    io.residual_out = _arg("residual_out", residual_out, s, rt, dev)
+    gs = BlockNormGrads(_arg("dy", dy, s, x.dtype, dev), _arg("dresidual_out", dresidual_out, s, rt, dev))
+    ws, wsb = _workspace(workspace, dev)
+    weights = [(n, t) for n, t in (("post_weight", post_weight), ("pre_weight", pre_weight), ("scale", scale)) if t is not None]
+    with _owned_by(stream):
+        if grads is None:
+            grads = {"x": torch.empty(s, dtype=x.dtype, device=x.device)}
+            if z is not None:
+                grads["z"] = torch.empty(s, dtype=x.dtype, device=x.device)
+            if want_dresidual:
+                grads["residual"] = torch.empty(s, dtype=rt, device=x.device)
+            for name, _ in weights:
+                grads[name] = torch.empty((C,), dtype=f32, device=x.device)
+        want = {"x": (s, x.dtype), "residual": (s, rt)}
+        if z is not None:
+            want["z"] = (s, x.dtype)
+        for name, _ in weights:
+            want[name] = ((C,), f32)
+        sums = False
+        for name, t in grads.items():
+            if name not in want:
+                raise ValueError("grads: unknown entry %r" % name)
+            setattr(gs, "d" + name, _arg("grads[%r]" % name, t, *want[name], dev))
+            sums = sums or (t is not None and name not in ("x", "z", "residual"))
+        _need("grads['x']", grads.get("x"))
+        if z is not None:
+            _need("grads['z']", grads.get("z"))
+        _on_gpu(dev)
+        need = lib.m3_block_norm_bwd_workspace_bytes(ctypes.byref(shape)) if sums else 0
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws, wsb = workspace.data_ptr(), need
+    _launch(lib.m3_block_norm_bwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io), ctypes.byref(gs), ws, wsb)
     return grads
 
 
