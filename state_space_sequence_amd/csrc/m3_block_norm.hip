@@ -21,7 +21,8 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kChainRows = 256;  // rows whose weight gradients a thread adds up in fp32
-constexpr int64_t kMaxGrid = 0x3fffff;
+constexpr int64_t kMaxGrid = 0x3fffff;  // workgroups of 1024 threads: 2^32 threads
+constexpr int64_t kLastCache = 256 << 20;
 
 struct BlockArgs {
     const void *x, *z, *r;
@@ -35,6 +36,7 @@ struct BlockArgs {
     float eps, alpha;
     int act;
     bool post, pre, sums;
+    bool past;  // stores past the caches
 };
 
 // V consecutive values of one dtype as they lie in memory
@@ -85,8 +87,10 @@ __device__ __forceinline__ void unpack(const Packed<BF16, V> &o, float (&x)[V]) 
         else x[e] = __uint_as_float(e % 2 ? o.w[e / 2] & 0xffff0000u : o.w[e / 2] << 16);
     }
 }
-template <bool BF16, int V, bool VEC>
-__device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V]) {
+// Past the caches: forwards where the tensors of the call do not fit them (ASK, past), with gradients always (b4 L4096 of 4096
+// channels 222 us by kernel trace, with the question 227)
+template <bool BF16, int V, bool VEC, bool ASK>
+__device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V], bool past) {
     constexpr int W = Packed<BF16, V>::W;
     if constexpr (VEC) {
         unsigned w[W];
@@ -96,9 +100,20 @@ __device__ __forceinline__ void store(void *p, int64_t i, int live, const float 
             else w[e] = __float_as_uint(x[e]);
         }
         if (live > 0) {
-            char *at = static_cast<char *>(p) + i * (BF16 ? 2 : 4);
-            if constexpr (W == 4) __builtin_nontemporal_store((u32x4{w[0], w[1], w[2], w[3]}), reinterpret_cast<u32x4 *>(at));
-            else __builtin_nontemporal_store((u32x2{w[0], w[1]}), reinterpret_cast<u32x2 *>(at));
+            typedef unsigned vec __attribute__((ext_vector_type(W)));
+            vec v;
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = w[e];
+            vec *to = reinterpret_cast<vec *>(static_cast<char *>(p) + i * (BF16 ? 2 : 4));
+            if constexpr (!ASK) {
+                __builtin_nontemporal_store(v, to);
+            } else if (past) {
+                asm volatile("");  // (two equal stores but for their hint would become one)
+                __builtin_nontemporal_store(v, to);
+                asm volatile("");
+            } else {
+                *to = v;
+            }
         }
     } else {
 #pragma unroll
@@ -237,7 +252,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void fwd_kern
             }
         const bool here = row < a.n;
 #pragma unroll
-        for (int k = 0; k < CH; ++k) store<RF, V, VEC>(a.R, row * a.C + p.c[k], here ? p.live[k] : 0, R[k]);
+        for (int k = 0; k < CH; ++k) store<RF, V, VEC, true>(a.R, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
         if (a.pre) {
             At::sum(s, lds, slot);
             const float rR = 1.f / sqrtf(s[0] * inv + a.eps);
@@ -245,7 +260,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void fwd_kern
             for (int k = 0; k < CH; ++k) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) R[k][e] *= rR * wp[k][e];
-                store<BF, V, VEC>(a.y, row * a.C + p.c[k], here ? p.live[k] : 0, R[k]);
+                store<BF, V, VEC, true>(a.y, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
             }
         }
     }
@@ -332,7 +347,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[e] = a.alpha * d[k][e];
-                store<RF, V, VEC>(a.dr, at, live, o);
+                store<RF, V, VEC, false>(a.dr, at, live, o, a.past);
             }
             float o[V];
 #pragma unroll
@@ -352,7 +367,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
                 d[k][e] *= w[k][e];
                 t[0] = __builtin_fmaf(d[k][e], n, t[0]);
             }
-            if (a.z) store<BF, V, VEC>(a.dz, at, live, o);
+            if (a.z) store<BF, V, VEC, false>(a.dz, at, live, o, a.past);
         }
         if (a.post) {
             At::sum(t, lds, slot);
@@ -363,7 +378,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
             if (a.post)
 #pragma unroll
                 for (int e = 0; e < V; ++e) d[k][e] = rx * (d[k][e] - xs[k][e] * t[0]);
-            store<BF, V, VEC>(a.dx, row * a.C + p.c[k], here ? p.live[k] : 0, d[k]);
+            store<BF, V, VEC, false>(a.dx, row * a.C + p.c[k], here ? p.live[k] : 0, d[k], a.past);
         }
     }
     if (!a.sums) return;
@@ -447,7 +462,9 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
     p->pieces = need <= p->lanes ? 1 : (need <= 2 * p->lanes ? 2 : 4);
     const int threads = p->lanes < 256 ? 256 : p->lanes, rows = threads / p->lanes;
     const int64_t passes = ceil_div(s->rows, rows);
-    const int64_t fwd = 256 * 2048 / threads, bwd = 256 * 1024 / threads;
+    // A CU with 1024 threads of them forwards (b8 L4096 of 2048 channels with an fp32 stream 165 us; 2048 172, 4096 168), 512 with
+    // gradients, each with its own sums of the weights (b4 L4096 of 4096 219 us by kernel trace; 1024 238, 2048 254)
+    const int64_t fwd = 256 * 1024 / threads, bwd = 256 * 512 / threads;
     p->fwd = passes < fwd ? passes : fwd;
     p->bwd = passes < bwd ? passes : bwd;
     if (p->bwd * kChainRows < passes) p->bwd = ceil_div(passes, kChainRows);
@@ -479,8 +496,11 @@ hipError_t launch_lanes(const BlockArgs &a, const BlockPlan &p, bool bwd, hipStr
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_any(const m3_block_norm_shape &s, const BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t hs) {
+hipError_t launch_any(const m3_block_norm_shape &s, BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t hs) {
     const bool bf = s.io_dtype == M3_BF16, rf = s.residual_dtype == M3_BF16;
+    // x, y and the gate, with gradients theirs; the stream before and behind, and its gradients
+    const int64_t each = (bf ? 2 : 4) * ((bwd ? 3 : 2) + (a.z ? (bwd ? 2 : 1) : 0)) + (rf ? 2 : 4) * (bwd ? 3 : 2);
+    a.past = a.n * a.C > kLastCache / each;
     if (bf && rf)
         return p.vec ? launch_lanes<true, true, 8, true>(a, p, bwd, hs) : launch_lanes<true, true, 8, false>(a, p, bwd, hs);
     if (bf)
@@ -529,7 +549,8 @@ m3_status m3_block_norm_fwd(const m3_block_norm_shape *shape, const m3_block_nor
         clash({io->residual_out}, {io->x, io->z}) || clash({io->y}, {io->residual}))
         return M3_ERR_INVALID_ARG;
     if (shape->rows == 0) return M3_OK;
-    const hipError_t e = launch_any(*shape, block_args(*shape, *io), p, false, reinterpret_cast<hipStream_t>(stream));
+    BlockArgs a = block_args(*shape, *io);
+    const hipError_t e = launch_any(*shape, a, p, false, reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
 
