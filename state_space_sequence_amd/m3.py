@@ -98,6 +98,17 @@ class BlockNormGrads(ctypes.Structure):
         "dy", "dresidual_out", "dx", "dz", "dresidual", "dpost_weight", "dpre_weight", "dscale")]
 
 
+class RotaryShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("headdim", ctypes.c_int64), ("rotary", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class RotaryIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "freqs", "positions", "offsets", "q_out", "k_out")]
+
+
 class RecShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
                 ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
@@ -195,6 +206,8 @@ def _load():
                                       ctypes.POINTER(BlockNormGrads), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.m3_block_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.m3_block_norm_bwd_workspace_bytes.argtypes = [ctypes.POINTER(BlockNormShape)]
+    lib.m3_rotary.restype = ctypes.c_int
+    lib.m3_rotary.argtypes = [ctypes.POINTER(RotaryShape), ctypes.POINTER(RotaryIO), ctypes.c_void_p]
     lib.m3_recurrence_fwd.restype = ctypes.c_int
     lib.m3_recurrence_fwd.argtypes = [ctypes.POINTER(RecShape), ctypes.POINTER(RecIO), ctypes.c_void_p, ctypes.c_size_t,
                                       ctypes.c_void_p]
@@ -1162,6 +1175,95 @@ def recurrence_step(x, decay_gate, log_decay, h, *, input_gate=None, scaled=True
         ptrs.y = y.data_ptr()
     _launch(lib.m3_recurrence_step, x.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
     return y
+
+
+# -------------------------------------------------------- rotary positions ---
+M3_ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
+M3_ROTARY_BACKWARD = 2
+
+
+def rotary_frequencies(rotary, base=10000.0, *, scaling=None, factor=1.0, trained_length=None, fast=32.0, slow=1.0,
+                       device=None):
+    """Frequencies for rotary() of `rotary` turned channels: base ** (-2 i / rotary), fp32 [rotary / 2]. For
+    contexts `factor` times the trained length, scaling is "linear" (positions divided by factor), "base" (the
+    base times factor ** (rotary / (rotary - 2)), so that the slowest turns as with "linear" and the fastest as before)
+    or "parts" (pairs that turn more than `fast` times within trained_length as before, those that turn less than `slow`
+    times divided by factor, linear in their turns between)."""
+    if isinstance(rotary, bool) or not isinstance(rotary, int) or rotary < 0 or rotary % 2:
+        raise ValueError("rotary: expected an even number of channels, got %r" % (rotary,))
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling == "base":
+        if rotary < 4:
+            raise ValueError("scaling='base': at least 4 channels")
+        base = base * factor ** (rotary / (rotary - 2))
+    i = torch.arange(rotary // 2, dtype=torch.float64)
+    freqs = base ** (-2 * i / max(rotary, 1))
+    if scaling == "linear":
+        freqs = freqs / factor
+    elif scaling == "parts":
+        if trained_length is None or not trained_length > 0 or not fast > slow:
+            raise ValueError("scaling='parts': trained_length is required, and fast > slow")
+        turns = trained_length * freqs / (2 * torch.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        freqs = freqs * (keep + (1 - keep) / factor)
+    return freqs.float().to(device)
+
+
+def rotary(q, k, freqs, *, positions=None, offsets=None, layout="half", scale=1.0, backward=False, q_out=None, k_out=None,
+           stream=None):
+    """Queries and keys turned by their positions (m3_rotary): q [b,L,H,D], k [b,L,G,D] or None (or [b,H,D],
+    [b,G,D]: a token a row), freqs [rotary/2] fp32 radians a position (rotary_frequencies), of the first `rotary`
+    channels of a head; the others are copied. Pairs are channels (i, i + rotary/2) with layout="half",
+    (2i, 2i+1) with "interleaved". Positions: positions int32 of the shape of the tokens, or offsets [b]
+    int32 of each row's first token, or 0 1 2 ... . scale: a factor on the turned channels. backward: q and k are
+    gradients of the outputs, turned back. q_out may be q, k_out k. Returns (q_out, k_out)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q: expected a torch.Tensor")
+    iot = _io_dtype(q)
+    if q.dim() not in (3, 4):
+        raise ValueError("q: expected [batch, length, heads, channels] or [batch, heads, channels], got shape %s" % (
+            tuple(q.shape),))
+    if layout not in M3_ROTARY_LAYOUT:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    _need("freqs", freqs)
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise TypeError("freqs: expected a torch.Tensor of one dimension")
+    if positions is not None and offsets is not None:
+        raise ValueError("positions or offsets, not both")
+    io, dev, lead, (H, D) = q.dtype, q.get_device(), q.shape[:-2], q.shape[-2:]
+    if H == 0 or D == 0:
+        raise ValueError("q: no heads or channels, got shape %s" % (tuple(q.shape),))
+    n = freqs.shape[0]
+    if 2 * n > D:
+        raise ValueError("freqs: %d pairs are more than the %d channels of a head" % (n, D))
+    G = 0
+    if k is not None:
+        ks = _dims5("k", k, q.dim())
+        G = ks[-2]
+        if G == 0:
+            raise ValueError("k: no heads, got shape %s" % (ks,))
+    sk = tuple(lead) + (G, D)
+    if k is None and k_out is not None:
+        raise ValueError("k_out: only with k")
+    ptrs = RotaryIO(_arg("q", q, q.shape, io, dev), _arg("k", k, sk, io, dev),
+                    _arg("freqs", freqs, (n,), torch.float32, dev), _arg("positions", positions, lead, torch.int32, dev),
+                    _arg("offsets", offsets, lead[:1], torch.int32, dev), _arg("q_out", q_out, q.shape, io, dev),
+                    _arg("k_out", k_out, sk, io, dev))
+    _on_gpu(dev)
+    shape = RotaryShape(lead[0], lead[1] if len(lead) > 1 else 1, H, G, D, 2 * n, iot,
+                        M3_ROTARY_LAYOUT[layout] | (M3_ROTARY_BACKWARD if backward else 0), scale, 0)
+    with _owned_by(stream):
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+            ptrs.q_out = q_out.data_ptr()
+        if k is not None and k_out is None:
+            k_out = k.new_empty(sk)
+            ptrs.k_out = k_out.data_ptr()
+    _launch(lib.m3_rotary, q.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
+    return q_out, k_out
 
 
 # ------------------------------------------------------ calibration probes ---
