@@ -948,16 +948,20 @@ def _block_norm_call(x, z, activation, scale, post_norm, post_weight, pre_norm, 
         raise ValueError("pre_weight: only with pre_norm")
     if residual_dtype is not torch.float32 and residual_dtype is not x.dtype:
         raise TypeError("the residual stream must be float32 or of the dtype of x, got %s" % residual_dtype)
-    C, s, f32, dev = x.shape[-1], x.shape, torch.float32, x.get_device()
-    rows = 1
-    for n in s[:-1]:
-        rows *= int(n)
-    io = BlockNormIO(_arg("x", x, s, x.dtype, dev), _arg("z", z, s, x.dtype, dev), None,
-                     _arg("post_weight", post_weight, (C,), f32, dev), _arg("pre_weight", pre_weight, (C,), f32, dev),
-                     _arg("scale", scale, (C,), f32, dev))
+    s, f32, dev = x.shape, torch.float32, x.get_device()
+    C = s[-1]
+    io = BlockNormIO(_arg("x", x, s, x.dtype, dev))
+    if z is not None:
+        io.z = _arg("z", z, s, x.dtype, dev)
+    if post_weight is not None:
+        io.post_weight = _arg("post_weight", post_weight, (C,), f32, dev)
+    if pre_weight is not None:
+        io.pre_weight = _arg("pre_weight", pre_weight, (C,), f32, dev)
+    if scale is not None:
+        io.scale = _arg("scale", scale, (C,), f32, dev)
     flags = (M3_BLOCK_POST_NORM if post_norm else 0) | (M3_BLOCK_PRE_NORM if pre_norm else 0)
     rt = M3_F32 if residual_dtype is torch.float32 else M3_BF16
-    return BlockNormShape(rows, C, iot, rt, M3_BLOCK_ACT[activation], eps, residual_scale, flags), io
+    return BlockNormShape(x.numel() // C, C, iot, rt, M3_BLOCK_ACT[activation], eps, residual_scale, flags), io
 
 
 def block_norm_fwd(x, residual=None, *, z=None, activation="silu", scale=None, post_norm=False, post_weight=None,
@@ -974,19 +978,22 @@ def block_norm_fwd(x, residual=None, *, z=None, activation="silu", scale=None, p
         residual_dtype = given.dtype if isinstance(given, torch.Tensor) else getattr(x, "dtype", None)
     shape, io = _block_norm_call(x, z, activation, scale, post_norm, post_weight, pre_norm, pre_weight,
                                  residual_scale, eps, residual_dtype)
-    dev = x.get_device()
-    io.residual = _arg("residual", residual, x.shape, residual_dtype, dev)
-    io.residual_out = _arg("residual_out", residual_out, x.shape, residual_dtype, dev)
-    io.y = _arg("y", y, x.shape, x.dtype, dev)
-    if y is not None and not pre_norm:
-        raise ValueError("y: only with pre_norm")
+    dev, sx = x.get_device(), x.shape
+    if residual is not None:
+        io.residual = _arg("residual", residual, sx, residual_dtype, dev)
+    if residual_out is not None:
+        io.residual_out = _arg("residual_out", residual_out, sx, residual_dtype, dev)
+    if y is not None:
+        io.y = _arg("y", y, sx, x.dtype, dev)
+        if not pre_norm:
+            raise ValueError("y: only with pre_norm")
     _on_gpu(dev)
     with _owned_by(stream):
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=residual_dtype, device=x.device)
+            residual_out = torch.empty_like(x, dtype=residual_dtype) if residual is None else torch.empty_like(residual)
             io.residual_out = residual_out.data_ptr()
         if y is None and pre_norm:
-            y = x.new_empty(x.shape)
+            y = torch.empty_like(x)
             io.y = y.data_ptr()
     _launch(lib.m3_block_norm_fwd, x.device, stream, ctypes.byref(shape), ctypes.byref(io))
     return y, residual_out
@@ -1164,14 +1171,17 @@ def recurrence_step(x, decay_gate, log_decay, h, *, input_gate=None, scaled=True
     _need("decay_gate", decay_gate)
     _need("log_decay", log_decay)
     _need("h", h)
-    ptrs = RecStepIO(_arg("x", x, s, io, dev), _arg("decay_gate", decay_gate, s, io, dev),
-                     _arg("input_gate", input_gate, s, io, dev), _arg("log_decay", log_decay, (C,), f32, dev),
-                     _arg("h", h, s, f32, dev), _arg("y", y, s, io, dev))
+    ptrs = RecStepIO(_arg("x", x, s, io, dev), _arg("decay_gate", decay_gate, s, io, dev), None,
+                     _arg("log_decay", log_decay, (C,), f32, dev), _arg("h", h, s, f32, dev))
+    if input_gate is not None:
+        ptrs.input_gate = _arg("input_gate", input_gate, s, io, dev)
+    if y is not None:
+        ptrs.y = _arg("y", y, s, io, dev)
     _on_gpu(dev)
     shape = RecShape(b, 1, C, iot, 0 if scaled else M3_REC_UNSCALED)
     if y is None:
         with _owned_by(stream):
-            y = x.new_empty(s)
+            y = torch.empty_like(x)
         ptrs.y = y.data_ptr()
     _launch(lib.m3_recurrence_step, x.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
     return y
@@ -1222,46 +1232,54 @@ def rotary(q, k, freqs, *, positions=None, offsets=None, layout="half", scale=1.
     gradients of the outputs, turned back. q_out may be q, k_out k. Returns (q_out, k_out)."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q: expected a torch.Tensor")
-    iot = _io_dtype(q)
-    if q.dim() not in (3, 4):
-        raise ValueError("q: expected [batch, length, heads, channels] or [batch, heads, channels], got shape %s" % (
-            tuple(q.shape),))
+    iot, io, sq, dev = _io_dtype(q), q.dtype, q.shape, q.get_device()
+    if len(sq) == 4:
+        b, L, H, D = sq
+        lead = (b, L)
+    elif len(sq) == 3:
+        (b, H, D), L = sq, 1
+        lead = (b,)
+    else:
+        raise ValueError("q: expected [batch, length, heads, channels] or [batch, heads, channels], got shape %s" % (tuple(sq),))
     if layout not in M3_ROTARY_LAYOUT:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    _need("freqs", freqs)
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        _need("freqs", freqs)
         raise TypeError("freqs: expected a torch.Tensor of one dimension")
-    if positions is not None and offsets is not None:
-        raise ValueError("positions or offsets, not both")
-    io, dev, lead, (H, D) = q.dtype, q.get_device(), q.shape[:-2], q.shape[-2:]
     if H == 0 or D == 0:
-        raise ValueError("q: no heads or channels, got shape %s" % (tuple(q.shape),))
-    n = freqs.shape[0]
+        raise ValueError("q: no heads or channels, got shape %s" % (tuple(sq),))
+    n, G, sk = len(freqs), 0, None
     if 2 * n > D:
         raise ValueError("freqs: %d pairs are more than the %d channels of a head" % (n, D))
-    G = 0
+    ptrs = RotaryIO(_arg("q", q, sq, io, dev), None, _arg("freqs", freqs, (n,), torch.float32, dev))
     if k is not None:
-        ks = _dims5("k", k, q.dim())
-        G = ks[-2]
+        G = _dims5("k", k, len(sq))[-2]
+        sk = lead + (G, D)
+        ptrs.k = _arg("k", k, sk, io, dev)
         if G == 0:
-            raise ValueError("k: no heads, got shape %s" % (ks,))
-    sk = tuple(lead) + (G, D)
-    if k is None and k_out is not None:
+            raise ValueError("k: no heads, got shape %s" % (sk,))
+    elif k_out is not None:
         raise ValueError("k_out: only with k")
-    ptrs = RotaryIO(_arg("q", q, q.shape, io, dev), _arg("k", k, sk, io, dev),
-                    _arg("freqs", freqs, (n,), torch.float32, dev), _arg("positions", positions, lead, torch.int32, dev),
-                    _arg("offsets", offsets, lead[:1], torch.int32, dev), _arg("q_out", q_out, q.shape, io, dev),
-                    _arg("k_out", k_out, sk, io, dev))
+    if positions is not None:
+        ptrs.positions = _arg("positions", positions, lead, torch.int32, dev)
+        if offsets is not None:
+            raise ValueError("positions or offsets, not both")
+    elif offsets is not None:
+        ptrs.offsets = _arg("offsets", offsets, (b,), torch.int32, dev)
+    if q_out is not None:
+        ptrs.q_out = _arg("q_out", q_out, sq, io, dev)
+    if k_out is not None:
+        ptrs.k_out = _arg("k_out", k_out, sk, io, dev)
     _on_gpu(dev)
-    shape = RotaryShape(lead[0], lead[1] if len(lead) > 1 else 1, H, G, D, 2 * n, iot,
-                        M3_ROTARY_LAYOUT[layout] | (M3_ROTARY_BACKWARD if backward else 0), scale, 0)
-    with _owned_by(stream):
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-            ptrs.q_out = q_out.data_ptr()
-        if k is not None and k_out is None:
-            k_out = k.new_empty(sk)
-            ptrs.k_out = k_out.data_ptr()
+    if q_out is None or (k is not None and k_out is None):
+        with _owned_by(stream):
+            if q_out is None:
+                q_out = torch.empty_like(q)
+                ptrs.q_out = q_out.data_ptr()
+            if k is not None and k_out is None:
+                k_out = torch.empty_like(k)
+                ptrs.k_out = k_out.data_ptr()
+    shape = RotaryShape(b, L, H, G, D, 2 * n, iot, M3_ROTARY_LAYOUT[layout] | (M3_ROTARY_BACKWARD if backward else 0), scale, 0)
     _launch(lib.m3_rotary, q.device, stream, ctypes.byref(shape), ctypes.byref(ptrs))
     return q_out, k_out
 
