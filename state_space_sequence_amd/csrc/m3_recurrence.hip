@@ -20,7 +20,7 @@
 //
 // Bound by HBM and, nearly as much, by vector issue: 34 instructions an element, 5 of them exponentials, reciprocals and roots, 53 ns
 // an element of a wave on a SIMD, so 110 us of the prompt's 206. bf16, with an input gate: prompt b8 L4096 of 4096
-// channels 206 us (5.2 TB/s), long b2 L32768 of 2560 in a chain 309 (4.3 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
+// channels 206 us (5.2 TB/s), long b2 L32768 of 2560 in a chain 300 (4.5 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
 #include <math.h>
 
 #include <type_traits>
@@ -239,11 +239,13 @@ __device__ __forceinline__ void give_end(const RecArgs &a, int row, int k, int c
     put(a.ends + ((int64_t)row * a.ntile + k) * a.C + c, word(h));
 }
 
-// What tile k starts from, for one channel a lane: the nearest state before it that is known, and the maps from there
-__device__ __forceinline__ float chain(const RecArgs &a, int row, int k, int c, bool in) {
+// What tile k starts from, for one channel a lane: the nearest state before it that is known, and the maps from there.
+// `meanwhile` runs while the words first come
+template <class F>
+__device__ __forceinline__ float chain(const RecArgs &a, int row, int k, int c, bool in, F meanwhile) {
     const uint64_t *map = a.maps + ((int64_t)row * a.ntile + k - 1) * a.C + c;
     const unsigned *end = a.ends + ((int64_t)row * a.ntile + k - 1) * a.C + c, *begin = a.begins + (int64_t)row * a.C + c;
-    while (true) {
+    for (bool again = false;; again = true) {
         uint64_t m[kWindow - 1];
         unsigned e[kWindow];
 #pragma unroll
@@ -256,6 +258,7 @@ __device__ __forceinline__ float chain(const RecArgs &a, int row, int k, int c, 
             m[j] = kEmpty;
             if (in && j < k) m[j] = get(map - (int64_t)j * a.C);
         }
+        if (!again) meanwhile();
         bool known = false;
         float h = 0.f;
 #pragma unroll
@@ -390,40 +393,49 @@ __global__ __launch_bounds__(kThreads, 2) void fwd_kernel(const RecArgs a) {
         }
         if (CHAIN && threadIdx.x == 0) taken[2 + (turn & 1)] = later;
         __syncthreads();  // (two sides of maps: the next tile's are written while these are read)
+        float hw[V];
         if constexpr (CHAIN) {
             later = __builtin_amdgcn_readfirstlane(taken[2 + (turn & 1)]);
-            // (the state behind the tile is always that of its joint map, whoever forms it: the same bits)
+            // The maps of the runs before this one, and of all. (The state behind the tile is always that of the joint map,
+            // whoever forms it: the same bits)
+            float PA[V], PB[V];
+            auto fold = [&] {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                A[v] = 1.f;
-                B[v] = 0.f;
-#pragma unroll
-                for (int j = 0; j < kW; ++j) {
-                    A[v] *= maps[0][j][p.lane * V + v];
-                    B[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], B[v], maps[1][j][p.lane * V + v]);
+                for (int v = 0; v < V; ++v) {
+                    A[v] = 1.f;
+                    B[v] = 0.f;
                 }
-                if (p.wave == 0 && p.in && k + 1 < a.ntile) give_map(a, p.row, k, p.c + v, A[v], B[v]);
+#pragma unroll
+                for (int j = 0; j < kW; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (j == p.wave) {
+                            PA[v] = A[v];
+                            PB[v] = B[v];
+                        }
+                        B[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], B[v], maps[1][j][p.lane * V + v]);
+                        A[v] *= maps[0][j][p.lane * V + v];
+                    }
+            };
+            // the first wave publishes, the last V look for the start, a channel a lane
+            const bool look = k != last + 1;
+            if (look && p.wave >= kW - V) {
+                const int l = (p.wave - (kW - V)) * 64 + p.lane, c = p.c + l - p.lane * V;
+                first[l] = chain(a, p.row, k, c, c < a.C, fold);
+            } else {
+                fold();
+                if (p.wave == 0 && p.in && k + 1 < a.ntile)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) give_map(a, p.row, k, p.c + v, A[v], B[v]);
             }
-            if (k != last + 1) {
-                if (p.wave < V) {  // (a channel a lane)
-                    const int c = p.c + (p.wave * 64 + p.lane) - p.lane * V;
-                    first[p.wave * 64 + p.lane] = chain(a, p.row, k, c, c < a.C);
-                }
+            if (look) {
                 __syncthreads();
 #pragma unroll
                 for (int v = 0; v < V; ++v) h[v] = first[p.lane * V + v];
             }
-        }
-        float hw[V];
-        if constexpr (CHAIN) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) hw[v] = h[v];
-            for (int j = 0; j < p.wave; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    hw[v] = __builtin_fmaf(maps[0][j][p.lane * V + v], hw[v], maps[1][j][p.lane * V + v]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                hw[v] = __builtin_fmaf(PA[v], h[v], PB[v]);
                 h[v] = __builtin_fmaf(A[v], h[v], B[v]);
                 if (p.wave == 0 && p.in && k + 1 < a.ntile) give_end(a, p.row, k, p.c + v, h[v]);
             }
@@ -611,7 +623,7 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(const RecArgs a) {
             if (k != last + 1) {
                 if (p.wave < V) {  // (a channel a lane)
                     const int c = p.c + (p.wave * 64 + p.lane) - p.lane * V;
-                    first[p.wave * 64 + p.lane] = chain(a, p.row, k, c, c < a.C);
+                    first[p.wave * 64 + p.lane] = chain(a, p.row, k, c, c < a.C, [] {});
                 }
                 __syncthreads();
 #pragma unroll
