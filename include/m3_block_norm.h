@@ -13,7 +13,8 @@
  *     [channels] fp32 or NULL (ones). Sums are fp32 within a row; those over rows
  *     fp32 for at most 256 rows, one after another, and fp64 beyond; each output is
  *     rounded once. A row of zeros with an eps of 0 gives NaN.
- * channels: 1 to 32768 where x and r are both bf16, else to 16384.
+ * channels: 1 to 2^20; rows * channels <= 2^44 (else M3_ERR_UNSUPPORTED). Rows of over 16384 channels (8192 with
+ * gradients) are read two or three times.
  *
  * Conventions as in m3.h: dense row-major tensors, 16-byte aligned pointers, the
  * caller owns every buffer and the workspace (contents need not be initialised
@@ -76,7 +77,8 @@ m3_status m3_block_norm_fwd(const m3_block_norm_shape *shape, const m3_block_nor
 /* dpost_weight and dpre_weight need their norms. */
 m3_status m3_block_norm_bwd(const m3_block_norm_shape *shape, const m3_block_norm_io *io,
                             const m3_block_norm_grads *grads, void *workspace, size_t ws_bytes, void *stream);
-/* Bytes of device workspace m3_block_norm_bwd needs where it forms a weight's gradient (0 for a refused shape). */
+/* Bytes of device workspace m3_block_norm_bwd needs (0 for a refused shape); without a weight's gradient
+ * it needs none up to 8192 channels. */
 size_t m3_block_norm_bwd_workspace_bytes(const m3_block_norm_shape *shape);
 
 #ifdef __cplusplus

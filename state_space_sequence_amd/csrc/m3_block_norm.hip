@@ -16,8 +16,6 @@ namespace m3i {
 namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kChainRows = 256;  // rows whose weight gradients a thread adds up in fp32
@@ -30,13 +28,15 @@ struct BlockArgs {
     void *R, *y;
     const void *dy, *dR;
     void *dx, *dz, *dr;
-    float *part;  // [workgroups][3][C]: sums of dw, dwp, dsc
+    float *part;   // [workgroups][3][C]: sums of dw, dwp, dsc
+    float *stats;  // (wide rows) [n][kStats]
     int64_t n;
     int C;
     float eps, alpha;
     int act;
     bool post, pre, sums;
     bool past;  // stores past the caches
+    int rows;   // (wide rows) rows of a workgroup that sums columns
 };
 
 // V consecutive values of one dtype as they lie in memory
@@ -46,37 +46,31 @@ struct Packed {
     unsigned w[W];
 };
 
-// VEC: live is 0 or V, one access of 8 or 16 bytes (two of an fp32 V of 8 do not occur)
-template <bool BF16, int V, bool VEC>
+// N words at an address that is aligned to the values alone (rows of odd widths): one access all the same
+template <bool BF16, int N, bool WHOLE>
+struct Words {
+    typedef unsigned any __attribute__((ext_vector_type(N), aligned(WHOLE ? 4 * N : BF16 ? 2 : 4)));
+};
+
+// `live` of V values: all of them in one access of 8 or 16 bytes, fewer one by one. WHOLE: rows of a whole number of aligned
+// accesses, live is 0 or V (the question costs the gradients of b4 L4096 of 4096 channels 196 -> 247 us)
+template <bool BF16, int V, bool WHOLE>
 __device__ __forceinline__ void load(const void *p, int64_t i, int live, Packed<BF16, V> &o) {
     constexpr int W = Packed<BF16, V>::W;
-    if constexpr (VEC) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) o.w[e] = 0;
-        if (live > 0) {
-            const char *at = static_cast<const char *>(p) + i * (BF16 ? 2 : 4);
-            if constexpr (W == 4) {
-                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
+    for (int e = 0; e < W; ++e) o.w[e] = 0;
+    const char *at = static_cast<const char *>(p) + i * (BF16 ? 2 : 4);
+    if (WHOLE ? live > 0 : live == V) {
+        const auto v = __builtin_nontemporal_load(reinterpret_cast<const typename Words<BF16, W, WHOLE>::any *>(at));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o.w[e] = v[e];
-            } else {
-                static_assert(W == 2, "8 or 16 bytes");
-                const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(at));
-                o.w[0] = v[0];
-                o.w[1] = v[1];
+        for (int e = 0; e < W; ++e) o.w[e] = v[e];
+    } else if (!WHOLE && live > 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < live) {
+                if constexpr (BF16) o.w[e / 2] |= (unsigned)reinterpret_cast<const uint16_t *>(at)[e] << (e % 2 * 16);
+                else o.w[e] = reinterpret_cast<const unsigned *>(at)[e];
             }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            if constexpr (BF16) {
-                const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-                const unsigned lo = 2 * e < live ? q[2 * e] : 0, hi = 2 * e + 1 < live ? q[2 * e + 1] : 0;
-                o.w[e] = lo | hi << 16;
-            } else {
-                o.w[e] = e < live ? static_cast<const unsigned *>(p)[i + e] : 0;
-            }
-        }
     }
 }
 template <bool BF16, int V>
@@ -89,38 +83,34 @@ __device__ __forceinline__ void unpack(const Packed<BF16, V> &o, float (&x)[V]) 
 }
 // Past the caches: forwards where the tensors of the call do not fit them (ASK, past), with gradients always (b4 L4096 of 4096
 // channels 222 us by kernel trace, with the question 227)
-template <bool BF16, int V, bool VEC, bool ASK>
+template <bool BF16, int V, bool WHOLE, bool ASK>
 __device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V], bool past) {
     constexpr int W = Packed<BF16, V>::W;
-    if constexpr (VEC) {
-        unsigned w[W];
+    char *at = static_cast<char *>(p) + i * (BF16 ? 2 : 4);
+    if (WHOLE ? live > 0 : live == V) {
+        typedef typename Words<BF16, W, WHOLE>::any vec;
+        vec v;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-            if constexpr (BF16) w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x[2 * e], x[2 * e + 1]}), bf16x2));
-            else w[e] = __float_as_uint(x[e]);
+            if constexpr (BF16) v[e] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x[2 * e], x[2 * e + 1]}), bf16x2));
+            else v[e] = __float_as_uint(x[e]);
         }
-        if (live > 0) {
-            typedef unsigned vec __attribute__((ext_vector_type(W)));
-            vec v;
-#pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = w[e];
-            vec *to = reinterpret_cast<vec *>(static_cast<char *>(p) + i * (BF16 ? 2 : 4));
-            if constexpr (!ASK) {
-                __builtin_nontemporal_store(v, to);
-            } else if (past) {
-                asm volatile("");  // (two equal stores but for their hint would become one)
-                __builtin_nontemporal_store(v, to);
-                asm volatile("");
-            } else {
-                *to = v;
-            }
+        vec *to = reinterpret_cast<vec *>(at);
+        if constexpr (!ASK) {
+            __builtin_nontemporal_store(v, to);
+        } else if (past) {
+            asm volatile("");  // (two equal stores but for their hint would become one)
+            __builtin_nontemporal_store(v, to);
+            asm volatile("");
+        } else {
+            *to = v;
         }
-    } else {
+    } else if (!WHOLE && live > 0) {
 #pragma unroll
         for (int e = 0; e < V; ++e)
             if (e < live) {
-                if constexpr (BF16) static_cast<__bf16 *>(p)[i + e] = (__bf16)x[e];
-                else static_cast<float *>(p)[i + e] = x[e];
+                if constexpr (BF16) reinterpret_cast<__bf16 *>(at)[e] = (__bf16)x[e];
+                else reinterpret_cast<float *>(at)[e] = x[e];
             }
     }
 }
@@ -143,8 +133,29 @@ __device__ __forceinline__ void gate(float z, int act, float &v, float &slope) {
     }
 }
 
+// `live` of V channels of a weight from c on, a multiple of V (none given: 1)
+template <int V>
+__device__ __forceinline__ void read_weight(const float *p, int c, int live, float (&w)[V]) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = 1.f;
+    if (!p) return;
+    if (live == V) {
+#pragma unroll
+        for (int f = 0; f < V; f += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(p + c + f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[f + e] = v[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < live) w[e] = p[c + e];
+    }
+}
+
 // Where a thread is: LANES lanes a row, CH pieces of LANES * V channels
-template <int LANES, int CH, int V, bool VEC>
+template <int LANES, int CH, int V>
 struct Lanes {
     static constexpr int kThreads = LANES < 256 ? 256 : LANES, kRows = kThreads / LANES;
     int r;              // its row among those of a pass
@@ -158,12 +169,7 @@ struct Lanes {
             live[k] = left <= 0 ? 0 : (left < V ? left : V);
         }
     }
-    __device__ __forceinline__ void weights(const float *p, float (&w)[CH][V]) const {
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) w[k][e] = p && e < live[k] ? p[c[k] + e] : 1.f;
-    }
+    __device__ __forceinline__ void weights(const float *p, int k, float (&w)[V]) const { read_weight<V>(p, c[k], live[k], w); }
     // N sums over the lanes of a row. `slot` alternates: a slow wave still reads the last one's
     template <int N>
     static __device__ __forceinline__ void sum(float (&s)[N], float (*lds)[kThreads / 64][4], int &slot) {
@@ -187,16 +193,34 @@ struct Lanes {
     }
 };
 
+// One of the three weights: in registers for all rows, or (rows of 1024 lanes with gradients) read for each row again, from
+// the caches
+template <int LANES, int CH, int V, bool KEEP>
+struct Weight {
+    const float *p;
+    float w[KEEP ? CH : 1][V];
+    __device__ __forceinline__ Weight(const Lanes<LANES, CH, V> &at, const float *from) : p(from) {
+        if constexpr (KEEP)
+#pragma unroll
+            for (int k = 0; k < CH; ++k) at.weights(p, k, w[k]);
+    }
+    __device__ __forceinline__ void get(const Lanes<LANES, CH, V> &at, int k, float (&o)[V]) const {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = w[k][e];
+        } else {
+            at.weights(p, k, o);
+        }
+    }
+};
+
 // BF: x, z, y in bf16; RF: the residual stream in bf16
-template <bool BF, bool RF, int V, int LANES, int CH, bool VEC>
-__global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void fwd_kernel(const BlockArgs a) {
-    using At = Lanes<LANES, CH, V, VEC>;
+template <bool BF, bool RF, int V, int LANES, int CH, bool WHOLE>
+__global__ __launch_bounds__((Lanes<LANES, CH, V>::kThreads)) void fwd_kernel(const BlockArgs a) {
+    using At = Lanes<LANES, CH, V>;
     __shared__ float lds[2][At::kThreads / 64][4];
     const At p(a.C);
-    float w[CH][V], wp[CH][V], sc[CH][V];
-    p.weights(a.w, w);
-    p.weights(a.wp, wp);
-    p.weights(a.sc, sc);
+    const Weight<LANES, CH, V, true> Kw(p, a.w), Kp(p, a.wp), Ks(p, a.sc);
     const float inv = 1.f / (float)a.C;
     Packed<BF, V> x[CH], z[CH];
     Packed<RF, V> r[CH];
@@ -204,9 +228,9 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void fwd_kern
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int live = row < a.n ? p.live[k] : 0;
-            load<BF, V, VEC>(a.x, row * a.C + p.c[k], live, x[k]);
-            if (a.z) load<BF, V, VEC>(a.z, row * a.C + p.c[k], live, z[k]);
-            if (a.r) load<RF, V, VEC>(a.r, row * a.C + p.c[k], live, r[k]);
+            load<BF, V, WHOLE>(a.x, row * a.C + p.c[k], live, x[k]);
+            if (a.z) load<BF, V, WHOLE>(a.z, row * a.C + p.c[k], live, z[k]);
+            if (a.r) load<RF, V, WHOLE>(a.r, row * a.C + p.c[k], live, r[k]);
         }
     };
     const int64_t step = (int64_t)gridDim.x * At::kRows;
@@ -220,14 +244,16 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void fwd_kern
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             unpack<BF, V>(x[k], v[k]);
-            float zs[V], rs[V];
+            float zs[V], rs[V], w[V], sc[V];
+            Kw.get(p, k, w);
+            Ks.get(p, k, sc);
             unpack<BF, V>(z[k], zs);
             unpack<RF, V>(r[k], rs);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 R[k][e] = a.r ? a.alpha * rs[e] : 0.f;
                 s[0] = __builtin_fmaf(v[k][e], v[k][e], s[0]);
-                float on = sc[k][e] * w[k][e], slope;
+                float on = sc[e] * w[e], slope;
                 if (a.z) {
                     float act;
                     gate<BF>(zs[e], a.act, act, slope);
@@ -252,29 +278,31 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void fwd_kern
             }
         const bool here = row < a.n;
 #pragma unroll
-        for (int k = 0; k < CH; ++k) store<RF, V, VEC, true>(a.R, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
+        for (int k = 0; k < CH; ++k) store<RF, V, WHOLE, true>(a.R, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
         if (a.pre) {
             At::sum(s, lds, slot);
             const float rR = 1.f / sqrtf(s[0] * inv + a.eps);
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
+                float wp[V];
+                Kp.get(p, k, wp);
 #pragma unroll
-                for (int e = 0; e < V; ++e) R[k][e] *= rR * wp[k][e];
-                store<BF, V, VEC, true>(a.y, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
+                for (int e = 0; e < V; ++e) R[k][e] *= rR * wp[e];
+                store<BF, V, WHOLE, true>(a.y, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
             }
         }
     }
 }
 
-template <bool BF, bool RF, int V, int LANES, int CH, bool VEC>
-__global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kernel(const BlockArgs a) {
-    using At = Lanes<LANES, CH, V, VEC>;
+template <bool BF, bool RF, int V, int LANES, int CH, bool WHOLE>
+__global__ __launch_bounds__((Lanes<LANES, CH, V>::kThreads)) void bwd_kernel(const BlockArgs a) {
+    using At = Lanes<LANES, CH, V>;
     __shared__ float lds[2][At::kThreads / 64][4];
     const At p(a.C);
-    float w[CH][V], wp[CH][V], sc[CH][V], dw[CH][V], dwp[CH][V], dsc[CH][V];
-    p.weights(a.w, w);
-    p.weights(a.wp, wp);
-    p.weights(a.sc, sc);
+    float dw[CH][V], dwp[CH][V], dsc[CH][V];
+    // (weights in registers and loads ahead where those allow it)
+    constexpr bool AHEAD = LANES <= 512;
+    const Weight<LANES, CH, V, AHEAD> Kw(p, a.w), Kp(p, a.wp), Ks(p, a.sc);
 #pragma unroll
     for (int k = 0; k < CH; ++k)
 #pragma unroll
@@ -287,21 +315,22 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
         for (int k = 0; k < CH; ++k) {
             const int live = row < a.n ? p.live[k] : 0;
             const int64_t at = row * a.C + p.c[k];
-            load<BF, V, VEC>(a.x, at, live, x[k]);
-            if (a.z) load<BF, V, VEC>(a.z, at, live, z[k]);
+            load<BF, V, WHOLE>(a.x, at, live, x[k]);
+            if (a.z) load<BF, V, WHOLE>(a.z, at, live, z[k]);
             if (a.pre) {
-                load<RF, V, VEC>(a.R, at, live, R[k]);
-                load<BF, V, VEC>(a.dy, at, live, y[k]);
+                load<RF, V, WHOLE>(a.R, at, live, R[k]);
+                load<BF, V, WHOLE>(a.dy, at, live, y[k]);
             }
-            if (a.dR) load<RF, V, VEC>(a.dR, at, live, D[k]);
+            if (a.dR) load<RF, V, WHOLE>(a.dR, at, live, D[k]);
         }
     };
     const int64_t step = (int64_t)gridDim.x * At::kRows;
     int slot = 0;
-    fetch((int64_t)blockIdx.x * At::kRows + p.r);
+    if constexpr (AHEAD) fetch((int64_t)blockIdx.x * At::kRows + p.r);
     for (int64_t pass = (int64_t)blockIdx.x * At::kRows; pass < a.n; pass += step) {
         const int64_t row = pass + p.r;
         const bool here = row < a.n;
+        if constexpr (!AHEAD) fetch(row);
         float xs[CH][V], zs[CH][V], d[CH][V], Rs[CH][V], q[CH][V];
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
@@ -311,17 +340,19 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
             unpack<BF, V>(y[k], q[k]);
             unpack<RF, V>(R[k], Rs[k]);
             unpack<RF, V>(D[k], d[k]);
+            float wp[V];
+            Kp.get(p, k, wp);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 s[0] = __builtin_fmaf(xs[k][e], xs[k][e], s[0]);
                 if (!a.dR) d[k][e] = 0.f;
                 if (a.pre) {
                     s[1] = __builtin_fmaf(Rs[k][e], Rs[k][e], s[1]);
-                    s[2] = __builtin_fmaf(q[k][e] * wp[k][e], Rs[k][e], s[2]);
+                    s[2] = __builtin_fmaf(q[k][e] * wp[e], Rs[k][e], s[2]);
                 }
             }
         }
-        fetch(row + step);
+        if constexpr (AHEAD) fetch(row + step);
         float rx = 1.f;
         if (a.post || a.pre) {
             At::sum(s, lds, slot);
@@ -330,13 +361,16 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
         if (a.pre) {
             const float rR = 1.f / sqrtf(s[1] * inv + a.eps), mean = s[2] * inv * rR * rR;
 #pragma unroll
-            for (int k = 0; k < CH; ++k)
+            for (int k = 0; k < CH; ++k) {
+                float wp[V];
+                Kp.get(p, k, wp);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float n = here ? Rs[k][e] * rR : 0.f;  // (rows behind the last: 1/sqrt(eps) may be infinite)
                     dwp[k][e] = __builtin_fmaf(q[k][e], n, dwp[k][e]);
-                    d[k][e] += rR * (q[k][e] * wp[k][e] - Rs[k][e] * mean);
+                    d[k][e] += rR * (q[k][e] * wp[e] - Rs[k][e] * mean);
                 }
+            }
         }
         float t[1] = {0.f};
 #pragma unroll
@@ -347,27 +381,29 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[e] = a.alpha * d[k][e];
-                store<RF, V, VEC, false>(a.dr, at, live, o, a.past);
+                store<RF, V, WHOLE, false>(a.dr, at, live, o, a.past);
             }
-            float o[V];
+            float o[V], w[V], sc[V];
+            Kw.get(p, k, w);
+            Ks.get(p, k, sc);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 if (!here) d[k][e] = 0.f;
-                const float n = here ? xs[k][e] * rx : 0.f, v = n * w[k][e];
+                const float n = here ? xs[k][e] * rx : 0.f, v = n * w[e];
                 xs[k][e] = n;
                 float act = 1.f, slope = 0.f;
                 if (a.z) {
                     gate<BF>(zs[k][e], a.act, act, slope);
-                    o[e] = d[k][e] * sc[k][e] * v * slope;
+                    o[e] = d[k][e] * sc[e] * v * slope;
                 }
                 const float da = d[k][e] * act;
                 dsc[k][e] = __builtin_fmaf(da, v, dsc[k][e]);
-                d[k][e] = da * sc[k][e];
+                d[k][e] = da * sc[e];
                 dw[k][e] = __builtin_fmaf(d[k][e], n, dw[k][e]);
-                d[k][e] *= w[k][e];
+                d[k][e] *= w[e];
                 t[0] = __builtin_fmaf(d[k][e], n, t[0]);
             }
-            if (a.z) store<BF, V, VEC, false>(a.dz, at, live, o, a.past);
+            if (a.z) store<BF, V, WHOLE, false>(a.dz, at, live, o, a.past);
         }
         if (a.post) {
             At::sum(t, lds, slot);
@@ -378,7 +414,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
             if (a.post)
 #pragma unroll
                 for (int e = 0; e < V; ++e) d[k][e] = rx * (d[k][e] - xs[k][e] * t[0]);
-            store<BF, V, VEC, false>(a.dx, row * a.C + p.c[k], here ? p.live[k] : 0, d[k], a.past);
+            store<BF, V, WHOLE, false>(a.dx, row * a.C + p.c[k], here ? p.live[k] : 0, d[k], a.past);
         }
     }
     if (!a.sums) return;
@@ -415,6 +451,234 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V, VEC>::kThreads)) void bwd_kern
     }
 }
 
+// --------------------------------------------------------------- wide rows ---
+// Rows that the registers do not hold: a workgroup goes over its row two or three times, V channels a thread, from the
+// caches after the first; gradients of weights by columns, from the rows' factors and means, in a launch of their own. Gradients of
+// 4096 bf16 rows of 16384 channels 520 us, bound by its passes (element by element 2140).
+constexpr int kWide = 1024;
+constexpr int kStats = 4;  // a row's rx, rR, mean(q R rR) rR, mean(g x rx)
+
+// N sums over a workgroup, the same in all threads
+template <int N>
+__device__ __forceinline__ void wide_sum(float (&s)[N], float (*lds)[N]) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        s[j] = wave_sum(s[j]);
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6][j] = s[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        s[j] = 0.f;
+        for (int w = 0; w < kWide / 64; ++w) s[j] += lds[w][j];
+    }
+}
+
+template <bool BF, int V>
+__device__ __forceinline__ void wide_read(const void *p, int64_t i, int live, float (&x)[V]) {
+    Packed<BF, V> o;
+    load<BF, V, false>(p, i, live, o);
+    unpack<BF, V>(o, x);
+}
+
+// the stream behind the block, of V channels, before it is rounded
+template <bool BF, bool RF, int V>
+__device__ __forceinline__ void wide_stream(const BlockArgs &a, int64_t i, int c, int live, float rx, float (&R)[V]) {
+    float x[V], z[V], r[V], w[V], sc[V];
+    wide_read<BF, V>(a.x, i, live, x);
+    if (a.z) wide_read<BF, V>(a.z, i, live, z);
+    if (a.r) wide_read<RF, V>(a.r, i, live, r);
+    read_weight<V>(a.w, c, live, w);
+    read_weight<V>(a.sc, c, live, sc);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        float act = 1.f, slope;
+        if (a.z) gate<BF>(z[e], a.act, act, slope);
+        R[e] = __builtin_fmaf(x[e] * (sc[e] * w[e] * act), rx, a.r ? a.alpha * r[e] : 0.f);
+    }
+}
+
+template <bool BF, bool RF, int V>
+__global__ __launch_bounds__(kWide) void wide_fwd_kernel(const BlockArgs a) {
+    __shared__ float lds[kWide / 64][1];
+    const float inv = 1.f / (float)a.C;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        const int64_t base = row * a.C;
+        float rx = 1.f, s[1] = {0.f};
+        if (a.post) {
+            for (int c = threadIdx.x * V; c < a.C; c += kWide * V) {
+                float x[V];
+                wide_read<BF, V>(a.x, base + c, a.C - c < V ? a.C - c : V, x);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[0] = __builtin_fmaf(x[e], x[e], s[0]);
+            }
+            wide_sum(s, lds);
+            rx = 1.f / sqrtf(s[0] * inv + a.eps);
+        }
+        if (a.pre) {
+            s[0] = 0.f;
+            for (int c = threadIdx.x * V; c < a.C; c += kWide * V) {
+                float R[V];
+                const int live = a.C - c < V ? a.C - c : V;
+                wide_stream<BF, RF, V>(a, base + c, c, live, rx, R);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[0] = e < live ? __builtin_fmaf(R[e], R[e], s[0]) : s[0];
+            }
+            wide_sum(s, lds);
+        }
+        const float rR = a.pre ? 1.f / sqrtf(s[0] * inv + a.eps) : 0.f;
+        // (what is overwritten in place is read by the thread itself just before)
+        for (int c = threadIdx.x * V; c < a.C; c += kWide * V) {
+            float R[V], wp[V];
+            const int live = a.C - c < V ? a.C - c : V;
+            wide_stream<BF, RF, V>(a, base + c, c, live, rx, R);
+            store<RF, V, false, true>(a.R, base + c, live, R, a.past);
+            if (a.pre) {
+                read_weight<V>(a.wp, c, live, wp);
+#pragma unroll
+                for (int e = 0; e < V; ++e) R[e] *= rR * wp[e];
+                store<BF, V, false, true>(a.y, base + c, live, R, a.past);
+            }
+        }
+    }
+}
+
+// V channels of a row: the gradient of R, and x's part
+template <bool BF, bool RF, int V>
+struct WideStep {
+    float D[V], n[V], w[V], sc[V], act[V], slope[V], q[V], N[V];
+    __device__ __forceinline__ WideStep(const BlockArgs &a, int64_t i, int c, int live, float rx, float rR, float mean) {
+        float R[V], z[V], wp[V];
+        wide_read<BF, V>(a.x, i, live, n);
+        if (a.dR) wide_read<RF, V>(a.dR, i, live, D);
+        if (a.z) wide_read<BF, V>(a.z, i, live, z);
+        if (a.pre) {
+            wide_read<RF, V>(a.R, i, live, R);
+            wide_read<BF, V>(a.dy, i, live, q);
+            read_weight<V>(a.wp, c, live, wp);
+        }
+        read_weight<V>(a.w, c, live, w);
+        read_weight<V>(a.sc, c, live, sc);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (!a.dR) D[e] = 0.f;
+            if (a.pre) {
+                N[e] = R[e] * rR;
+                D[e] += rR * (q[e] * wp[e] - R[e] * mean);
+            } else {
+                q[e] = N[e] = 0.f;
+            }
+            n[e] *= rx;
+            act[e] = 1.f;
+            slope[e] = 0.f;
+            if (a.z) gate<BF>(z[e], a.act, act[e], slope[e]);
+        }
+    }
+};
+
+template <bool BF, bool RF, int V>
+__global__ __launch_bounds__(kWide) void wide_stats_kernel(const BlockArgs a) {
+    __shared__ float lds[kWide / 64][3], one[kWide / 64][1];
+    const float inv = 1.f / (float)a.C;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        const int64_t base = row * a.C;
+        float s[3] = {0.f, 0.f, 0.f};
+        for (int c = threadIdx.x * V; c < a.C; c += kWide * V) {
+            const int live = a.C - c < V ? a.C - c : V;
+            float x[V], R[V], q[V], wp[V];
+            wide_read<BF, V>(a.x, base + c, live, x);
+            if (a.pre) {
+                wide_read<RF, V>(a.R, base + c, live, R);
+                wide_read<BF, V>(a.dy, base + c, live, q);
+                read_weight<V>(a.wp, c, live, wp);
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                s[0] = __builtin_fmaf(x[e], x[e], s[0]);
+                if (a.pre) {
+                    s[1] = __builtin_fmaf(R[e], R[e], s[1]);
+                    s[2] = __builtin_fmaf(q[e] * wp[e], R[e], s[2]);
+                }
+            }
+        }
+        wide_sum(s, lds);
+        const float rx = a.post ? 1.f / sqrtf(s[0] * inv + a.eps) : 1.f;
+        const float rR = a.pre ? 1.f / sqrtf(s[1] * inv + a.eps) : 0.f, mean = s[2] * inv * rR * rR;
+        float t[1] = {0.f};
+        if (a.post) {
+            for (int c = threadIdx.x * V; c < a.C; c += kWide * V) {
+                const int live = a.C - c < V ? a.C - c : V;
+                const WideStep<BF, RF, V> k(a, base + c, c, live, rx, rR, mean);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (e < live) t[0] = __builtin_fmaf(k.D[e] * k.act[e] * k.sc[e] * k.w[e], k.n[e], t[0]);
+            }
+            wide_sum(t, one);
+        }
+        if (threadIdx.x == 0) {
+            float *to = a.stats + row * kStats;
+            to[0] = rx;
+            to[1] = rR;
+            to[2] = mean;
+            to[3] = t[0] * inv;
+        }
+    }
+}
+
+// (behind the sums below: what dx, dz and dr may overwrite is read by the thread itself just before)
+template <bool BF, bool RF, int V>
+__global__ __launch_bounds__(kWide) void wide_bwd_kernel(const BlockArgs a) {
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        const int64_t base = row * a.C;
+        const float *s = a.stats + row * kStats;
+        const float rx = s[0], rR = s[1], mean = s[2], t = s[3];
+        for (int c = threadIdx.x * V; c < a.C; c += kWide * V) {
+            const int live = a.C - c < V ? a.C - c : V;
+            const WideStep<BF, RF, V> k(a, base + c, c, live, rx, rR, mean);
+            float dx[V], dz[V], dr[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float g = k.D[e] * k.act[e] * k.sc[e] * k.w[e];
+                dr[e] = a.alpha * k.D[e];
+                dz[e] = k.D[e] * k.sc[e] * (k.n[e] * k.w[e]) * k.slope[e];
+                dx[e] = a.post ? rx * (g - k.n[e] * t) : g;
+            }
+            if (a.dr) store<RF, V, false, false>(a.dr, base + c, live, dr, true);
+            if (a.z) store<BF, V, false, false>(a.dz, base + c, live, dz, true);
+            store<BF, V, false, false>(a.dx, base + c, live, dx, true);
+        }
+    }
+}
+
+// partial sums of the weights' gradients: a thread V columns, up to kChainRows rows
+template <bool BF, bool RF, int V>
+__global__ __launch_bounds__(64) void wide_sums_kernel(const BlockArgs a) {
+    const int c = (blockIdx.x * 64 + threadIdx.x) * V, live = a.C - c < V ? a.C - c : V;
+    if (c >= a.C) return;
+    const int64_t first = (int64_t)blockIdx.y * a.rows, end = first + a.rows < a.n ? first + a.rows : a.n;
+    float dw[V] = {}, dwp[V] = {}, dsc[V] = {};
+    for (int64_t row = first; row < end; ++row) {
+        const float *s = a.stats + row * kStats;
+        const WideStep<BF, RF, V> k(a, row * a.C + c, c, live, s[0], s[1], s[2]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float da = k.D[e] * k.act[e];
+            dwp[e] = __builtin_fmaf(k.q[e], k.N[e], dwp[e]);
+            dsc[e] = __builtin_fmaf(da, k.n[e] * k.w[e], dsc[e]);
+            dw[e] = __builtin_fmaf(da * k.sc[e], k.n[e], dw[e]);
+        }
+    }
+    float *part = a.part + (int64_t)blockIdx.y * 3 * a.C + c;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (e < live) {
+            part[e] = dw[e];
+            part[a.C + e] = dwp[e];
+            part[2 * (int64_t)a.C + e] = dsc[e];
+        }
+}
+
 // the weights' gradients: partial sums of all workgroups in a fixed order, 64 columns and kRuns runs a workgroup
 constexpr int kRuns = 16;
 __global__ __launch_bounds__(64 * kRuns) void weight_sums_kernel(const float *part, int64_t n, int C, float *dw, float *dwp,
@@ -439,12 +703,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct BlockPlan {
-    int V, lanes, pieces;
-    bool vec;
-    int64_t fwd, bwd;  // workgroups
+    bool whole, wide[2];         // rows of whole aligned accesses; (forward, backward) rows that the registers do not hold
+    int V, lanes[2], pieces[2];
+    int64_t groups[2], parts;    // workgroups; partial sums of the weights' gradients
+    int64_t rows;                // (wide) rows of such a sum
+    size_t stats, total;         // bytes of workspace
 };
 
-// lanes of a row: one access each where 1024 are enough
 m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
     if (!s) return M3_ERR_INVALID_ARG;
     if (s->rows < 0 || s->channels < 1 || !(s->eps >= 0.f) || !isfinite(s->eps) || !isfinite(s->residual_scale))
@@ -453,47 +718,95 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
     if (s->residual_dtype != M3_F32 && s->residual_dtype != s->io_dtype) return M3_ERR_INVALID_ARG;
     if (s->activation < M3_ACT_NONE || s->activation > M3_ACT_SIGMOID) return M3_ERR_INVALID_ARG;
     if (s->flags & ~(uint32_t)(M3_BLOCK_POST_NORM | M3_BLOCK_PRE_NORM)) return M3_ERR_INVALID_ARG;
+    if (s->rows > (1LL << 40) || s->channels > (1 << 20) || s->rows > (1LL << 44) / s->channels) return M3_ERR_UNSUPPORTED;
     p->V = s->io_dtype == M3_BF16 && s->residual_dtype == M3_BF16 ? 8 : 4;
-    if (s->rows > (1LL << 40) || s->channels > 4096 * p->V) return M3_ERR_UNSUPPORTED;
-    p->vec = s->channels % p->V == 0;
     const int64_t need = ceil_div(s->channels, p->V);
-    p->lanes = 16;
-    while (p->lanes < need && p->lanes < 1024) p->lanes *= 2;
-    p->pieces = need <= p->lanes ? 1 : (need <= 2 * p->lanes ? 2 : 4);
-    const int threads = p->lanes < 256 ? 256 : p->lanes, rows = threads / p->lanes;
-    const int64_t passes = ceil_div(s->rows, rows);
-    // A CU with 1024 threads of them forwards (b8 L4096 of 2048 channels with an fp32 stream 165 us; 2048 172, 4096 168), 512 with
-    // gradients, each with its own sums of the weights (b4 L4096 of 4096 219 us by kernel trace; 1024 238, 2048 254)
-    const int64_t fwd = 256 * 1024 / threads, bwd = 256 * 512 / threads;
-    p->fwd = passes < fwd ? passes : fwd;
-    p->bwd = passes < bwd ? passes : bwd;
-    if (p->bwd * kChainRows < passes) p->bwd = ceil_div(passes, kChainRows);
-    if (p->bwd > kMaxGrid) return M3_ERR_UNSUPPORTED;
+    p->whole = s->channels % p->V == 0;
+    p->parts = 0;
+    for (int b = 0; b < 2; ++b) {
+        p->wide[b] = s->channels > (b ? 8192 : 16384);
+        // Lanes of a row: one access each, of 4 channels two each from 512 lanes on with gradients, whose registers hold three sums a channel
+        // too. 1024 lanes leave those no room for weights and loads ahead (16384 rows of 4096 channels, bf16 with an fp32 stream: 305 us
+        // with 512 lanes, 574 with 1024 and their weights in registers that spill). A whole number of waves from 256 on
+        const int64_t lanes = b && p->V == 4 && need > 512 ? ceil_div(need, 2) : need;
+        p->lanes[b] = 16;
+        while (p->lanes[b] < lanes && p->lanes[b] < 256) p->lanes[b] *= 2;
+        for (int more : {320, 384, 512, 1024})
+            if (p->lanes[b] < lanes) p->lanes[b] = more;
+        p->pieces[b] = need <= p->lanes[b] ? 1 : (need <= 2 * p->lanes[b] ? 2 : 4);
+        const int threads = p->wide[b] ? kWide : (p->lanes[b] < 256 ? 256 : p->lanes[b]);
+        const int64_t passes = p->wide[b] ? s->rows : ceil_div(s->rows, threads / p->lanes[b]);
+        // About 1024 threads of them a CU forwards (b8 L4096 of 2048 channels with an fp32 stream 165 us; 2048 172, 4096 168), 640 with
+        // gradients, each with its own sums of the weights (b4 L4096 of 4096, 512 lanes a row: one a CU 219 us by kernel trace, two 238)
+        const int each = ((b ? 640 : 1024) + threads / 2) / threads;
+        const int64_t best = p->wide[b] ? 512 : 256 * (each < 1 ? 1 : each);
+        p->groups[b] = passes < best ? passes : best;
+        if (b && !p->wide[b] && p->groups[b] * kChainRows < passes) p->groups[b] = ceil_div(passes, kChainRows);
+    }
+    // (wide rows: a wave has 64 V columns of up to kChainRows rows, of fewer where that fills the card)
+    const int64_t across = ceil_div(need, 64), want = ceil_div(4096, across), least = ceil_div(s->rows, kChainRows);
+    p->rows = s->rows ? ceil_div(s->rows, want > least ? (want < s->rows ? want : s->rows) : least) : 1;
+    p->parts = p->wide[1] ? ceil_div(s->rows, p->rows) : p->groups[1];
+    if (p->groups[1] > kMaxGrid || (p->wide[1] && p->parts > 65535)) return M3_ERR_UNSUPPORTED;
+    p->stats = p->wide[1] ? ((size_t)s->rows * kStats * sizeof(float) + 255) & ~(size_t)255 : 0;
+    p->total = p->stats + (size_t)p->parts * 3 * (size_t)s->channels * sizeof(float);
     return M3_OK;
 }
 
-template <bool BF, bool RF, int V, int LANES, int CH, bool VEC>
+template <bool BF, bool RF, int V, int LANES, int CH, bool WHOLE>
 hipError_t launch(const BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t s) {
-    const dim3 t((Lanes<LANES, CH, V, VEC>::kThreads));
-    if (bwd) hipLaunchKernelGGL((bwd_kernel<BF, RF, V, LANES, CH, VEC>), dim3((unsigned)p.bwd), t, 0, s, a);
-    else hipLaunchKernelGGL((fwd_kernel<BF, RF, V, LANES, CH, VEC>), dim3((unsigned)p.fwd), t, 0, s, a);
-    return hipGetLastError();
+    const dim3 t((Lanes<LANES, CH, V>::kThreads)), g((unsigned)p.groups[bwd]);
+    // (what the plan does not ask for: forwards two pieces of fewer than 1024 lanes, with gradients over 8 channels a lane)
+    constexpr bool forward = LANES == 1024 || CH == 1, backward = CH * V <= 8;
+    if constexpr (backward)
+        if (bwd) hipLaunchKernelGGL((bwd_kernel<BF, RF, V, LANES, CH, WHOLE>), g, t, 0, s, a);
+    if constexpr (forward)
+        if (!bwd) hipLaunchKernelGGL((fwd_kernel<BF, RF, V, LANES, CH, WHOLE>), g, t, 0, s, a);
+    return (bwd ? backward : forward) ? hipGetLastError() : hipErrorInvalidValue;
 }
 
-template <bool BF, bool RF, int V, bool VEC>
+template <bool BF, bool RF, int V, bool WHOLE>
 hipError_t launch_lanes(const BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t s) {
-    switch (p.lanes * p.pieces) {
-        case 16: return launch<BF, RF, V, 16, 1, VEC>(a, p, bwd, s);
-        case 32: return launch<BF, RF, V, 32, 1, VEC>(a, p, bwd, s);
-        case 64: return launch<BF, RF, V, 64, 1, VEC>(a, p, bwd, s);
-        case 128: return launch<BF, RF, V, 128, 1, VEC>(a, p, bwd, s);
-        case 256: return launch<BF, RF, V, 256, 1, VEC>(a, p, bwd, s);
-        case 512: return launch<BF, RF, V, 512, 1, VEC>(a, p, bwd, s);
-        case 1024: return launch<BF, RF, V, 1024, 1, VEC>(a, p, bwd, s);
-        case 2048: return launch<BF, RF, V, 1024, 2, VEC>(a, p, bwd, s);
-        case 4096: return launch<BF, RF, V, 1024, 4, VEC>(a, p, bwd, s);
+    switch (p.lanes[bwd] * 8 + p.pieces[bwd]) {
+        case 16 * 8 + 1: return launch<BF, RF, V, 16, 1, WHOLE>(a, p, bwd, s);
+        case 32 * 8 + 1: return launch<BF, RF, V, 32, 1, WHOLE>(a, p, bwd, s);
+        case 64 * 8 + 1: return launch<BF, RF, V, 64, 1, WHOLE>(a, p, bwd, s);
+        case 128 * 8 + 1: return launch<BF, RF, V, 128, 1, WHOLE>(a, p, bwd, s);
+        case 256 * 8 + 1: return launch<BF, RF, V, 256, 1, WHOLE>(a, p, bwd, s);
+        case 320 * 8 + 1: return launch<BF, RF, V, 320, 1, WHOLE>(a, p, bwd, s);
+        case 384 * 8 + 1: return launch<BF, RF, V, 384, 1, WHOLE>(a, p, bwd, s);
+        case 512 * 8 + 1: return launch<BF, RF, V, 512, 1, WHOLE>(a, p, bwd, s);
+        case 1024 * 8 + 1: return launch<BF, RF, V, 1024, 1, WHOLE>(a, p, bwd, s);
+        case 320 * 8 + 2: return launch<BF, RF, V, 320, 2, WHOLE>(a, p, bwd, s);
+        case 384 * 8 + 2: return launch<BF, RF, V, 384, 2, WHOLE>(a, p, bwd, s);
+        case 512 * 8 + 2: return launch<BF, RF, V, 512, 2, WHOLE>(a, p, bwd, s);
+        case 1024 * 8 + 2: return launch<BF, RF, V, 1024, 2, WHOLE>(a, p, bwd, s);
+        case 1024 * 8 + 4: return launch<BF, RF, V, 1024, 4, WHOLE>(a, p, bwd, s);
     }
     return hipErrorInvalidValue;
+}
+
+template <bool BF, bool RF, int V>
+hipError_t launch_rows(const BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t s) {
+    return p.whole ? launch_lanes<BF, RF, V, true>(a, p, bwd, s) : launch_lanes<BF, RF, V, false>(a, p, bwd, s);
+}
+
+template <bool BF, bool RF, int V>
+hipError_t launch_wide(const BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t s) {
+    const dim3 g((unsigned)p.groups[bwd]);
+    if (!bwd) {
+        hipLaunchKernelGGL((wide_fwd_kernel<BF, RF, V>), g, dim3(kWide), 0, s, a);
+        return hipGetLastError();
+    }
+    hipError_t e;
+    hipLaunchKernelGGL((wide_stats_kernel<BF, RF, V>), g, dim3(kWide), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.sums) {
+        hipLaunchKernelGGL((wide_sums_kernel<BF, RF, V>), dim3((unsigned)ceil_div(a.C, 64 * V), (unsigned)p.parts), dim3(64), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((wide_bwd_kernel<BF, RF, V>), g, dim3(kWide), 0, s, a);
+    return hipGetLastError();
 }
 
 hipError_t launch_any(const m3_block_norm_shape &s, BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t hs) {
@@ -501,11 +814,12 @@ hipError_t launch_any(const m3_block_norm_shape &s, BlockArgs &a, const BlockPla
     // x, y and the gate, with gradients theirs; the stream before and behind, and its gradients
     const int64_t each = (bf ? 2 : 4) * ((bwd ? 3 : 2) + (a.z ? (bwd ? 2 : 1) : 0)) + (rf ? 2 : 4) * (bwd ? 3 : 2);
     a.past = a.n * a.C > kLastCache / each;
-    if (bf && rf)
-        return p.vec ? launch_lanes<true, true, 8, true>(a, p, bwd, hs) : launch_lanes<true, true, 8, false>(a, p, bwd, hs);
-    if (bf)
-        return p.vec ? launch_lanes<true, false, 4, true>(a, p, bwd, hs) : launch_lanes<true, false, 4, false>(a, p, bwd, hs);
-    return p.vec ? launch_lanes<false, false, 4, true>(a, p, bwd, hs) : launch_lanes<false, false, 4, false>(a, p, bwd, hs);
+    a.rows = (int)p.rows;
+    if (p.wide[bwd])
+        return bf && rf ? launch_wide<true, true, 8>(a, p, bwd, hs)
+                        : (bf ? launch_wide<true, false, 4>(a, p, bwd, hs) : launch_wide<false, false, 4>(a, p, bwd, hs));
+    if (bf && rf) return launch_rows<true, true, 8>(a, p, bwd, hs);
+    return bf ? launch_rows<true, false, 4>(a, p, bwd, hs) : launch_rows<false, false, 4>(a, p, bwd, hs);
 }
 
 BlockArgs block_args(const m3_block_norm_shape &s, const m3_block_norm_io &io) {
@@ -530,7 +844,7 @@ extern "C" {
 
 size_t m3_block_norm_bwd_workspace_bytes(const m3_block_norm_shape *shape) {
     BlockPlan p;
-    return block_plan(shape, &p) == M3_OK ? (size_t)p.bwd * 3 * (size_t)shape->channels * sizeof(float) : 0;
+    return block_plan(shape, &p) == M3_OK ? p.total : 0;
 }
 
 m3_status m3_block_norm_fwd(const m3_block_norm_shape *shape, const m3_block_norm_io *io, void *stream) {
@@ -570,7 +884,7 @@ m3_status m3_block_norm_bwd(const m3_block_norm_shape *shape, const m3_block_nor
                           gr->dx, gr->dz, gr->dresidual, gr->dpost_weight, gr->dpre_weight, gr->dscale, workspace};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;
-    const size_t need = sums ? (size_t)p.bwd * 3 * (size_t)shape->channels * sizeof(float) : 0;
+    const size_t need = sums ? p.total : p.stats;
     if (need && (!workspace || ws_bytes < need)) return M3_ERR_WORKSPACE_TOO_SMALL;
     void *ws = need ? workspace : nullptr;
     // (dx may be x or dy, dz may be z, dresidual may be dresidual_out)
@@ -584,11 +898,12 @@ m3_status m3_block_norm_bwd(const m3_block_norm_shape *shape, const m3_block_nor
     BlockArgs a = block_args(*shape, *io);
     a.dy = dy; a.dR = dR; a.dx = gr->dx; a.dz = gr->dz; a.dr = gr->dresidual;
     a.sums = sums;
-    a.part = static_cast<float *>(workspace);
+    a.stats = static_cast<float *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.stats);
     hipError_t e = shape->rows > 0 ? launch_any(*shape, a, p, true, hs) : hipSuccess;
     if (e == hipSuccess && sums) {
         hipLaunchKernelGGL(weight_sums_kernel, dim3((unsigned)ceil_div(3 * shape->channels, 64)), dim3(64 * kRuns), 0, hs, a.part,
-                           p.bwd, (int)shape->channels, gr->dpost_weight, gr->dpre_weight, gr->dscale);
+                           p.parts, (int)shape->channels, gr->dpost_weight, gr->dpre_weight, gr->dscale);
         e = hipGetLastError();
     }
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;

@@ -6,7 +6,8 @@
 // distance half of the turned channels, in the layout of halves): it forms the item's cosines and sines once and takes
 // head after head of its token with them, q's and then k's. A wave has one token, or several where their heads do not fill it; with few
 // tokens their heads go to several waves. The angle is a product in fp64, in turns, whose whole turns are dropped before it
-// is rounded to fp32: b8 L4096, 64 + 8 heads of 128, bf16 REPLACE us.
+// is rounded to fp32: b8 L4096, 64 + 8 heads of 128, bf16 215 us (5.6 TB/s); two or four heads ahead, and
+// more waves for few tokens, change nothing.
 #include <math.h>
 
 #include "m3_internal.h"

@@ -1047,7 +1047,7 @@ def block_norm_bwd(x, residual_out, dy, dresidual_out=None, *, z=None, activatio
         if z is not None:
             _need("grads['z']", grads.get("z"))
         _on_gpu(dev)
-        need = lib.m3_block_norm_bwd_workspace_bytes(ctypes.byref(shape)) if sums else 0
+        need = lib.m3_block_norm_bwd_workspace_bytes(ctypes.byref(shape)) if sums or C > 8192 else 0
         if need and workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
             ws, wsb = workspace.data_ptr(), need

@@ -126,15 +126,37 @@ IO = [(BF, BF), (BF, FP), (FP, FP)]
 
 @pytest.mark.parametrize("io,res", IO)
 @pytest.mark.parametrize("shape", [(1, 1), (3, 7), (2, 5, 16), (33, 128), (7, 130), (5, 512), (257, 264), (3, 1000), (4, 1001), (3, 2048),
-                                   (2, 4096), (2, 4100), (2, 8192), (1, 9001), (2, 16384)])
+                                   (2, 1280), (2, 1500), (2, 2560), (3, 2600), (2, 4096), (2, 4100), (3, 5000), (2, 8192), (1, 8191), (1, 9001),
+                                   (2, 16384)])
 def test_widths(shape, io, res):
     print("block norm", shape, io, res, flush=True)
     run(draw(sum(shape), shape, io, res))
 
 
-def test_the_widest_rows():
-    run(draw(1, (2, 32768), BF, BF))
-    run(draw(2, (2, 20001), BF, BF))
+@pytest.mark.parametrize("io,res", IO)
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
+def test_rows_that_the_registers_do_not_hold(post, pre, io, res):
+    print("block norm wide", post, pre, io, res, flush=True)
+    for shape in ((2, 32768), (300, 8193), (3, 20001)):
+        run(draw(shape[1], shape, io, res, scale=pre), post=post, pre=pre)
+
+
+def test_wide_rows_in_place():
+    from state_space_sequence_amd import m3
+    d = draw(8, (5, 17000), BF, BF)
+    kw = dict(scale=d["scale"], post_norm=True, post_weight=d["w"], pre_weight=d["wp"], residual_scale=0.5)
+    y, R = m3.block_norm_fwd(d["x"], d["r"], z=d["z"], **kw)
+    ref = m3.block_norm_bwd(d["x"], R, d["dy"], d["dR"], z=d["z"], **kw)
+    plain = m3.block_norm_bwd(d["x"], R, d["dy"], d["dR"], z=d["z"], grads={n: torch.empty_like(ref[n]) for n in ("x", "z")}, **kw)
+    assert all(torch.equal(plain[n], ref[n]) for n in plain)
+    e = {n: t.clone() for n, t in d.items()}
+    m3.block_norm_fwd(e["x"], e["r"], z=e["z"], y=e["x"], residual_out=e["r"], **kw)
+    assert torch.equal(e["x"], y) and torch.equal(e["r"], R)
+    e = {n: t.clone() for n, t in d.items()}
+    g = {n: torch.empty_like(t) for n, t in ref.items()}
+    g.update(x=e["dy"], z=e["z"], residual=e["dR"])
+    m3.block_norm_bwd(e["x"], R, e["dy"], e["dR"], z=e["z"], grads=g, **kw)
+    assert all(torch.equal(g[n], ref[n]) for n in ref)
 
 
 @pytest.mark.parametrize("io,res", IO)
