@@ -56,7 +56,8 @@ typedef struct {
     const float *post_weight; /* [channels] or NULL; NULL without M3_BLOCK_POST_NORM */
     const float *pre_weight;  /* [channels] or NULL; NULL without M3_BLOCK_PRE_NORM */
     const float *scale;       /* [channels] or NULL */
-    void *residual_out;       /* [rows,channels] residual dtype: out of the forward, input of the backward */
+    void *residual_out;       /* [rows,channels] residual dtype: out of the forward (NULL with M3_BLOCK_PRE_NORM: not wanted),
+                                 input of the backward */
     void *y;                  /* out [rows,channels] io: required with M3_BLOCK_PRE_NORM, else NULL (not used by the backward) */
 } m3_block_norm_io;
 

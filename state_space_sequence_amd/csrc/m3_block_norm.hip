@@ -278,7 +278,8 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V>::kThreads)) void fwd_kernel(co
             }
         const bool here = row < a.n;
 #pragma unroll
-        for (int k = 0; k < CH; ++k) store<RF, V, WHOLE, true>(a.R, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
+        for (int k = 0; k < CH; ++k)
+            if (a.R) store<RF, V, WHOLE, true>(a.R, row * a.C + p.c[k], here ? p.live[k] : 0, R[k], a.past);
         if (a.pre) {
             At::sum(s, lds, slot);
             const float rR = 1.f / sqrtf(s[0] * inv + a.eps);
@@ -533,7 +534,7 @@ __global__ __launch_bounds__(kWide) void wide_fwd_kernel(const BlockArgs a) {
             float R[V], wp[V];
             const int live = a.C - c < V ? a.C - c : V;
             wide_stream<BF, RF, V>(a, base + c, c, live, rx, R);
-            store<RF, V, false, true>(a.R, base + c, live, R, a.past);
+            if (a.R) store<RF, V, false, true>(a.R, base + c, live, R, a.past);
             if (a.pre) {
                 read_weight<V>(a.wp, c, live, wp);
 #pragma unroll
@@ -854,7 +855,7 @@ m3_status m3_block_norm_fwd(const m3_block_norm_shape *shape, const m3_block_nor
     if (!io) return M3_ERR_INVALID_ARG;
     const bool pre = shape->flags & M3_BLOCK_PRE_NORM;
     if (stray(*shape, io->post_weight, io->pre_weight) || (!pre && io->y)) return M3_ERR_INVALID_ARG;
-    if (shape->rows > 0 && (!io->x || !io->residual_out || (pre && !io->y))) return M3_ERR_INVALID_ARG;
+    if (shape->rows > 0 && (!io->x || (pre ? !io->y : !io->residual_out))) return M3_ERR_INVALID_ARG;
     const void *ptrs[] = {io->x, io->z, io->residual, io->post_weight, io->pre_weight, io->scale, io->residual_out, io->y};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;

@@ -966,13 +966,14 @@ def _block_norm_call(x, z, activation, scale, post_norm, post_weight, pre_norm, 
 
 def block_norm_fwd(x, residual=None, *, z=None, activation="silu", scale=None, post_norm=False, post_weight=None,
                    pre_norm=True, pre_weight=None, residual_scale=1.0, eps=1e-5, residual_dtype=None, y=None,
-                   residual_out=None, stream=None):
+                   residual_out=None, want_residual=True, stream=None):
     """What stands between two blocks, in one pass (m3_block_norm_fwd): with x [..., C] a block's output and
     residual the stream around it (fp32 or of the dtype of x; None: 0),
     v = rms_norm(x) * post_weight (post_norm; else v = x), R = residual_scale * residual + scale * act(z) * v,
     y = rms_norm(R) * pre_weight (pre_norm). z: a gate like x or None, activation 'none', 'silu' or
     'sigmoid'; scale, post_weight, pre_weight [C] fp32 or None (ones). residual_dtype: of R without a residual
-    (else as residual; x's by default). Returns (y or None, R)."""
+    (else as residual; x's by default). want_residual=False: R is not written (a norm alone). Returns (y or None,
+    R or None)."""
     given = residual if residual is not None else residual_out
     if residual_dtype is None:
         residual_dtype = given.dtype if isinstance(given, torch.Tensor) else getattr(x, "dtype", None)
@@ -989,7 +990,7 @@ def block_norm_fwd(x, residual=None, *, z=None, activation="silu", scale=None, p
             raise ValueError("y: only with pre_norm")
     _on_gpu(dev)
     with _owned_by(stream):
-        if residual_out is None:
+        if residual_out is None and (want_residual or not pre_norm):
             residual_out = torch.empty_like(x, dtype=residual_dtype) if residual is None else torch.empty_like(residual)
             io.residual_out = residual_out.data_ptr()
         if y is None and pre_norm:

@@ -67,7 +67,7 @@ def test_required_aligned_and_workspace(m3):
     for name, _ in m3.BlockNormIO._fields_:
         io, = filled(m3.BlockNormIO())
         setattr(io, name, None)
-        if name in ("x", "residual_out", "y"):
+        if name in ("x", "y"):
             assert fwd(m3, s, io) == -1, name
         setattr(io, name, 0x900004)
         assert fwd(m3, s, io) == -3, name
@@ -78,6 +78,9 @@ def test_required_aligned_and_workspace(m3):
             assert bwd(m3, s, io, g) == -1, name
         setattr(g, name, 0x900004)
         assert bwd(m3, s, io, g) == -3, name
+    io, = filled(m3.BlockNormIO())
+    io.y = io.pre_weight = io.residual_out = None  # nothing to write
+    assert fwd(m3, shape(m3, flags=1), io) == -1
     io, g = filled(m3.BlockNormIO(), m3.BlockNormGrads())
     io.z = None  # a gate and its gradient go together
     assert bwd(m3, s, io, g) == -1

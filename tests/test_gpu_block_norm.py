@@ -141,6 +141,19 @@ def test_rows_that_the_registers_do_not_hold(post, pre, io, res):
         run(draw(shape[1], shape, io, res, scale=pre), post=post, pre=pre)
 
 
+def test_a_norm_alone():
+    """Without the stream behind: the same y."""
+    from state_space_sequence_amd import m3
+    for shape in ((50, 264), (3, 20001)):
+        d = draw(2, shape, BF, BF)
+        kw = dict(z=d["z"], post_norm=True, pre_weight=d["wp"])
+        y, R = m3.block_norm_fwd(d["x"], d["r"], **kw)
+        y2, none = m3.block_norm_fwd(d["x"], d["r"], want_residual=False, **kw)
+        assert none is None and torch.equal(y, y2)
+        y, _ = m3.block_norm_fwd(d["x"], pre_weight=d["wp"], want_residual=False)
+        check("y", y, reference(d["x"], None, wp=d["wp"])["y"])
+
+
 def test_wide_rows_in_place():
     from state_space_sequence_amd import m3
     d = draw(8, (5, 17000), BF, BF)
