@@ -25,8 +25,8 @@
  *     forward writes it where it is given; the backward then need not run the
  *     recurrence over the sequence again first.
  * C: 1 to 2^20; even C load fastest in bf16. b * L <= 2^40, and b times the tiles of 64
- * channels times those of 64 tokens below 2^24 (else M3_ERR_UNSUPPORTED). States, gates and sums are fp32,
- * sums over tokens and rows fp64 beyond 16 terms (joined from fp32 sums of 64); each output is rounded once. 1 - a_t
+ * channels times those of 64 tokens below 2^23 (else M3_ERR_UNSUPPORTED). States, gates and sums are fp32,
+ * sums over tokens and rows fp64 beyond 8 terms, held in fp32 once for every 64 tokens; each output is rounded once. 1 - a_t
  * is formed without cancellation, so slow decays keep their input. Where
  * 1 - a_t^2 is 0 (a log_decay of 0), an input has no effect and no gradient.
  *

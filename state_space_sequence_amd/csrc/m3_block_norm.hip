@@ -4,9 +4,10 @@
 //   dR' = dR + rR (q - R rR mean(q R rR)),  q = dy wp;  dr = alpha dR';  dz = dR' sc v act'(z)
 //   g = dR' sc act(z) w;  dx = rx (g - x rx mean(g x rx));  dwp = sum dy R rR;  dsc = sum dR' act(z) v;  dw = sum dR' sc act(z) x rx
 //
-// Bound by HBM: every tensor is read or written once. The lanes of a row (16 to 1024 of them) hold it in registers, up to
-// 32 values each; its sums go across a wave by DPP and row swaps, across waves by LDS. A lane keeps its channels from row
-// to row, so weights and their gradients stay in registers too, and the next row is loaded while this one is summed.
+// Bound by HBM: every tensor is read or written once. The lanes of a row (16 to 1024 of them) hold it in registers, 4 to
+// 16 values each; its sums go across a wave by DPP and row swaps, across waves by LDS. A lane keeps its channels from row
+// to row, so weights and their gradients stay in registers too, and the next row is loaded while this one is summed. bf16, all parts:
+// b8 L4096 of 2048 channels with an fp32 stream 161 us (5.8 TB/s), gradients of b4 L4096 of 4096 193 us (5.5 TB/s).
 #include <math.h>
 
 #include "m3_block_norm.h"

@@ -19,8 +19,8 @@
 // taken in order from a counter, a workgroup does what it took in that order, and a tile needs nothing from later ones.
 //
 // Bound by HBM and, nearly as much, by vector issue: 34 instructions an element, 5 of them exponentials, reciprocals and roots, 53 ns
-// an element of a wave on a SIMD, so 110 us of the prompt's 206. bf16, with an input gate: prompt b8 L4096 of 4096
-// channels 206 us (5.2 TB/s), long b2 L32768 of 2560 in a chain 300 (4.5 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
+// an element of a wave on a SIMD, so 110 us of the prompt's 211. bf16, with an input gate, times of a call: prompt b8 L4096 of
+// 4096 channels 211 us (5.1 TB/s), long b2 L32768 of 2560 in a chain 292 (4.6 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
 #include <math.h>
 
 #include <type_traits>
