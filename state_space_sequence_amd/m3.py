@@ -1083,10 +1083,16 @@ def _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, scaled)
         raise ValueError("x: no channels, got shape %s" % (tuple(s),))
     _need("decay_gate", decay_gate)
     _need("log_decay", log_decay)
-    ptrs = RecIO(_arg("x", x, s, io, dev), _arg("decay_gate", decay_gate, s, io, dev),
-                 _arg("input_gate", input_gate, s, io, dev), _arg("log_decay", log_decay, (C,), f32, dev),
-                 _arg("h0", h0, (b, C), f32, dev), _arg("lengths", lengths, (b,), torch.int32, dev), None, None,
-                 _arg("states", states, (b, -(-L // M3_REC_KEEP), C), f32, dev))
+    ptrs = RecIO(_arg("x", x, s, io, dev), _arg("decay_gate", decay_gate, s, io, dev), None,
+                 _arg("log_decay", log_decay, (C,), f32, dev))
+    if input_gate is not None:
+        ptrs.input_gate = _arg("input_gate", input_gate, s, io, dev)
+    if h0 is not None:
+        ptrs.h0 = _arg("h0", h0, (b, C), f32, dev)
+    if lengths is not None:
+        ptrs.lengths = _arg("lengths", lengths, (b,), torch.int32, dev)
+    if states is not None:
+        ptrs.states = _arg("states", states, (b, -(-L // M3_REC_KEEP), C), f32, dev)
     return RecShape(b, L, C, iot, 0 if scaled else M3_REC_UNSCALED), ptrs
 
 
@@ -1102,16 +1108,19 @@ def recurrence_fwd(x, decay_gate, log_decay, *, input_gate=None, h0=None, length
     shape, ptrs = _rec_call(x, decay_gate, log_decay, input_gate, h0, lengths, states, scaled)
     b, L, C = x.shape
     f32, dev = torch.float32, x.get_device()
-    ptrs.y, ptrs.h_final = _arg("y", y, x.shape, x.dtype, dev), _arg("h_final", h_final, (b, C), f32, dev)
+    if y is not None:
+        ptrs.y = _arg("y", y, x.shape, x.dtype, dev)
+    if h_final is not None:
+        ptrs.h_final = _arg("h_final", h_final, (b, C), f32, dev)
     ws, wsb = _workspace(workspace, dev)
     _on_gpu(dev)
     need = lib.m3_recurrence_workspace_bytes(ctypes.byref(shape))
     with _owned_by(stream):
         if y is None:
-            y = x.new_empty(x.shape)
+            y = torch.empty_like(x)
             ptrs.y = y.data_ptr()
         if h_final is None and want_state:
-            h_final = torch.empty((b, C), dtype=f32, device=x.device)
+            h_final = x.new_empty((b, C), dtype=f32)
             ptrs.h_final = h_final.data_ptr()
         if states is None and want_states:
             states = torch.empty((b, -(-L // M3_REC_KEEP), C), dtype=f32, device=x.device)
@@ -1140,7 +1149,7 @@ def recurrence_bwd(x, decay_gate, log_decay, dy, *, input_gate=None, h0=None, le
     required = ("x", "decay_gate") if input_gate is None else ("x", "decay_gate", "input_gate")
     with _owned_by(stream):
         if grads is None:
-            grads = {name: torch.empty(s, dtype=io, device=x.device) for name in required}
+            grads = {name: torch.empty_like(x) for name in required}
             if want_dlog_decay:
                 grads["log_decay"] = torch.empty((C,), dtype=f32, device=x.device)
             if want_dh0:
