@@ -16,7 +16,8 @@
  * t is formed in fp64 and reduced there, so far positions keep their angle: cosine and sine are
  * off by at most 2^-22. Each output is rounded once.
  * D: 1 to 1024; rotary even, 0 to D; H, G 1 to 4096, b * L * (H + G) * D <= 2^40 (else
- * M3_ERR_UNSUPPORTED). Multiples of 16 (rotary) and 8 (D) in bf16, 8 and 4 in fp32, load fastest.
+ * M3_ERR_UNSUPPORTED). D in multiples of 8 in bf16, of 4 in fp32, load
+ * fastest, with halves rotary in multiples of 16 or 8 too; half of each in bf16 comes next.
  *
  * Conventions as in m3.h: dense row-major tensors, 16-byte aligned pointers, the
  * caller owns every buffer, the stream is a hipStream_t of the current device

@@ -17,7 +17,6 @@ namespace m3i {
 namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256, kAhead = 3;  // heads whose loads are in flight
@@ -40,17 +39,17 @@ struct RotArgs {
 template <bool BF16, int V>
 struct Vec {
     static constexpr int W = V == 1 ? 1 : (BF16 ? V / 2 : V);
+    typedef unsigned words __attribute__((ext_vector_type(W)));  // (aligned to its size)
     unsigned w[W];
     __device__ __forceinline__ void load(const void *p, int64_t i) {
         if constexpr (V == 1) {
             if constexpr (BF16) w[0] = static_cast<const uint16_t *>(p)[i];
             else w[0] = static_cast<const unsigned *>(p)[i];
         } else {
-            static_assert(W == 4, "16 bytes");
-            const u32x4 v = __builtin_nontemporal_load(
-                reinterpret_cast<const u32x4 *>(static_cast<const char *>(p) + i * (BF16 ? 2 : 4)));
+            const words v = __builtin_nontemporal_load(
+                reinterpret_cast<const words *>(static_cast<const char *>(p) + i * (BF16 ? 2 : 4)));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = v[e];
+            for (int e = 0; e < W; ++e) w[e] = v[e];
         }
     }
     __device__ __forceinline__ void store(void *p, int64_t i, bool past) const {
@@ -58,8 +57,10 @@ struct Vec {
             if constexpr (BF16) static_cast<uint16_t *>(p)[i] = (uint16_t)w[0];
             else static_cast<unsigned *>(p)[i] = w[0];
         } else {
-            u32x4 v = {w[0], w[1], w[2], w[3]};
-            u32x4 *to = reinterpret_cast<u32x4 *>(static_cast<char *>(p) + i * (BF16 ? 2 : 4));
+            words v;
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = w[e];
+            words *to = reinterpret_cast<words *>(static_cast<char *>(p) + i * (BF16 ? 2 : 4));
             if (past) {
                 asm volatile("");  // (two equal stores but for their hint would become one)
                 __builtin_nontemporal_store(v, to);
@@ -241,11 +242,13 @@ extern "C" m3_status m3_rotary(const m3_rotary_shape *shape, const m3_rotary_io 
     a.q = io->q; a.k = io->k; a.qo = io->q_out; a.ko = io->k_out; a.freqs = io->freqs; a.positions = io->positions;
     a.offsets = io->offsets; a.L = s.seqlen; a.H = (int)s.nheads; a.G = io->k ? (int)s.ngroups : 0; a.D = (int)s.headdim;
     a.half = (int)(s.rotary / 2); a.scale = s.scale; a.back = s.flags & M3_ROTARY_BACKWARD;
-    // 16 bytes at a time where every piece is aligned to them
-    const int wide = bf16 ? 8 : 4;
-    const bool vec = s.headdim % wide == 0 && (paired || a.half % wide == 0);
-    const int V = vec ? wide : 1, rest = a.D - 2 * a.half;
-    if (paired && vec) a.items = in_place ? (int)ceil_div(2 * a.half, V) : a.D / V;
+    // 16 bytes at a time, in bf16 8 (halves, D 96 with 40 turned, b4 L4096, 16 + 4 heads: 42 us, one value at a time
+    // 67; D 72: 26 and 38), where every piece is aligned to them; pieces of two values are slower than single ones
+    // (D 100, halves: bf16 56 us and 41, fp32 57 and 50)
+    int V = bf16 ? 8 : 4;
+    while (V > 1 && (s.headdim % V || (!paired && a.half % V))) V = V > 4 ? 4 : 1;
+    const int rest = a.D - 2 * a.half;
+    if (paired && V > 1) a.items = in_place ? (int)ceil_div(2 * a.half, V) : a.D / V;
     else a.items = a.half / V + (in_place ? 0 : rest / V);
     if (a.items == 0) return M3_OK;
     const int all = a.H + a.G;
@@ -259,7 +262,9 @@ extern "C" m3_status m3_rotary(const m3_rotary_shape *shape, const m3_rotary_io 
     a.units = groups * a.split;
     a.past = a.tokens * all * a.D > kLastCache / (bf16 ? 4 : 8);
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const hipError_t e = bf16 ? (vec ? launch<true, 8>(a, paired, hs) : launch<true, 1>(a, paired, hs))
-                              : (vec ? launch<false, 4>(a, paired, hs) : launch<false, 1>(a, paired, hs));
+    const hipError_t e = bf16 ? (V == 8   ? launch<true, 8>(a, paired, hs)
+                                 : V == 4 ? launch<true, 4>(a, paired, hs)
+                                          : launch<true, 1>(a, paired, hs))
+                              : (V == 4 ? launch<false, 4>(a, paired, hs) : launch<false, 1>(a, paired, hs));
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
 }

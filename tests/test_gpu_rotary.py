@@ -49,7 +49,8 @@ def draw(seed, b, L, H, G, D, io):
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("H,G,D,n", [(1, 1, 2, 2), (3, 1, 7, 4), (8, 2, 64, 64), (64, 8, 128, 128), (5, 5, 80, 40), (4, 2, 96, 32), (2, 1, 256, 256),
-                                     (3, 2, 24, 6), (7, 1, 100, 100), (2, 2, 1024, 1024), (1, 1, 1000, 400), (4, 4, 16, 0), (1, 1, 1, 0)])
+                                     (3, 2, 24, 6), (7, 1, 100, 100), (2, 2, 1024, 1024), (1, 1, 1000, 400), (4, 4, 16, 0), (1, 1, 1, 0), (2, 3, 96, 50),
+                                     (3, 1, 72, 24), (2, 2, 100, 92), (5, 1, 36, 20)])
 @pytest.mark.parametrize("where", ["none", "each", "offsets"])
 def test_layouts_and_positions(where, H, G, D, n, layout, io):
     from state_space_sequence_amd import m3
