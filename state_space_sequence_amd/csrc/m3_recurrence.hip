@@ -20,7 +20,7 @@
 //
 // Bound by HBM and, nearly as much, by vector issue: 34 instructions an element, 5 of them exponentials, reciprocals and roots, 53 ns
 // an element of a wave on a SIMD, so 110 us of the prompt's 211. bf16, with an input gate, times of a call: prompt b8 L4096 of
-// 4096 channels 211 us (5.1 TB/s), long b2 L32768 of 2560 in a chain 292 (4.6 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
+// 4096 channels 211 us (5.1 TB/s), long b2 L32768 of 2560 in a chain 288 (4.7 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
 #include <math.h>
 
 #include <type_traits>
@@ -609,6 +609,11 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(const RecArgs a) {
                 fl[t][v] = left - fl[t][v];
                 h[v] = left + sb[t][v];
             }
+        if (!whole)  // (a state that is infinite or NaN has no part in what is behind the length)
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int v = 0; v < V; ++v) fl[t][v] = p.wave * T + t < n ? fl[t][v] : 0.f;
         if constexpr (CHAIN) {
             later = __builtin_amdgcn_readfirstlane(taken[2 + (turn & 1)]);
 #pragma unroll

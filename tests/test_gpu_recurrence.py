@@ -201,6 +201,37 @@ def test_a_nan_stays_in_its_row_and_channel():
 
 
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("L", [100, 1500])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_state_has_no_part_behind_the_lengths(bad, L, kept, io):
+    """An empty row whose start state is not finite (the place of no sequence in a batch) adds nothing to d log_decay, and
+    gradients behind a length are 0 also where the last token's state is not finite."""
+    from state_space_sequence_amd import m3
+
+    d = draw(12, 3, L, 70, io)
+    lengths = torch.tensor([0, L // 2 + 3, L], dtype=torch.int32, device="cuda")
+    names = ["x", "decay_gate", "input_gate"]
+
+    def grads(h0, x):
+        a = dict(input_gate=d["i"], h0=h0, lengths=lengths)
+        st = m3.recurrence_fwd(x, d["r"], d["ld"], want_states=True, **a)[2] if kept else None
+        return m3.recurrence_bwd(x, d["r"], d["ld"], d["dy"], dh_final=d["dh"], states=st, **a)
+
+    h0 = d["h0"].clone()
+    h0[0] = bad
+    want, got = grads(d["h0"], d["x"]), grads(h0, d["x"])
+    for k in want:
+        assert torch.equal(got[k], want[k]) and got[k].isfinite().all(), k
+    assert all((got[k][0] == 0).all() for k in names)
+    x = d["x"].clone()
+    x[1, L // 2 + 2] = bad
+    got = grads(d["h0"], x)
+    assert all((got[k][1, L // 2 + 3:] == 0).all() for k in names)
+    assert all(torch.equal(got[k][2], want[k][2]) for k in names)
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("gate,scaled", [(True, True), (False, True), (True, False)])
 @pytest.mark.parametrize("b,C", [(1, 1), (3, 7), (5, 256), (129, 130)])
 def test_step(b, C, gate, scaled, io):
