@@ -962,17 +962,20 @@ m3_status m3_recurrence_bwd(const m3_rec_shape *shape, const m3_rec_io *io, cons
 }
 
 m3_status m3_recurrence_step(const m3_rec_shape *shape, const m3_rec_step_io *io, void *stream) {
-    const m3_status st = rec_check(shape);
+    if (!shape) return M3_ERR_INVALID_ARG;
+    m3_rec_shape s = *shape;
+    s.seqlen = 1;  // (not used)
+    const m3_status st = rec_check(&s);
     if (st != M3_OK) return st;
     if (!io) return M3_ERR_INVALID_ARG;
-    if (shape->batch > 0 && (!io->x || !io->decay_gate || !io->log_decay || !io->h || !io->y)) return M3_ERR_INVALID_ARG;
+    if (s.batch > 0 && (!io->x || !io->decay_gate || !io->log_decay || !io->h || !io->y)) return M3_ERR_INVALID_ARG;
     const void *ptrs[] = {io->x, io->decay_gate, io->input_gate, io->log_decay, io->h, io->y};
     for (const void *q : ptrs)
         if (!al16(q)) return M3_ERR_MISALIGNED;
     if (clash({io->h, io->y}, {io->x, io->decay_gate, io->input_gate, io->log_decay})) return M3_ERR_INVALID_ARG;
-    if (shape->batch == 0) return M3_OK;
+    if (s.batch == 0) return M3_OK;
     const hipError_t e =
-        M3_REC_PICK(launch_step, shape, io->input_gate != nullptr, *shape, *io, reinterpret_cast<hipStream_t>(stream));
+        M3_REC_PICK(launch_step, &s, io->input_gate != nullptr, s, *io, reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
 
