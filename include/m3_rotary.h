@@ -13,8 +13,8 @@
  *     them; `scale` is its factor on the magnitude)
  *   positions [b,L] int32: each token's; or offsets [b] int32: token t of row i is at
  *     offsets[i] + t; or neither: at t. (A single token a row: L = 1.)
- * t is formed in fp64 and reduced there, so far positions keep their angle: cosine and sine are
- * off by at most 2^-22. Each output is rounded once.
+ * t is formed and reduced in two fp64 numbers, so far positions keep their angle: cosine and sine are
+ * off by at most 2^-22 where |t| <= 2^64. Each output is rounded once.
  * D: 1 to 1024; rotary even, 0 to D; H, G 1 to 4096, b * L * (H + G) * D <= 2^40 (else
  * M3_ERR_UNSUPPORTED). D in multiples of 8 in bf16, of 4 in fp32, load
  * fastest, with halves rotary in multiples of 16 or 8 too; half of each in bf16 comes next.

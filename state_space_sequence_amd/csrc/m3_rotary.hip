@@ -5,7 +5,7 @@
 // Bound by HBM: q and k read and written once. A lane has an item of a head, 16 bytes of it (two pieces of 16 bytes, their
 // distance half of the turned channels, in the layout of halves): it forms the item's cosines and sines once and takes
 // head after head of its token with them, q's and then k's. A wave has one token, or several where their heads do not fill it; with few
-// tokens their heads go to several waves. The angle is a product in fp64, in turns, whose whole turns are dropped before it
+// tokens their heads go to several waves. The angle is formed in turns, whose whole ones are dropped before it
 // is rounded to fp32: b8 L4096, 64 + 8 heads of 128, bf16 215 us (5.6 TB/s); two or four heads ahead, and
 // more waves for few tokens, change nothing.
 #include <math.h>
@@ -89,13 +89,21 @@ struct Vec {
     }
 };
 
-// cosine and sine of pos * freq, times scale
+// Cosine and sine of pos * freq, times scale. The product and its turns are kept to twice the bits of fp64 until whole turns
+// are dropped (1/(2 pi) in two parts, what each product leaves behind by an FMA): of 2^31 positions at a frequency of 1 a
+// product of fp64 alone is off by 2^-21 rad. What the fraction loses as an fp32 number goes in behind.
 __device__ __forceinline__ void turn(const RotArgs &a, double pos, float freq, float &c, float &s) {
-    const double t = pos * ((double)freq * 0.15915494309189535);
-    const float f = (float)(t - __builtin_rint(t));
-    sincospif(2.f * f, &s, &c);
-    c *= a.scale;
-    s *= a.back ? -a.scale : a.scale;
+#pragma clang fp contract(off)  // (t - rint(t) of the rounded t)
+    constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
+    const double p = pos * (double)freq, left = __builtin_fma(pos, (double)freq, -p), t = p * kHigh;
+    double f = __builtin_fma(p, kHigh, -t) + __builtin_fma(p, kLow, left * kHigh);
+    f += t - __builtin_rint(t);
+    f -= __builtin_rint(f);
+    const float near = (float)f, d = (float)((f - (double)near) * 6.283185307179586);
+    float c0, s0;
+    sincospif(2.f * near, &s0, &c0);
+    c = __builtin_fmaf(-s0, d, c0) * a.scale;
+    s = __builtin_fmaf(c0, d, s0) * (a.back ? -a.scale : a.scale);
 }
 
 // PAIRED: pairs are neighbours, an item is V channels (V = 1: two); else an item is V channels and those `half` further.
