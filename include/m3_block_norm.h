@@ -11,8 +11,8 @@
  * R is rounded. m3_block_norm_bwd gives the gradients, from x, z and the stored R.
  *   x, z, y: io dtype. r, R: residual dtype, fp32 or that of x. Weights and scale
  *     [channels] fp32 or NULL (ones). Sums are fp32 within a row; those over rows
- *     fp32 for at most 256 rows, one after another, and fp64 beyond; each output is
- *     rounded once. A row of zeros with an eps of 0 gives NaN.
+ *     fp32 for at most 256 rows, one after another, and fp64 beyond, held in fp32 once for
+ *     every workgroup; each output is rounded once. A row of zeros with an eps of 0 gives NaN.
  * channels: 1 to 2^20; rows * channels <= 2^44 (else M3_ERR_UNSUPPORTED). Rows of over 16384 channels (8192 with
  * gradients) are read two or three times.
  *

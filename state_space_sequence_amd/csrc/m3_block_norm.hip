@@ -420,7 +420,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V>::kThreads)) void bwd_kernel(co
         }
     }
     if (!a.sums) return;
-    // the sums of a workgroup's lanes of rows, in a fixed order
+    // the sums of a workgroup's lanes of rows, in a fixed order, and in fp64: they are of up to kRows * kChainRows rows
     float *part = a.part + (int64_t)blockIdx.x * 3 * a.C;
     if constexpr (At::kRows > 1) {
         __shared__ float join[3][At::kThreads];
@@ -435,9 +435,9 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V>::kThreads)) void bwd_kernel(co
                 __syncthreads();
                 for (int i = threadIdx.x; i < 3 * LANES; i += At::kThreads) {
                     const int j = i / LANES, l = i % LANES, c = (k * LANES + l) * V + e;
-                    float t = 0.f;
+                    double t = 0.;
                     for (int r = 0; r < At::kRows; ++r) t += join[j][r * LANES + l];
-                    if (c < a.C) part[(int64_t)j * a.C + c] = t;
+                    if (c < a.C) part[(int64_t)j * a.C + c] = (float)t;
                 }
             }
     } else {
