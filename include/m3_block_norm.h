@@ -13,8 +13,8 @@
  *     [channels] fp32 or NULL (ones). Sums are fp32 within a row; those over rows
  *     fp32 for at most 256 rows, one after another, and fp64 beyond, held in fp32 once for
  *     every workgroup; each output is rounded once. A row of zeros with an eps of 0 gives NaN.
- * channels: 1 to 2^20; rows * channels <= 2^44 (else M3_ERR_UNSUPPORTED). Rows of over 16384 channels (8192 with
- * gradients) are read two or three times.
+ * channels: 1 to 2^20; rows: up to 2^41 / max(channels, 64), up to 2^23 of over 8192 channels (more may be
+ * M3_ERR_UNSUPPORTED). Rows of over 16384 channels (8192 with gradients) are read two or three times.
  *
  * Conventions as in m3.h: dense row-major tensors, 16-byte aligned pointers, the
  * caller owns every buffer and the workspace (contents need not be initialised
@@ -39,7 +39,7 @@ extern "C" {
 #define M3_BLOCK_PRE_NORM 2
 
 typedef struct {
-    int64_t rows;           /* >= 0, up to 2^40 */
+    int64_t rows;           /* >= 0 */
     int64_t channels;       /* >= 1 */
     int32_t io_dtype;       /* m3_dtype of x, z, y, dy, dx, dz */
     int32_t residual_dtype; /* m3_dtype of r, R and their gradients: M3_F32 or io_dtype */

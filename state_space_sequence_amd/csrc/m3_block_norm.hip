@@ -20,7 +20,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kChainRows = 256;  // rows whose weight gradients a thread adds up in fp32
-constexpr int64_t kMaxGrid = 0x3fffff;  // workgroups of 1024 threads: 2^32 threads
+constexpr int64_t kMaxThreads = 0xffffffff;  // of a launch
 constexpr int64_t kLastCache = 256 << 20;
 
 struct BlockArgs {
@@ -725,6 +725,7 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
     const int64_t need = ceil_div(s->channels, p->V);
     p->whole = s->channels % p->V == 0;
     p->parts = 0;
+    int threads[2];
     for (int b = 0; b < 2; ++b) {
         p->wide[b] = s->channels > (b ? 8192 : 16384);
         // Lanes of a row: one access each, of 4 channels two each from 512 lanes on with gradients, whose registers hold three sums a channel
@@ -736,11 +737,11 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
         for (int more : {320, 384, 512, 1024})
             if (p->lanes[b] < lanes) p->lanes[b] = more;
         p->pieces[b] = need <= p->lanes[b] ? 1 : (need <= 2 * p->lanes[b] ? 2 : 4);
-        const int threads = p->wide[b] ? kWide : (p->lanes[b] < 256 ? 256 : p->lanes[b]);
-        const int64_t passes = p->wide[b] ? s->rows : ceil_div(s->rows, threads / p->lanes[b]);
+        threads[b] = p->wide[b] ? kWide : (p->lanes[b] < 256 ? 256 : p->lanes[b]);
+        const int64_t passes = p->wide[b] ? s->rows : ceil_div(s->rows, threads[b] / p->lanes[b]);
         // About 1024 threads of them a CU forwards (b8 L4096 of 2048 channels with an fp32 stream 165 us; 2048 172, 4096 168), 640 with
         // gradients, each with its own sums of the weights (b4 L4096 of 4096, 512 lanes a row: one a CU 219 us by kernel trace, two 238)
-        const int each = ((b ? 640 : 1024) + threads / 2) / threads;
+        const int each = ((b ? 640 : 1024) + threads[b] / 2) / threads[b];
         const int64_t best = p->wide[b] ? 512 : 256 * (each < 1 ? 1 : each);
         p->groups[b] = passes < best ? passes : best;
         if (b && !p->wide[b] && p->groups[b] * kChainRows < passes) p->groups[b] = ceil_div(passes, kChainRows);
@@ -749,7 +750,7 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
     const int64_t across = ceil_div(need, 64), want = ceil_div(4096, across), least = ceil_div(s->rows, kChainRows);
     p->rows = s->rows ? ceil_div(s->rows, want > least ? (want < s->rows ? want : s->rows) : least) : 1;
     p->parts = p->wide[1] ? ceil_div(s->rows, p->rows) : p->groups[1];
-    if (p->groups[1] > kMaxGrid || (p->wide[1] && p->parts > 65535)) return M3_ERR_UNSUPPORTED;
+    if (p->groups[1] > kMaxThreads / threads[1] || (p->wide[1] && p->parts > 65535)) return M3_ERR_UNSUPPORTED;
     p->stats = p->wide[1] ? ((size_t)s->rows * kStats * sizeof(float) + 255) & ~(size_t)255 : 0;
     p->total = p->stats + (size_t)p->parts * 3 * (size_t)s->channels * sizeof(float);
     return M3_OK;
