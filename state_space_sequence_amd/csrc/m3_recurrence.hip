@@ -121,7 +121,8 @@ struct Io {
 };
 
 // The sigmoid, and 1 - sigmoid without cancellation (where e^-x overflows: any finite factor of 0). bf16: the
-// hardware exponential of a rounded argument is off by |x| 2^-23, far below the outputs' rounding
+// hardware exponential of a rounded argument is off by |x| 2^-23, far below the rounding of outputs in bf16. The fp32 states take it
+// as it is, each term off by that much of itself; an exact argument would cost an exponential more a gate, and issue is a bound here
 template <bool BF16>
 __device__ __forceinline__ float neg_exp(float x) {
     return BF16 ? __builtin_amdgcn_exp2f(-1.4426950408889634f * x) : expf(-x);
@@ -135,10 +136,11 @@ __device__ __forceinline__ float sigmoid(float x, float &rest) {
     return s;
 }
 
-// a = 2^l and p = 1 - a for l <= 0, both to half a step: 2^f - 1 = f P(f) for the rest f of l from its nearest whole
-// number n, P the polynomial of degree 5 that is closest over |f| <= 1/2 (1.1e-8 relative; fitted here). p has no
-// cancellation: for n = 0 it is -f P(f), else at least 0.29. A state of slow decay keeps what hundreds of steps
-// bring, so a and m must not be off in one direction.
+// a = 2^l and p = 1 - a for l <= 0: 2^f - 1 = f P(f) for the rest f of l from its nearest whole
+// number n, P the polynomial of degree 5 that is closest over |f| <= 1/2 (fitted here; 2.1e-8 relative with fp32 coefficients). p has no
+// cancellation: for n = 0 it is -f P(f), else at least 0.29. With all roundings a is off by at most 1.6 * 2^-24 of itself and p by 2.1.
+// A state of slow decay keeps what hundreds of steps bring, so a and m must not be off in one direction: on average both
+// are by less than 0.12 * 2^-24.
 __device__ __forceinline__ void decay(float l, float &a, float &p) {
     const float n = __builtin_rintf(l), f = l - n;
     const float z = __builtin_amdgcn_ldexpf(1.f, (int)n);
@@ -152,8 +154,9 @@ __device__ __forceinline__ void decay(float l, float &a, float &p) {
     p = __builtin_fmaf(-z, e, 1.f - z);
 }
 
-// The same for kMild <= l <= 0, where one polynomial of degree 6 gives p (3.2e-9 relative; fitted here) without a division
-// of the range: 8 operations in place of 13. A channel's l is between 0 and its log_decay in powers of 2
+// The same for kMild <= l <= 0, where one polynomial of degree 6 gives p (fitted here; 9.8e-9 relative) without a division
+// of the range: 8 operations in place of 13. p is off by at most 2.1 * 2^-24, a = 1 - p by 1.5 where l > -1/2, else by 3.8. A channel's l is
+// between 0 and its log_decay in powers of 2
 constexpr float kMild = -1.5f;
 __device__ __forceinline__ void mild_decay(float l, float &a, float &p) {
     float q = __builtin_fmaf(l, -0x1.458340p-17f, -0x1.2c9900p-13f);
