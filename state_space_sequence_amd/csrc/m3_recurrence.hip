@@ -32,7 +32,6 @@ namespace m3i {
 namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -74,7 +73,7 @@ struct RecArgs {
 template <bool BF16, int V>
 struct Io {
     static constexpr int B = (BF16 ? 2 : 4) * V, W = (B + 3) / 4;  // bytes and words of a lane and token
-    static_assert(B == 2 || B == 4 || B == 8, "an access of two to eight bytes");
+    static_assert(B == 2 || B == 4, "an access of two or four bytes");
     struct raw { unsigned w[W]; };
     using rsrc_t = decltype(__builtin_amdgcn_make_buffer_rsrc(static_cast<void *>(nullptr), 0, 0, 0));
     // tokens t0 .. t0 + n - 1 of a row
@@ -85,15 +84,8 @@ struct Io {
     }
     static __device__ __forceinline__ raw load(rsrc_t r, unsigned at) {
         raw o;
-        if constexpr (B == 8) {
-            const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, kPast);
-            o.w[0] = w[0];
-            o.w[W - 1] = w[1];
-        } else if constexpr (B == 4) {
-            o.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kPast);
-        } else {
-            o.w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, kPast);
-        }
+        if constexpr (B == 4) o.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kPast);
+        else o.w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, kPast);
         return o;
     }
     // (the words stay packed until here: unpacked ahead, as the compiler would, two paths' values spill)
@@ -114,8 +106,7 @@ struct Io {
             else if constexpr (V == 1) w[e] = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
             else w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{v[2 * e], v[2 * e + 1]}), bf16x2));
         }
-        if constexpr (B == 8) __builtin_amdgcn_raw_buffer_store_b64((u32x2{w[0], w[W - 1]}), r, at, 0, kPast);
-        else if constexpr (B == 4) __builtin_amdgcn_raw_buffer_store_b32(w[0], r, at, 0, kPast);
+        if constexpr (B == 4) __builtin_amdgcn_raw_buffer_store_b32(w[0], r, at, 0, kPast);
         else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w[0], r, at, 0, 0);
     }
 };
