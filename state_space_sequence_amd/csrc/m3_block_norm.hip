@@ -770,8 +770,9 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
 template <bool BF, bool RF, int V, int LANES, int CH, bool WHOLE>
 hipError_t launch(const BlockArgs &a, const BlockPlan &p, bool bwd, hipStream_t s) {
     const dim3 t((Lanes<LANES, CH, V>::kThreads)), g((unsigned)p.groups[bwd]);
-    // (what the plan does not ask for: forwards two pieces of fewer than 1024 lanes, with gradients over 8 channels a lane)
-    constexpr bool forward = LANES == 1024 || CH == 1, backward = CH * V <= 8;
+    // (what the plan does not ask for: forwards two pieces of fewer than 1024 lanes, or over 16 channels a lane; with gradients over 8
+    // channels a lane, or 1024 lanes of 4)
+    constexpr bool forward = CH == 1 || (LANES == 1024 && CH * V <= 16), backward = CH * V <= 8 && !(LANES == 1024 && CH * V == 4);
     if constexpr (backward)
         if (bwd) hipLaunchKernelGGL((bwd_kernel<BF, RF, V, LANES, CH, WHOLE>), g, t, 0, s, a);
     if constexpr (forward)
