@@ -177,7 +177,7 @@ const char *m3_status_str(m3_status st) {
     return "unknown status";
 }
 
-int m3_version(void) { return 107; }
+int m3_version(void) { return 108; }
 
 // Output epilogue flags against the pointers: the gain needs the norm flag, and
 // the after-gate position needs the norm and the fused gate.

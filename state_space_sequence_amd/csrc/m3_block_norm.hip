@@ -7,7 +7,7 @@
 // Bound by HBM: every tensor is read or written once. The lanes of a row (16 to 1024 of them) hold it in registers, 4 to
 // 16 values each; its sums go across a wave by DPP and row swaps, across waves by LDS. A lane keeps its channels from row
 // to row, so weights and their gradients stay in registers too, and the next row is loaded while this one is summed. bf16, all parts:
-// b8 L4096 of 2048 channels with an fp32 stream 161 us (5.8 TB/s), gradients of b4 L4096 of 4096 193 us (5.5 TB/s).
+// b8 L4096 of 2048 channels with an fp32 stream 161 us (5.8 TB/s), gradients of b4 L4096 of 4096 191 us (5.6 TB/s).
 #include <math.h>
 
 #include "m3_block_norm.h"
@@ -82,8 +82,8 @@ __device__ __forceinline__ void unpack(const Packed<BF16, V> &o, float (&x)[V]) 
         else x[e] = __uint_as_float(e % 2 ? o.w[e / 2] & 0xffff0000u : o.w[e / 2] << 16);
     }
 }
-// Past the caches: forwards where the tensors of the call do not fit them (ASK, past), with gradients always (b4 L4096 of 4096
-// channels 222 us by kernel trace, with the question 227)
+// Past the caches: forwards where the tensors of the call do not fit them (ASK, past), with gradients always (the question
+// changes nothing for b4 L4096 of 4096 channels, 190 us and 189, in fp32 of half the tokens 187 and 188)
 template <bool BF16, int V, bool WHOLE, bool ASK>
 __device__ __forceinline__ void store(void *p, int64_t i, int live, const float (&x)[V], bool past) {
     constexpr int W = Packed<BF16, V>::W;
@@ -467,7 +467,7 @@ __global__ __launch_bounds__((Lanes<LANES, CH, V>::kThreads)) void bwd_kernel(co
 // --------------------------------------------------------------- wide rows ---
 // Rows that the registers do not hold: a workgroup goes over its row two or three times, V channels a thread, from the
 // caches after the first; gradients of weights by columns, from the rows' factors and means, in a launch of their own. Gradients of
-// 4096 bf16 rows of 16384 channels 520 us, bound by its passes (element by element 2140).
+// 4096 bf16 rows of 16384 channels 530 us, bound by its passes (element by element 2140).
 constexpr int kWide = 1024;
 constexpr int kStats = 4;  // a row's rx, rR, mean(q R rR) rR, mean(g x rx)
 
@@ -740,7 +740,7 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
     for (int b = 0; b < 2; ++b) {
         p->wide[b] = s->channels > (b ? 8192 : 16384);
         // Lanes of a row: one access each, of 4 channels two each from 512 lanes on with gradients, whose registers hold three sums a channel
-        // too. 1024 lanes leave those no room for weights and loads ahead (16384 rows of 4096 channels, bf16 with an fp32 stream: 305 us
+        // too. 1024 lanes leave those no room for weights and loads ahead (16384 rows of 4096 channels, bf16 with an fp32 stream: 273 us
         // with 512 lanes, 574 with 1024 and their weights in registers that spill). A whole number of waves from 256 on
         const int64_t lanes = b && p->V == 4 && need > 512 ? ceil_div(need, 2) : need;
         p->lanes[b] = 16;
@@ -750,8 +750,8 @@ m3_status block_plan(const m3_block_norm_shape *s, BlockPlan *p) {
         p->pieces[b] = need <= p->lanes[b] ? 1 : (need <= 2 * p->lanes[b] ? 2 : 4);
         threads[b] = p->wide[b] ? kWide : (p->lanes[b] < 256 ? 256 : p->lanes[b]);
         const int64_t passes = p->wide[b] ? s->rows : ceil_div(s->rows, threads[b] / p->lanes[b]);
-        // About 1024 threads of them a CU forwards (b8 L4096 of 2048 channels with an fp32 stream 165 us; 2048 172, 4096 168), 640 with
-        // gradients, each with its own sums of the weights (b4 L4096 of 4096, 512 lanes a row: one a CU 219 us by kernel trace, two 238)
+        // About 1024 threads of them a CU forwards (b8 L4096 of 2048 channels with an fp32 stream 163 us; 2048 175, 4096 171), 640 with
+        // gradients, each with its own sums of the weights (b4 L4096 of 4096, 512 lanes a row: one a CU 190 us, two 201)
         const int each = ((b ? 640 : 1024) + threads[b] / 2) / threads[b];
         const int64_t best = p->wide[b] ? 512 : 256 * (each < 1 ? 1 : each);
         p->groups[b] = passes < best ? passes : best;

@@ -13,14 +13,15 @@
 //
 // With few columns several workgroups share one, and the state that a tile starts from comes through memory (CHAIN). A
 // tile publishes its map as soon as it has it, and the state behind it later; one that needs its start looks at the
-// kWindow tiles before it for the nearest known state and the maps from there. The state behind a tile is
+// kWindow tiles before it for the nearest known state and the maps from there (the published scan in a single pass with decoupled
+// look-back, of Merrill and Garland, 2016, for these maps). The state behind a tile is
 // A h + B of its joint map wherever it is formed, so the bits do not depend on who was first. A word is written and read
 // by one atomic access and is there whole or not at all, without fences or flags. A wait ends: the tiles of a column are
 // taken in order from a counter, a workgroup does what it took in that order, and a tile needs nothing from later ones.
 //
 // Bound by HBM and, nearly as much, by vector issue: 34 instructions an element, 5 of them exponentials, reciprocals and roots, 53 ns
 // an element of a wave on a SIMD, so 110 us of the prompt's 211. bf16, with an input gate, times of a call: prompt b8 L4096 of
-// 4096 channels 211 us (5.1 TB/s), long b2 L32768 of 2560 in a chain 288 (4.7 TB/s), gradients b8 L2048 of 4096 202 (4.7 TB/s).
+// 4096 channels 211 us (5.1 TB/s), long b2 L32768 of 2560 in a chain 288 (4.7 TB/s), gradients b8 L2048 of 4096 201 (4.7 TB/s).
 #include <math.h>
 
 #include <type_traits>
